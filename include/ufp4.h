@@ -331,6 +331,60 @@ int ufp4_philox_fill(uint64_t seed, uint32_t stream_id, uint64_t first, int64_t 
  * misalignment or overlapping ranges.  Asynchronous on `stream`. */
 int ufp4_stream_copy(const void* src, void* dst, int64_t nbytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Language-model operators around the GEMMs.  The conventions at the top hold:
+ * device pointers owned by the caller, nothing allocated or kept, work
+ * enqueued on `stream`, arguments checked before any HIP call.  Outputs must
+ * not overlap inputs or each other.
+ * ------------------------------------------------------------------------- */
+
+/* Element types of inputs that may come in either (a GEMM's fp32 output, or
+ * bf16), and the activations: SiLU g / (1 + e^-g), and GELU in its tanh form
+ * g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2. */
+enum { UFP4_BF16 = 0, UFP4_FP32 = 1 };
+enum { UFP4_ACT_SILU = 0, UFP4_ACT_GELU = 1 };
+
+/* Gated activation of an expert (between its gate / up products and its down
+ * product), with its inputs kept in 8 bits for the backward pass:
+ *   h[r][c] = row_scale[r] * act(gate[r][c]) * up[r][c]          (bf16)
+ * computed in fp32 from the inputs as they are and rounded once.
+ *   gate, up  : [rows][ld] of dtype (UFP4_FP32 or UFP4_BF16), ld >= cols
+ *               (both with the same pitch, so two halves of one matrix serve).
+ *   row_scale : fp32 [rows], a factor per row (a token's expert weight), or
+ *               NULL for 1.
+ *   h         : bf16 [rows][ldh], ldh >= cols (ldh % 8 == 0 and 16-byte
+ *               alignment make it an input of the quantizers).
+ *   gate_codes, up_codes   : uint8 [rows][cols], or all four NULL: no
+ *   gate_scales, up_scales : uint8 [rows][ceil(cols / 32)]  checkpoint (serving).
+ * The checkpoint of a tensor is its MXFP8 quantization without rotation, the
+ * layout and values of ufp4_rht_quant with UFP4_E4M3, 1 x 32 power-of-two
+ * blocks and rht_n = 1 ([2DFP4] mixed-precision section), but any cols >= 0 is
+ * allowed: the last block of a row may be short.  A NaN element is a NaN code;
+ * in a block that holds an infinity the scale is 2^120 and the infinity the
+ * largest code, which reads back as infinity.
+ * Any strides and alignments that fit the element type are accepted; 16-byte
+ * aligned rows with cols % 8 == 0 run with vector accesses.
+ * Errors: UFP4_ERR_INVALID_ARG (sizes, enums, null pointers, a pitch below
+ * cols, some checkpoint pointers null and some not, a pointer not aligned to its
+ * elements). */
+int ufp4_glu_fwd(const void* gate, const void* up, int32_t dtype, int64_t rows, int64_t cols,
+                 int64_t ld, int32_t act, const float* row_scale, void* h, int64_t ldh,
+                 uint8_t* gate_codes, uint8_t* gate_scales, uint8_t* up_codes,
+                 uint8_t* up_scales, void* stream);
+
+/* Backward pass of ufp4_glu_fwd from its checkpoint: with g, u the values the
+ * codes stand for and dh the gradient of h ([rows][lddh] of dtype),
+ *   dgate = row_scale dh u act'(g)      dup = row_scale dh act(g)    (bf16 [rows][ldd])
+ *   drow_scale[r] = sum over c of dh act(g) u        (fp32, NULL to skip)
+ *   h = row_scale act(g) u        (bf16 [rows][ldh], NULL to skip): the down
+ *       product's operand again, for a WGRAD that did not keep it.
+ * drow_scale needs row_scale.  The row sums are added in a fixed order, so
+ * equal inputs give equal bits.  Errors as ufp4_glu_fwd. */
+int ufp4_glu_bwd(const uint8_t* gate_codes, const uint8_t* gate_scales, const uint8_t* up_codes,
+                 const uint8_t* up_scales, int64_t rows, int64_t cols, int32_t act,
+                 const float* row_scale, const void* dh, int32_t dtype, int64_t lddh, void* dgate,
+                 void* dup, int64_t ldd, float* drow_scale, void* h, int64_t ldh, void* stream);
+
 /* Name of a status code (static string). */
 const char* ufp4_status_string(int status);
 

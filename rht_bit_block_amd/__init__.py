@@ -26,6 +26,8 @@ UFP4_SCALE_F32, UFP4_SCALE_POW2 = 0, 1
 UFP4_OK, UFP4_ERR_INVALID_ARG, UFP4_ERR_SHAPE = 0, -1, -2
 UFP4_ERR_MISMATCH, UFP4_ERR_UNSUPPORTED, UFP4_ERR_HIP = -3, -4, -5
 UFP4_GEMM_FPROP, UFP4_GEMM_DGRAD, UFP4_GEMM_WGRAD = 0, 1, 2
+UFP4_BF16, UFP4_FP32 = 0, 1
+UFP4_ACT_SILU, UFP4_ACT_GELU = 0, 1
 
 EXPORTED = [
     "ufp4_rht_quant", "ufp4_rht_quant_segmented", "ufp4_rht_quant_dual", "ufp4_quant_diag",
@@ -36,6 +38,7 @@ EXPORTED = [
     "ufp4_gemm_workspace_bytes", "ufp4_gemm_ws",
     "ufp4_transpose_qtensor", "ufp4_codes_bytes", "ufp4_scales_bytes",
     "ufp4_philox_fill", "ufp4_stream_copy", "ufp4_status_string",
+    "ufp4_glu_fwd", "ufp4_glu_bwd",
 ]
 
 
@@ -125,6 +128,9 @@ def _lib():
             "ufp4_transpose_qtensor": [qtp, vp, vp, vp],
             "ufp4_philox_fill": [u64, u32, u64, i64, vp, vp],
             "ufp4_stream_copy": [vp, vp, i64, vp],
+            "ufp4_glu_fwd": [vp, vp, i32, i64, i64, i64, i32, vp, vp, i64, vp, vp, vp, vp, vp],
+            "ufp4_glu_bwd": [vp, vp, vp, vp, i64, i64, i32, vp, vp, i32, i64, vp, vp, i64, vp, vp,
+                             i64, vp],
         }
         for name, args in sig.items():
             f = getattr(lib, name)
@@ -505,6 +511,141 @@ def ufp4_stream_copy(src, dst):
     st = _lib().ufp4_stream_copy(_ptr(src), _ptr(dst), n, _stream(dst))
     _check("ufp4_stream_copy", st)
     return dst
+
+
+# ---------------------------------------------------------------------------
+# Language-model operators around the GEMMs
+# ---------------------------------------------------------------------------
+def _dtype_code(name, t):
+    if t.dtype == torch.bfloat16:
+        return UFP4_BF16
+    if t.dtype == torch.float32:
+        return UFP4_FP32
+    raise ValueError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _check_input(name, t, shape=None, dtype=None, device=None):
+    """A 2-D input with unit column stride; returns its row pitch."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
+    rows, cols = t.shape
+    if cols > 1 and rows and t.stride(1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    if rows > 1 and t.stride(0) < cols:
+        raise ValueError(f"{name} row pitch {t.stride(0)} is below its {cols} columns")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return t.stride(0) if rows > 1 else cols
+
+
+def _check_vector(name, t, n, dtype, device):
+    """A contiguous 1-D input of n elements."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 1 or t.shape[0] != n or t.dtype != dtype:
+        raise ValueError(f"{name} must be a 1-D {dtype} tensor of {n} elements")
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+
+
+@dataclass
+class GluCheckpoint:
+    """What ufp4_glu_fwd keeps of gate and up for the backward pass: E4M3
+    codes uint8 [rows, cols] and E8M0 scales uint8 [rows, ceil(cols / 32)]."""
+    gate_codes: torch.Tensor
+    gate_scales: torch.Tensor
+    up_codes: torch.Tensor
+    up_scales: torch.Tensor
+    act: int
+
+    def check(self):
+        """(rows, cols), after checking the four buffers against each other."""
+        if not isinstance(self.gate_codes, torch.Tensor) or self.gate_codes.dim() != 2:
+            raise ValueError("gate_codes must be a 2-D tensor")
+        rows, cols = self.gate_codes.shape
+        dev = self.gate_codes.device
+        for name, t, n in (("gate_codes", self.gate_codes, cols), ("up_codes", self.up_codes, cols),
+                           ("gate_scales", self.gate_scales, (cols + 31) // 32),
+                           ("up_scales", self.up_scales, (cols + 31) // 32)):
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8 or t.shape != (rows, n):
+                raise ValueError(f"{name} must be a uint8 tensor of shape ({rows}, {n})")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            if t.device != dev:
+                raise ValueError(f"{name} must be on {dev}")
+        return rows, cols
+
+    def qtensors(self):
+        """The checkpoints of gate and up as QTensors (cols % 32 == 0), e.g.
+        for ufp4_dequant."""
+        rows, cols = self.check()
+        if cols % 32:
+            raise ValueError("a QTensor holds whole 32-element blocks: cols % 32 must be 0")
+        cfg = make_cfg(UFP4_E4M3, UFP4_RTNE, UFP4_SCALE_POW2, 1, 32, 1)
+        return (QTensor(self.gate_codes, self.gate_scales, rows, cols, cfg),
+                QTensor(self.up_codes, self.up_scales, rows, cols, cfg))
+
+
+def ufp4_glu_fwd(gate: torch.Tensor, up: torch.Tensor, act=UFP4_ACT_SILU, row_scale=None,
+                 checkpoint=True, out=None):
+    """h = row_scale * act(gate) * up in bf16 (gate, up [rows, cols], both
+    bfloat16 or both float32, same row pitch; row_scale float32 [rows] or None).
+    Returns (h, GluCheckpoint), or (h, None) with checkpoint=False (serving)."""
+    ld = _check_input("gate", gate)
+    dt = _dtype_code("gate", gate)
+    rows, cols = gate.shape
+    dev = gate.device
+    if _check_input("up", up, gate.shape, gate.dtype, dev) != ld:
+        raise ValueError("gate and up must have the same row pitch")
+    if row_scale is not None:
+        _check_vector("row_scale", row_scale, rows, torch.float32, dev)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    ldh = _check_input("out", out, gate.shape, torch.bfloat16, dev)
+    kept = None
+    if checkpoint:
+        nb = (cols + 31) // 32
+        kept = GluCheckpoint(torch.empty((rows, cols), dtype=torch.uint8, device=dev),
+                             torch.empty((rows, nb), dtype=torch.uint8, device=dev),
+                             torch.empty((rows, cols), dtype=torch.uint8, device=dev),
+                             torch.empty((rows, nb), dtype=torch.uint8, device=dev), int(act))
+    _on_gpu(gate, "gate")
+    k = (kept.gate_codes, kept.gate_scales, kept.up_codes, kept.up_scales) if kept else (None,) * 4
+    st = _lib().ufp4_glu_fwd(_ptr(gate), _ptr(up), dt, rows, cols, ld, int(act), _ptr(row_scale),
+                             _ptr(out), ldh, _ptr(k[0]), _ptr(k[1]), _ptr(k[2]), _ptr(k[3]),
+                             _stream(gate))
+    _check("ufp4_glu_fwd", st)
+    return out, kept
+
+
+def ufp4_glu_bwd(ckpt: GluCheckpoint, dh: torch.Tensor, row_scale=None, recompute=False,
+                 drow=True):
+    """Gradients of ufp4_glu_fwd from its checkpoint and dh [rows, cols]
+    (bfloat16 or float32).  Returns (dgate, dup, drow_scale, h): bf16 dgate and
+    dup; float32 drow_scale [rows] when row_scale is given (drow=False skips
+    it), else None; h recomputed from the checkpoint when asked for, else None."""
+    rows, cols = ckpt.check()
+    dev = ckpt.gate_codes.device
+    lddh = _check_input("dh", dh, (rows, cols), None, dev)
+    dt = _dtype_code("dh", dh)
+    if row_scale is not None:
+        _check_vector("row_scale", row_scale, rows, torch.float32, dev)
+    _on_gpu(dh, "dh")
+    dgate = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    dup = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    h = torch.empty((rows, cols), dtype=torch.bfloat16, device=dev) if recompute else None
+    dr = (torch.empty(rows, dtype=torch.float32, device=dev)
+          if row_scale is not None and drow else None)
+    st = _lib().ufp4_glu_bwd(_ptr(ckpt.gate_codes), _ptr(ckpt.gate_scales), _ptr(ckpt.up_codes),
+                             _ptr(ckpt.up_scales), rows, cols, int(ckpt.act), _ptr(row_scale),
+                             _ptr(dh), dt, lddh, _ptr(dgate), _ptr(dup), cols, _ptr(dr), _ptr(h),
+                             cols, _stream(dh))
+    _check("ufp4_glu_bwd", st)
+    return dgate, dup, dr, h
 
 
 def ufp4_codes_bytes(P, K):
