@@ -385,6 +385,47 @@ int ufp4_glu_bwd(const uint8_t* gate_codes, const uint8_t* gate_scales, const ui
                  const float* row_scale, const void* dh, int32_t dtype, int64_t lddh, void* dgate,
                  void* dup, int64_t ldd, float* drow_scale, void* h, int64_t ldh, void* stream);
 
+/* Softmax cross entropy of a linear layer over a large vocabulary, without
+ * storing the logits z = h w^T:
+ *   lse[t] = log sum over v of e^z[t][v]
+ *   loss[t] = lse[t] - z[t][targets[t]], or 0 where targets[t] is outside
+ *             0 .. V-1 (an ignored position, e.g. -100).
+ *   h : bf16 [T][ldh], w : bf16 [V][ldw] (16-byte aligned, ldh % 8 == 0,
+ *       ldw % 8 == 0, D % 8 == 0), targets : int64 [T], loss, lse : fp32 [T].
+ * Products are exact in fp32 and summed in fp32; the statistics are fp32.
+ * workspace: device memory, 256-byte aligned, at least
+ * ufp4_linear_xent_workspace_bytes(T, V, D, 0) bytes; its contents on entry do
+ * not matter.  Calls that share a workspace must be ordered on one stream.
+ * T >= 0 (0: nothing to do), V >= 1, D >= 8.
+ * Errors: UFP4_ERR_INVALID_ARG (sizes, pitches, alignment, null pointers, a
+ * workspace that is too small), UFP4_ERR_SHAPE (D % 8), UFP4_ERR_UNSUPPORTED
+ * (T > 2^21, V > 2^30, D or a pitch > 2^20). */
+int ufp4_linear_xent_fwd(const void* h, int64_t ldh, const void* w, int64_t ldw,
+                         const int64_t* targets, int64_t T, int64_t V, int64_t D, float* loss,
+                         float* lse, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of ufp4_linear_xent_fwd given dloss [T] and, if not NULL, dlse [T]
+ * (fp32; a term on the returned lse, as in a squared-lse penalty):
+ *   G[t][v] = (b + dlse[t]) e^(z[t][v] - lse[t]) - b [v = targets[t]],
+ *             b = dloss[t], or 0 at an ignored position
+ *   dh = G w  (bf16 [T][lddh])      dw = G^T h  (bf16 [V][lddw])
+ * The logits are computed again, one piece of the vocabulary at a time, and G
+ * is rounded to bf16 for the two products; their sums are fp32, rounded once.
+ * lse is the forward call's.  A token whose b and dlse are both 0 has dh = 0
+ * and adds nothing to dw, whatever its h holds.  dh and dw: 16-byte aligned,
+ * pitches % 8 == 0; both are overwritten (T == 0: dw = 0).  The workspace
+ * (ufp4_linear_xent_workspace_bytes(T, V, D, 1)) holds one piece of G, at most
+ * about 2^26 elements (more only where T > 2^18), and of w^T.  Equal
+ * inputs give equal bits.  Errors as the forward call. */
+int ufp4_linear_xent_bwd(const void* h, int64_t ldh, const void* w, int64_t ldw,
+                         const int64_t* targets, int64_t T, int64_t V, int64_t D, const float* lse,
+                         const float* dloss, const float* dlse, void* dh, int64_t lddh, void* dw,
+                         int64_t lddw, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of the forward (backward = 0) or backward (1) call; 0 for
+ * sizes that the calls refuse or that need none (T == 0). */
+size_t ufp4_linear_xent_workspace_bytes(int64_t T, int64_t V, int64_t D, int32_t backward);
+
 /* Name of a status code (static string). */
 const char* ufp4_status_string(int status);
 

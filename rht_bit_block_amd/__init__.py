@@ -39,6 +39,7 @@ EXPORTED = [
     "ufp4_transpose_qtensor", "ufp4_codes_bytes", "ufp4_scales_bytes",
     "ufp4_philox_fill", "ufp4_stream_copy", "ufp4_status_string",
     "ufp4_glu_fwd", "ufp4_glu_bwd",
+    "ufp4_linear_xent_fwd", "ufp4_linear_xent_bwd", "ufp4_linear_xent_workspace_bytes",
 ]
 
 
@@ -131,6 +132,10 @@ def _lib():
             "ufp4_glu_fwd": [vp, vp, i32, i64, i64, i64, i32, vp, vp, i64, vp, vp, vp, vp, vp],
             "ufp4_glu_bwd": [vp, vp, vp, vp, i64, i64, i32, vp, vp, i32, i64, vp, vp, i64, vp, vp,
                              i64, vp],
+            "ufp4_linear_xent_fwd": [vp, i64, vp, i64, vp, i64, i64, i64, vp, vp, vp,
+                                     ctypes.c_size_t, vp],
+            "ufp4_linear_xent_bwd": [vp, i64, vp, i64, vp, i64, i64, i64, vp, vp, vp, vp, i64, vp,
+                                     i64, vp, ctypes.c_size_t, vp],
         }
         for name, args in sig.items():
             f = getattr(lib, name)
@@ -138,6 +143,8 @@ def _lib():
             f.restype = ctypes.c_int
         lib.ufp4_gemm_workspace_bytes.argtypes = [i32, qtp, qtp, i32]
         lib.ufp4_gemm_workspace_bytes.restype = ctypes.c_size_t
+        lib.ufp4_linear_xent_workspace_bytes.argtypes = [i64, i64, i64, i32]
+        lib.ufp4_linear_xent_workspace_bytes.restype = ctypes.c_size_t
         lib.ufp4_codes_bytes.argtypes = [i64, i64]
         lib.ufp4_codes_bytes.restype = ctypes.c_size_t
         lib.ufp4_scales_bytes.argtypes = [i64, i64, cfgp]
@@ -646,6 +653,72 @@ def ufp4_glu_bwd(ckpt: GluCheckpoint, dh: torch.Tensor, row_scale=None, recomput
                              cols, _stream(dh))
     _check("ufp4_glu_bwd", st)
     return dgate, dup, dr, h
+
+
+def ufp4_linear_xent_workspace_bytes(T, V, D, backward=False):
+    return int(_lib().ufp4_linear_xent_workspace_bytes(int(T), int(V), int(D), int(bool(backward))))
+
+
+def _xent_inputs(h, w, targets):
+    ldh = _check_input("h", h, None, torch.bfloat16)
+    T, D = h.shape
+    ldw = _check_input("w", w, None, torch.bfloat16, h.device)
+    if w.shape[1] != D:
+        raise ValueError(f"w has {w.shape[1]} columns, h has {D}")
+    _check_vector("targets", targets, T, torch.int64, h.device)
+    return T, w.shape[0], D, (ldh if T > 1 else (D + 7) // 8 * 8), (
+        ldw if w.shape[0] > 1 else (D + 7) // 8 * 8)
+
+
+def _xent_workspace(T, V, D, backward, workspace, device):
+    need = int(_lib().ufp4_linear_xent_workspace_bytes(T, V, D, backward))
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    _check_buffer("workspace", workspace, torch.uint8, need, device)
+    return workspace
+
+
+def ufp4_linear_xent_fwd(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor, workspace=None):
+    """Softmax cross entropy of z = h w^T (h [T, D], w [V, D] bfloat16, targets
+    int64 [T]; a target outside 0 .. V-1 is ignored) without storing z.  Returns
+    float32 (loss [T], lse [T]).  workspace: uint8 device buffer of
+    ufp4_linear_xent_workspace_bytes(T, V, D) (allocated when not given)."""
+    T, V, D, ldh, ldw = _xent_inputs(h, w, targets)
+    _on_gpu(h, "h")
+    dev = h.device
+    loss = torch.empty(T, dtype=torch.float32, device=dev)
+    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    ws = _xent_workspace(T, V, D, 0, workspace, dev)
+    st = _lib().ufp4_linear_xent_fwd(_ptr(h), ldh, _ptr(w), ldw, _ptr(targets), T, V, D, _ptr(loss),
+                                     _ptr(lse), _ptr(ws), ws.numel(), _stream(h))
+    _check("ufp4_linear_xent_fwd", st)
+    return loss, lse
+
+
+def ufp4_linear_xent_bwd(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor,
+                         lse: torch.Tensor, dloss: torch.Tensor, dlse=None, out=None,
+                         workspace=None):
+    """Gradients (dh [T, D], dw [V, D], bfloat16) of ufp4_linear_xent_fwd for
+    dloss [T] and optionally dlse [T] (float32); lse is the forward call's.
+    out: optional (dh, dw) to write into; workspace as there, backward=True."""
+    T, V, D, ldh, ldw = _xent_inputs(h, w, targets)
+    dev = h.device
+    _check_vector("lse", lse, T, torch.float32, dev)
+    _check_vector("dloss", dloss, T, torch.float32, dev)
+    if dlse is not None:
+        _check_vector("dlse", dlse, T, torch.float32, dev)
+    dh, dw = out if out is not None else (
+        torch.empty((T, D), dtype=torch.bfloat16, device=dev),
+        torch.empty((V, D), dtype=torch.bfloat16, device=dev))
+    lddh = _check_input("dh", dh, h.shape, torch.bfloat16, dev)
+    lddw = _check_input("dw", dw, w.shape, torch.bfloat16, dev)
+    _on_gpu(w, "w")
+    ws = _xent_workspace(T, V, D, 1, workspace, dev)
+    st = _lib().ufp4_linear_xent_bwd(_ptr(h), ldh, _ptr(w), ldw, _ptr(targets), T, V, D, _ptr(lse),
+                                     _ptr(dloss), _ptr(dlse), _ptr(dh), lddh, _ptr(dw), lddw,
+                                     _ptr(ws), ws.numel(), _stream(w))
+    _check("ufp4_linear_xent_bwd", st)
+    return dh, dw
 
 
 def ufp4_codes_bytes(P, K):

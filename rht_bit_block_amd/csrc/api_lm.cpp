@@ -25,9 +25,96 @@ uintptr_t elem_bytes(int32_t d) { return d == UFP4_BF16 ? 2 : 4; }
 
 constexpr int64_t kMaxGluCols = (int64_t)1 << 30;   // a row's 8-element chunks in one launch
 
+// Sizes of a linear cross entropy: 32-bit offsets inside a 256-row tile and
+// grids of a launch bound them.
+int xent_sizes(int64_t T, int64_t V, int64_t D) {
+  if (T < 0 || V < 1 || D < 1) return UFP4_ERR_INVALID_ARG;
+  if (D % 8) return UFP4_ERR_SHAPE;
+  if (T > ((int64_t)1 << 21) || V > ((int64_t)1 << 30) || D > ((int64_t)1 << 20))
+    return UFP4_ERR_UNSUPPORTED;
+  return UFP4_OK;
+}
+
+int xent_matrix(const void* p, int64_t ld, int64_t cols) {
+  if (!p || ld < cols || ld % 8 || !aligned(p, 16)) return UFP4_ERR_INVALID_ARG;
+  return ld > ((int64_t)1 << 20) ? UFP4_ERR_UNSUPPORTED : UFP4_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t ufp4_linear_xent_workspace_bytes(int64_t T, int64_t V, int64_t D, int32_t backward) {
+  if (xent_sizes(T, V, D) || T == 0) return 0;
+  const XentPlan p = xent_plan(T, V, D);
+  return (size_t)(backward ? p.bwd_bytes : p.fwd_bytes);
+}
+
+int ufp4_linear_xent_fwd(const void* h, int64_t ldh, const void* w, int64_t ldw,
+                         const int64_t* targets, int64_t T, int64_t V, int64_t D, float* loss,
+                         float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = xent_sizes(T, V, D);
+  if (st) return st;
+  if (T == 0) return UFP4_OK;
+  if ((st = xent_matrix(h, ldh, D)) || (st = xent_matrix(w, ldw, D))) return st;
+  if (!targets || !loss || !lse || !workspace) return UFP4_ERR_INVALID_ARG;
+  if (!aligned(targets, 8) || !aligned(loss, 4) || !aligned(lse, 4) || !aligned(workspace, 256))
+    return UFP4_ERR_INVALID_ARG;
+  if (workspace_bytes < ufp4_linear_xent_workspace_bytes(T, V, D, 0)) return UFP4_ERR_INVALID_ARG;
+  XentLaunch x;
+  std::memset(&x, 0, sizeof(x));
+  x.h = static_cast<const uint16_t*>(h);
+  x.w = static_cast<const uint16_t*>(w);
+  x.targets = targets;
+  x.T = T;
+  x.V = V;
+  x.D = D;
+  x.ldh = ldh;
+  x.ldw = ldw;
+  x.loss = loss;
+  x.lse_out = lse;
+  x.ws = static_cast<uint8_t*>(workspace);
+  return hip_status(launch_xent_fwd(x, (hipStream_t)stream));
+}
+
+int ufp4_linear_xent_bwd(const void* h, int64_t ldh, const void* w, int64_t ldw,
+                         const int64_t* targets, int64_t T, int64_t V, int64_t D, const float* lse,
+                         const float* dloss, const float* dlse, void* dh, int64_t lddh, void* dw,
+                         int64_t lddw, void* workspace, size_t workspace_bytes, void* stream) {
+  int st = xent_sizes(T, V, D);
+  if (st) return st;
+  if ((st = xent_matrix(dw, lddw, D))) return st;
+  if (T > 0) {
+    if ((st = xent_matrix(h, ldh, D)) || (st = xent_matrix(w, ldw, D)) ||
+        (st = xent_matrix(dh, lddh, D)))
+      return st;
+    if (!targets || !lse || !dloss || !workspace) return UFP4_ERR_INVALID_ARG;
+    if (!aligned(targets, 8) || !aligned(lse, 4) || !aligned(dloss, 4) || !aligned(dlse, 4) ||
+        !aligned(workspace, 256))
+      return UFP4_ERR_INVALID_ARG;
+    if (workspace_bytes < ufp4_linear_xent_workspace_bytes(T, V, D, 1))
+      return UFP4_ERR_INVALID_ARG;
+  }
+  XentLaunch x;
+  std::memset(&x, 0, sizeof(x));
+  x.h = static_cast<const uint16_t*>(h);
+  x.w = static_cast<const uint16_t*>(w);
+  x.targets = targets;
+  x.T = T;
+  x.V = V;
+  x.D = D;
+  x.ldh = ldh;
+  x.ldw = ldw;
+  x.lse = lse;
+  x.dloss = dloss;
+  x.dlse = dlse;
+  x.dh = static_cast<uint16_t*>(dh);
+  x.dw = static_cast<uint16_t*>(dw);
+  x.lddh = lddh;
+  x.lddw = lddw;
+  x.ws = static_cast<uint8_t*>(workspace);
+  return hip_status(launch_xent_bwd(x, (hipStream_t)stream));
+}
 
 int ufp4_glu_fwd(const void* gate, const void* up, int32_t dtype, int64_t rows, int64_t cols,
                  int64_t ld, int32_t act, const float* row_scale, void* h, int64_t ldh,

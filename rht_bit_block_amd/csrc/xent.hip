@@ -1,0 +1,567 @@
+// Softmax cross entropy of a linear layer over a large vocabulary, and its
+// gradients, in pieces of the vocabulary: the logits are never stored.
+//
+//   z = h W^T                        h [T][D], W [V][D] bf16; fp32 sums
+//   lse_t = log sum_v e^z_tv         loss_t = lse_t - z_t,target
+//   G_tv = a_t e^(z_tv - lse_t) - b_t [v = target_t]
+//   dh = G W        dW = G^T h
+// with b = dloss (0 where the target is no class) and a = b + dlse.
+//
+// Forward: one product whose 256 x 256 tiles end in a running maximum and sum
+// of exponentials per token instead of a store; a small kernel joins the tiles.
+// Backward, for one piece of the vocabulary after another: the product again,
+// whose tiles end in G (bf16: the operand type of the two products that follow;
+// half a step of rounding per element, averaged over the long sums), then dh
+// += G W in fp32 and dW = G^T h.  Every product runs as C[m][n] = sum_k
+// A[m][k] B[n][k] with both operands K-contiguous, so h, the piece of W and G
+// are also laid out transposed (plain tiled copies, 1/256 of the product's
+// operations' time).
+//
+// The products are bound by the matrix cores: v_mfma_f32_32x32x16_bf16, 256 x
+// 256 tiles, four waves of 128 x 128 (accumulators in AGPRs), operands copied
+// HBM -> LDS by buffer_load ... lds in 128-byte rows with XOR-swizzled 16-byte
+// chunks.  The output's contiguous dimension is m, because a lane of the
+// instruction holds four consecutive m of one n: 8- and 16-byte stores, and
+// the softmax statistics of a token (an n) are almost all inside one lane.
+#include "gemm_epilogue.h"
+#include "lds_copy.h"
+#include "lm_internal.h"
+
+namespace ufp4 {
+
+namespace {
+
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const f32x2 v = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+// Byte offset of 16-byte chunk c of tile row `row` in LDS (128-byte rows,
+// chunks XOR-swizzled so that 16 consecutive rows reading one chunk fill all
+// 64 banks).
+__device__ __forceinline__ uint32_t off128(int row, int c) {
+  return (uint32_t)(row * 128 + 16 * (c ^ ((row >> 1) & 7)));
+}
+
+// What a tile ends in.
+enum { kStats = 0, kGrad = 1, kSlab = 2, kOut = 3 };
+
+// Operands [rows][ld] of a product with m over A's rows and n over B's.
+struct Prod {
+  const uint16_t* a;
+  const uint16_t* b;
+  int64_t M, N, K;          // K: elements contracted (a multiple of 8)
+  int64_t lda, ldb;         // row pitches in elements
+  int32_t tiles_m, tiles_n, tiles, splits;
+  int64_t k_per_split;      // a multiple of 64
+  // kStats: partials [2 tiles_m][N] (maximum, sum), logits of the targets
+  float2* part;
+  float* zt;
+  // kStats, kGrad
+  const int64_t* targets;   // class of n; m + m0 is the class of m
+  int64_t m0, classes;
+  const float* lse;
+  const float* dloss;
+  const float* dlse;
+  // kGrad, kOut: bf16 [N][ldo], m contiguous, m < m_store written
+  uint16_t* out;
+  int64_t ldo, m_store, n_store;
+  // kSlab: fp32 [splits][N][M], added to unless `first`
+  float* slab;
+  int32_t first;
+};
+
+// Tile shape: WM x WN waves of (32 NI) x (32 NJ).
+template <int WM_, int WN_, int NI_, int NJ_, int ST_>
+struct Shape {
+  static constexpr int WM = WM_, WN = WN_, NI = NI_, NJ = NJ_, ST = ST_;
+  static constexpr int TM = WM * NI * 32, TN = WN * NJ * 32;
+  static constexpr int STAGE = (TM + TN) * 128;
+  static constexpr int LA = TM / 32, LB = TN / 32;   // 8-row loads per wave and step
+  static_assert(WM * WN == 4, "four waves");
+};
+using Big = Shape<2, 2, 4, 4, 2>;
+
+// The swizzle's part that differs between a wave's 8-row loads.
+__device__ __forceinline__ uint32_t chunk_flip(int row8) { return (uint32_t)(row8 & 1) << 6; }
+
+template <class S>
+struct Ctx {
+  sgpr4 ra, rb;
+  uint32_t lds0;
+  uint32_t va[S::LA], vb[S::LB];
+  uint32_t kbytes, cbyte;    // bytes of K in this split, this lane's chunk within a step
+  int wave, nsteps;
+};
+
+// Copy step `step` (64 k) into stage `st`.  Past the last step nothing is
+// copied that is read; chunks past K read as zeros.
+template <class S>
+__device__ __forceinline__ void issue(const Ctx<S>& c, int step, int st) {
+  const int s = step < c.nsteps ? step : c.nsteps - 1;
+  const uint32_t base = c.lds0 + (uint32_t)st * S::STAGE;
+  const uint32_t koff = (uint32_t)s * 128u;
+  const bool tail = koff + 128u > c.kbytes;
+  // outside every buffer: zeros
+  auto in_k = [&](uint32_t v, int row8) {
+    return tail && koff + (c.cbyte ^ chunk_flip(row8)) >= c.kbytes ? 0x7FFFFF00u : v;
+  };
+#pragma unroll
+  for (int q = 0; q < S::LA; ++q) {
+    const int row8 = c.wave * S::LA + q;
+    lds_load16(base + (uint32_t)row8 * 1024u, c.ra, in_k(c.va[q], row8), koff);
+  }
+#pragma unroll
+  for (int q = 0; q < S::LB; ++q) {
+    const int row8 = c.wave * S::LB + q;
+    lds_load16(base + (uint32_t)(S::TM / 8 + row8) * 1024u, c.rb, in_k(c.vb[q], row8), koff);
+  }
+}
+
+template <class S>
+__device__ __forceinline__ void frags(const uint8_t* stage, int s, int lane, int wm, int wn,
+                                      bf16x8 (&a)[S::NI], bf16x8 (&b)[S::NJ]) {
+  const int h = lane >> 5;
+#pragma unroll
+  for (int i = 0; i < S::NI; ++i)
+    a[i] = *reinterpret_cast<const bf16x8*>(
+        stage + off128(wm * S::NI * 32 + i * 32 + (lane & 31), 2 * s + h));
+#pragma unroll
+  for (int j = 0; j < S::NJ; ++j)
+    b[j] = *reinterpret_cast<const bf16x8*>(
+        stage + S::TM * 128 + off128(wn * S::NJ * 32 + j * 32 + (lane & 31), 2 * s + h));
+}
+
+template <class S>
+__device__ __forceinline__ void mfmas(floatx16 (&acc)[S::NI][S::NJ], const bf16x8 (&a)[S::NI],
+                                      const bf16x8 (&b)[S::NJ]) {
+#pragma unroll
+  for (int i = 0; i < S::NI; ++i)
+#pragma unroll
+    for (int j = 0; j < S::NJ; ++j)
+      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+}
+
+template <class S, int EPI>
+__global__ __launch_bounds__(kThreads) void k_prod(Prod p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int wm = wave / S::WN, wn = wave % S::WN, h = lane >> 5;
+  const int split = blockIdx.x / p.tiles, b = blockIdx.x % p.tiles;
+  int tm, tn;
+  tile_order(b, p.tiles, p.tiles_m, p.tiles_n, tm, tn);
+  const int64_t row0 = (int64_t)tm * S::TM, col0 = (int64_t)tn * S::TN;
+  const int64_t k0 = (int64_t)split * p.k_per_split;
+  const int64_t kn = p.K - k0 < p.k_per_split ? p.K - k0 : p.k_per_split;
+  const int64_t rows = p.M - row0 < S::TM ? p.M - row0 : S::TM;
+  const int64_t cols = p.N - col0 < S::TN ? p.N - col0 : S::TN;
+
+  Ctx<S> c;
+  c.wave = wave;
+  c.kbytes = (uint32_t)(2 * kn);
+  c.nsteps = (int)((kn + 63) / 64);
+  c.ra = rsrc4(p.a + row0 * p.lda + k0, (uint32_t)(2 * ((rows - 1) * p.lda + kn)));
+  c.rb = rsrc4(p.b + col0 * p.ldb + k0, (uint32_t)(2 * ((cols - 1) * p.ldb + kn)));
+  c.lds0 = (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)lds;
+  // lane i of a wave load covers row i / 8 of its eight and the chunk whose
+  // swizzled slot is i % 8
+  c.cbyte = 16u * (uint32_t)((lane & 7) ^ (lane >> 4));
+#pragma unroll
+  for (int q = 0; q < S::LA; ++q) {
+    const int row8 = wave * S::LA + q;
+    c.va[q] = (uint32_t)(2 * (row8 * 8 + (lane >> 3)) * p.lda) + (c.cbyte ^ chunk_flip(row8));
+  }
+#pragma unroll
+  for (int q = 0; q < S::LB; ++q) {
+    const int row8 = wave * S::LB + q;
+    c.vb[q] = (uint32_t)(2 * (row8 * 8 + (lane >> 3)) * p.ldb) + (c.cbyte ^ chunk_flip(row8));
+  }
+
+  floatx16 acc[S::NI][S::NJ];
+#pragma unroll
+  for (int i = 0; i < S::NI; ++i)
+#pragma unroll
+    for (int j = 0; j < S::NJ; ++j) acc[i][j] = floatx16{};
+
+  issue<S>(c, 0, 0);
+  wait_vmcnt<0>();
+  __syncthreads();
+  bf16x8 a0[S::NI], b0[S::NJ], a1[S::NI], b1[S::NJ];
+  frags<S>(lds, 0, lane, wm, wn, a0, b0);
+  for (int step = 0; step < c.nsteps; ++step) {
+    const uint8_t* cur = lds + (step & 1) * S::STAGE;
+    issue<S>(c, step + 1, (step + 1) & 1);
+    frags<S>(cur, 1, lane, wm, wn, a1, b1);
+    mfmas<S>(acc, a0, b0);
+    frags<S>(cur, 2, lane, wm, wn, a0, b0);
+    mfmas<S>(acc, a1, b1);
+    frags<S>(cur, 3, lane, wm, wn, a1, b1);
+    mfmas<S>(acc, a0, b0);
+    mfmas<S>(acc, a1, b1);
+    wait_vmcnt<0>();
+    __syncthreads();
+    frags<S>(lds + ((step + 1) & 1) * S::STAGE, 0, lane, wm, wn, a0, b0);
+  }
+
+  // acc[i][j][r]: n = j 32 + lane % 32, m = i 32 + 8 (r / 4) + 4 (lane / 32) + r % 4
+  const int mw = wm * S::NI * 32 + 4 * h, nw = wn * S::NJ * 32 + (lane & 31);
+  if constexpr (EPI == kStats) {
+    const bool edge = rows < S::TM;
+#pragma unroll
+    for (int j = 0; j < S::NJ; ++j) {
+      const int64_t n = col0 + nw + j * 32;
+      const bool live = n < p.N;
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < S::NI; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (mw + i * 32 + 8 * (r >> 2) + (r & 3) >= rows) acc[i][j][r] = -INFINITY;
+      }
+      // the target's logit, if this lane holds it
+      const int64_t t = live ? p.targets[n] : -1;
+      const int64_t at = t - (p.m0 + row0) - mw;
+      const bool here = t >= 0 && t < p.classes && at >= 0 && at < S::NI * 32 && (at & 4) == 0;
+      if (__any(here)) {
+        float z = 0.0f;
+#pragma unroll
+        for (int i = 0; i < S::NI; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (at == i * 32 + 8 * (r >> 2) + (r & 3)) z = acc[i][j][r];
+        if (here) p.zt[n] = z;
+      }
+      float m = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < S::NI; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) m = fmaxf(m, acc[i][j][r]);
+      m = fmaxf(m, __shfl_xor(m, 32));
+      // a maximum of -inf leaves nothing to sum; NaNs pass fmaxf and reach the sum
+      // (the difference first: exact near the maximum however large the logits)
+      const float base = m == -INFINITY ? 0.0f : m;
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < S::NI; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          s += __builtin_amdgcn_exp2f((acc[i][j][r] - base) * kLog2e);
+      s += __shfl_xor(s, 32);
+      if (live && h == 0)
+        p.part[(int64_t)(tm * S::WM + wm) * p.N + n] = make_float2(m, s);
+    }
+  } else if constexpr (EPI == kGrad) {
+#pragma unroll
+    for (int j = 0; j < S::NJ; ++j) {
+      const int64_t n = col0 + nw + j * 32;
+      const bool live = n < p.N;
+      float a = 0.0f, bt = 0.0f, l = 0.0f;
+      int64_t at = -1;
+      if (live) {
+        const int64_t t = p.targets[n];
+        if (t >= 0 && t < p.classes) {
+          bt = p.dloss[n];
+          at = t - (p.m0 + row0) - mw;
+        }
+        a = bt + (p.dlse ? p.dlse[n] : 0.0f);
+        l = p.lse[n];
+      }
+      const bool none = a == 0.0f && bt == 0.0f;   // whatever its logits hold
+      uint16_t* o = p.out + n * p.ldo + row0 + mw;
+#pragma unroll
+      for (int i = 0; i < S::NI; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float g[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int m = i * 32 + 8 * q + r;
+            g[r] = a * __builtin_amdgcn_exp2f((acc[i][j][4 * q + r] - l) * kLog2e);
+            if (at == m) g[r] -= bt;
+            if (none || mw + m >= rows) g[r] = 0.0f;
+          }
+          const int64_t m = row0 + mw + i * 32 + 8 * q;
+          if (n < p.n_store && m < p.m_store) {
+            const u32x2 w = {pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3])};
+            *reinterpret_cast<u32x2*>(o + i * 32 + 8 * q) = w;
+          }
+        }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < S::NJ; ++j) {
+      const int64_t n = col0 + nw + j * 32;
+      if (n >= p.N) continue;
+#pragma unroll
+      for (int i = 0; i < S::NI; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t m = row0 + mw + i * 32 + 8 * q;
+          if (m >= p.M) continue;   // M is a multiple of 8: four at a time are in or out
+          if constexpr (EPI == kSlab) {
+            f32x4* o = reinterpret_cast<f32x4*>(p.slab + ((int64_t)split * p.N + n) * p.M + m);
+            f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                       acc[i][j][4 * q + 3]};
+            if (!p.first) v += *o;
+            *o = v;
+          } else {
+            const u32x2 w = {pack_bf16(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
+                             pack_bf16(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3])};
+            *reinterpret_cast<u32x2*>(p.out + n * p.ldo + m) = w;
+          }
+        }
+    }
+  }
+}
+
+// Joins the tiles' statistics: 8 tokens per workgroup, 32 threads each, their
+// partial results joined in a fixed order.
+__global__ __launch_bounds__(kThreads) void k_xent_join(const float2* part, const float* zt,
+                                                        const int64_t* targets, int64_t T,
+                                                        int64_t classes, int parts, float* loss,
+                                                        float* lse) {
+  __shared__ float2 red[32][8];
+  const int tl = threadIdx.x & 7, sl = threadIdx.x >> 3;
+  const int64_t t = (int64_t)blockIdx.x * 8 + tl;
+  float m = -INFINITY, s = 0.0f;
+  if (t < T) {
+    for (int q = sl; q < parts; q += 32) {
+      const float2 v = part[(int64_t)q * T + t];
+      const float big = fmaxf(m, v.x);
+      if (big == -INFINITY) {
+        s += v.y;   // nothing yet (a NaN stays)
+      } else {
+        s = s * __builtin_amdgcn_exp2f((m - big) * kLog2e) +
+            v.y * __builtin_amdgcn_exp2f((v.x - big) * kLog2e);
+        m = big;
+      }
+    }
+  }
+  red[sl][tl] = make_float2(m, s);
+  __syncthreads();
+  if (sl == 0 && t < T) {
+    float top = -INFINITY;
+    for (int q = 0; q < 32; ++q) top = fmaxf(top, red[q][tl].x);
+    float sum = 0.0f;
+    for (int q = 0; q < 32; ++q)
+      sum += red[q][tl].y *
+             (red[q][tl].x == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((red[q][tl].x - top) * kLog2e));
+    const float l = top + __builtin_amdgcn_logf(sum) * kLn2;   // log2
+    lse[t] = l;
+    const int64_t c = targets[t];
+    loss[t] = c >= 0 && c < classes ? l - zt[t] : 0.0f;
+  }
+}
+
+// dst[c][r] = src[r][c] for bf16, 64 x 64 tiles; rows r >= R and columns
+// c >= C of the padded destination [Cp][Rp] are zeros, and so are source rows
+// whose gradient factors are both zero (what they hold is not looked at).
+__global__ __launch_bounds__(kThreads) void k_turn(const uint16_t* src, int64_t R, int64_t C,
+                                                   int64_t ld, uint16_t* dst, int64_t Rp,
+                                                   int64_t Cp, const int64_t* targets,
+                                                   int64_t classes, const float* dloss,
+                                                   const float* dlse) {
+  __shared__ uint16_t t[64][66];
+  const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
+  const int x = threadIdx.x & 7, y = threadIdx.x >> 3;   // 8 columns of 8, 32 rows
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int64_t r = r0 + y + 32 * k, c = c0 + 8 * x;
+    u32x4 v = {0, 0, 0, 0};
+    bool take = r < R && c < C;
+    if (take && targets) {
+      const int64_t q = targets[r];
+      const float b = q >= 0 && q < classes ? dloss[r] : 0.0f;
+      const float a = b + (dlse ? dlse[r] : 0.0f);
+      take = a != 0.0f || b != 0.0f;
+    }
+    if (take) v = *reinterpret_cast<const u32x4*>(src + r * ld + c);   // C is a multiple of 8
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      t[8 * x + 2 * i][y + 32 * k] = (uint16_t)v[i];
+      t[8 * x + 2 * i + 1][y + 32 * k] = (uint16_t)(v[i] >> 16);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int64_t c = c0 + y + 32 * k, r = r0 + 8 * x;
+    if (c >= Cp || r >= Rp) continue;
+    u32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = (uint32_t)t[y + 32 * k][8 * x + 2 * i] |
+             ((uint32_t)t[y + 32 * k][8 * x + 2 * i + 1] << 16);
+    *reinterpret_cast<u32x4*>(dst + c * Rp + r) = v;
+  }
+}
+
+// out[n][m] = sum of the slabs, rounded to bf16; 4 elements per thread.
+__global__ __launch_bounds__(kThreads) void k_slab_sum(const float* slab, int64_t N, int64_t M,
+                                                       int splits, uint16_t* out, int64_t ldo) {
+  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+  if (i >= N * M) return;
+  f32x4 v = *reinterpret_cast<const f32x4*>(slab + i);
+  for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(slab + s * N * M + i);
+  const int64_t n = i / M, m = i - n * M;
+  const u32x2 w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+  *reinterpret_cast<u32x2*>(out + n * ldo + m) = w;
+}
+
+__global__ __launch_bounds__(kThreads) void k_zero_rows(uint16_t* out, int64_t N, int64_t M,
+                                                        int64_t ldo) {
+  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8;
+  if (i >= N * M) return;
+  const int64_t n = i / M, m = i - n * M;
+  *reinterpret_cast<u32x4*>(out + n * ldo + m) = u32x4{0, 0, 0, 0};
+}
+
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int64_t up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
+
+template <class S, int EPI>
+hipError_t launch_prod(Prod p, hipStream_t s) {
+  constexpr int bytes = S::ST * S::STAGE;
+  static std::atomic<uint64_t> lds_set{0};
+  const hipError_t e = set_lds_limit((const void*)k_prod<S, EPI>, bytes, lds_set);
+  if (e != hipSuccess) return e;
+  p.tiles_m = (int32_t)cdiv(p.M, S::TM);
+  p.tiles_n = (int32_t)cdiv(p.N, S::TN);
+  p.tiles = p.tiles_m * p.tiles_n;
+  if (p.splits < 1) p.splits = 1;
+  p.k_per_split = p.splits == 1 ? p.K : up(cdiv(p.K, p.splits), 64);
+  p.splits = (int32_t)cdiv(p.K, p.k_per_split);
+  hipLaunchKernelGGL((k_prod<S, EPI>), dim3((unsigned)(p.tiles * p.splits)), dim3(kThreads), bytes,
+                     s, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_turn(const uint16_t* src, int64_t R, int64_t C, int64_t ld, uint16_t* dst,
+                       int64_t Rp, int64_t Cp, const XentLaunch* dead, hipStream_t s) {
+  hipLaunchKernelGGL(k_turn, dim3((unsigned)cdiv(Cp, 64), (unsigned)cdiv(Rp, 64)), dim3(kThreads),
+                     0, s, src, R, C, ld, dst, Rp, Cp, dead ? dead->targets : nullptr,
+                     dead ? dead->V : 0, dead ? dead->dloss : nullptr,
+                     dead ? dead->dlse : nullptr);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// Backward plan: classes per piece, splits of the dh product, workspace parts.
+XentPlan xent_plan(int64_t T, int64_t V, int64_t D) {
+  XentPlan p;
+  p.parts = 2 * cdiv(V, 256);
+  p.fwd_bytes = up(8 * p.parts * T, 256) + up(4 * T, 256);
+  // one piece holds at most 2^26 elements of G, whole tiles of classes
+  int64_t piece = up(V, 256);
+  const int64_t most = ((int64_t)1 << 26) / up(T, 256) / 256 * 256;
+  if (piece > most) piece = most < 256 ? 256 : most;
+  p.pieces = cdiv(V, piece);
+  p.piece = piece;
+  p.Tp = up(T, 64);
+  // the dh product has few tiles and a long K: split it until the chip is
+  // covered, at least 512 of K each
+  const int64_t tiles = cdiv(D, 256) * cdiv(T, 256);
+  int64_t splits = cdiv(256, tiles);
+  if (splits > piece / 512) splits = piece / 512;
+  if (splits < 1) splits = 1;
+  p.splits = (int32_t)cdiv(piece, up(cdiv(piece, splits), 64));
+  int64_t at = 0;
+  auto take = [&](int64_t bytes) { const int64_t o = at; at += up(bytes, 256); return o; };
+  p.g = take(2 * T * piece);
+  p.gt = take(2 * piece * p.Tp);
+  p.wt = take(2 * D * piece);
+  p.ht = take(2 * D * p.Tp);
+  p.slab = take(4 * (int64_t)p.splits * T * D);
+  p.bwd_bytes = at;
+  return p;
+}
+
+hipError_t launch_xent_fwd(const XentLaunch& x, hipStream_t s) {
+  const XentPlan pl = xent_plan(x.T, x.V, x.D);
+  Prod p = {};
+  p.a = x.w; p.lda = x.ldw; p.M = x.V;
+  p.b = x.h; p.ldb = x.ldh; p.N = x.T;
+  p.K = x.D;
+  p.part = reinterpret_cast<float2*>(x.ws);
+  p.zt = reinterpret_cast<float*>(x.ws + up(8 * pl.parts * x.T, 256));
+  p.targets = x.targets;
+  p.classes = x.V;
+  hipError_t e = launch_prod<Big, kStats>(p, s);
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_xent_join, dim3((unsigned)cdiv(x.T, 8)), dim3(kThreads), 0, s, p.part, p.zt,
+                     x.targets, x.T, x.V, (int)pl.parts, x.loss, x.lse_out);
+  return hipGetLastError();
+}
+
+hipError_t launch_xent_bwd(const XentLaunch& x, hipStream_t s) {
+  if (x.T == 0) {   // no token: dW is zero
+    hipLaunchKernelGGL(k_zero_rows, dim3((unsigned)cdiv(x.V * x.D, 8 * kThreads)), dim3(kThreads), 0,
+                       s, x.dw, x.V, x.D, x.lddw);
+    return hipGetLastError();
+  }
+  const XentPlan pl = xent_plan(x.T, x.V, x.D);
+  uint16_t* G = reinterpret_cast<uint16_t*>(x.ws + pl.g);
+  uint16_t* GT = reinterpret_cast<uint16_t*>(x.ws + pl.gt);
+  uint16_t* WT = reinterpret_cast<uint16_t*>(x.ws + pl.wt);
+  uint16_t* HT = reinterpret_cast<uint16_t*>(x.ws + pl.ht);
+  float* slab = reinterpret_cast<float*>(x.ws + pl.slab);
+  hipError_t e = launch_turn(x.h, x.T, x.D, x.ldh, HT, pl.Tp, x.D, &x, s);
+  if (e != hipSuccess) return e;
+  int32_t splits = 1;
+  for (int64_t c = 0; c < pl.pieces; ++c) {
+    const int64_t v0 = c * pl.piece, vn = x.V - v0 < pl.piece ? x.V - v0 : pl.piece;
+    const int64_t vp = up(vn, 64);   // padded with zeros, in G and in W^T
+    const uint16_t* W = x.w + v0 * x.ldw;
+    Prod p = {};
+    p.a = W; p.lda = x.ldw; p.M = vn;
+    p.b = x.h; p.ldb = x.ldh; p.N = x.T;
+    p.K = x.D;
+    p.targets = x.targets;
+    p.m0 = v0;
+    p.classes = x.V;
+    p.lse = x.lse;
+    p.dloss = x.dloss;
+    p.dlse = x.dlse;
+    p.out = G;
+    p.ldo = vp;
+    p.m_store = vp;
+    p.n_store = x.T;
+    if ((e = launch_prod<Big, kGrad>(p, s)) != hipSuccess) return e;
+    if ((e = launch_turn(G, x.T, vp, vp, GT, pl.Tp, vp, nullptr, s)) != hipSuccess) return e;
+    if ((e = launch_turn(W, vn, x.D, x.ldw, WT, vp, x.D, nullptr, s)) != hipSuccess) return e;
+    Prod d = {};
+    d.a = WT; d.lda = vp; d.M = x.D;
+    d.b = G; d.ldb = vp; d.N = x.T;
+    d.K = vp;
+    d.splits = pl.splits;
+    d.slab = slab;
+    d.first = c == 0;
+    if ((e = launch_prod<Big, kSlab>(d, s)) != hipSuccess) return e;
+    Prod w = {};
+    w.a = HT; w.lda = pl.Tp; w.M = x.D;
+    w.b = GT; w.ldb = pl.Tp; w.N = vn;
+    w.K = pl.Tp;
+    w.out = x.dw + v0 * x.lddw;
+    w.ldo = x.lddw;
+    if ((e = launch_prod<Big, kOut>(w, s)) != hipSuccess) return e;
+    if (c == 0) splits = (int32_t)cdiv(vp, pl.splits == 1 ? vp : up(cdiv(vp, pl.splits), 64));
+  }
+  hipLaunchKernelGGL(k_slab_sum, dim3((unsigned)cdiv(x.T * x.D, 4 * kThreads)), dim3(kThreads), 0, s,
+                     slab, x.T, x.D, splits, x.dh, x.lddh);
+  return hipGetLastError();
+}
+
+}  // namespace ufp4
