@@ -426,6 +426,41 @@ int ufp4_linear_xent_bwd(const void* h, int64_t ldh, const void* w, int64_t ldw,
  * sizes that the calls refuse or that need none (T == 0). */
 size_t ufp4_linear_xent_workspace_bytes(int64_t T, int64_t V, int64_t D, int32_t backward);
 
+/* A whole mixture-of-experts layer for a few tokens (generation: 1 .. 64 of
+ * them) on 4-bit weights, activations in high precision:
+ *   chosen(t) = the top_k largest of logits[t][0 .. E-1]; of equal ones the
+ *               lowest index; -inf and NaN are never chosen
+ *   p[t][e]   = softmax of the logits over chosen(t) (renorm != 0), or over all
+ *               experts that are not -inf or NaN (renorm == 0)
+ *   y[t] = sum over e in chosen(t) of
+ *          p[t][e] Wd_e R(act(Wg_e R(x[t])) * (Wu_e R(x[t])))
+ * where W is what the codes and scales stand for and R the random rotation of
+ * that weight's quantization ([UFP4] Method: the rotation cancels in the
+ * product), so that the weights are the ones ufp4_rht_quant(along = 0) or
+ * ufp4_rht_quant_dual's row side wrote for FPROP.  A token with nothing to
+ * choose has y = 0.
+ *   x : bf16 [T][ldx], 16-byte aligned, ldx % 8 == 0;  logits : fp32 [T][ldl];
+ *   Wg, Wu : stacked [E*F][H];  Wd : stacked [E*H][F];  y : bf16 [T][ldy], 4-byte
+ *   aligned, ldy even, overwritten.
+ * Activations carry 16 bits of mantissa or more up to the one rounding of y;
+ * level products, scales and sums are fp32, added in a fixed order (equal
+ * inputs give equal bits).  T = 0 is a no-op.
+ * workspace: ufp4_moe_tokens_workspace_bytes(T, E, top_k, H, F) bytes,
+ * 256-byte aligned, any contents; calls that share one must be ordered on one
+ * stream.
+ * Errors: UFP4_ERR_INVALID_ARG (null pointers, sizes, pitches, alignment, top_k
+ * not in 1 .. E, a small workspace); UFP4_ERR_SHAPE (H or F not a multiple of
+ * 32, P not E times the other matrix's K); UFP4_ERR_MISMATCH (Wg and Wu differ
+ * in K, grid, scale mode, blocks, rht_n or sign_seed); UFP4_ERR_UNSUPPORTED
+ * (T > 64, E > 256, top_k > 16, E4M3 weights, E F or E H above 2^31 - 1). */
+int ufp4_moe_tokens(const void* x, int64_t ldx, int64_t T, const float* logits, int64_t ldl,
+                    int32_t E, int32_t top_k, int32_t renorm, int32_t act, const ufp4_qtensor* Wg,
+                    const ufp4_qtensor* Wu, const ufp4_qtensor* Wd, void* y, int64_t ldy,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of ufp4_moe_tokens; 0 for sizes that it refuses and T = 0. */
+size_t ufp4_moe_tokens_workspace_bytes(int64_t T, int32_t E, int32_t top_k, int64_t H, int64_t F);
+
 /* Name of a status code (static string). */
 const char* ufp4_status_string(int status);
 

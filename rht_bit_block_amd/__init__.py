@@ -40,6 +40,7 @@ EXPORTED = [
     "ufp4_philox_fill", "ufp4_stream_copy", "ufp4_status_string",
     "ufp4_glu_fwd", "ufp4_glu_bwd",
     "ufp4_linear_xent_fwd", "ufp4_linear_xent_bwd", "ufp4_linear_xent_workspace_bytes",
+    "ufp4_moe_tokens", "ufp4_moe_tokens_workspace_bytes",
 ]
 
 
@@ -136,6 +137,8 @@ def _lib():
                                      ctypes.c_size_t, vp],
             "ufp4_linear_xent_bwd": [vp, i64, vp, i64, vp, i64, i64, i64, vp, vp, vp, vp, i64, vp,
                                      i64, vp, ctypes.c_size_t, vp],
+            "ufp4_moe_tokens": [vp, i64, i64, vp, i64, i32, i32, i32, i32, qtp, qtp, qtp, vp, i64,
+                                vp, ctypes.c_size_t, vp],
         }
         for name, args in sig.items():
             f = getattr(lib, name)
@@ -145,6 +148,8 @@ def _lib():
         lib.ufp4_gemm_workspace_bytes.restype = ctypes.c_size_t
         lib.ufp4_linear_xent_workspace_bytes.argtypes = [i64, i64, i64, i32]
         lib.ufp4_linear_xent_workspace_bytes.restype = ctypes.c_size_t
+        lib.ufp4_moe_tokens_workspace_bytes.argtypes = [i64, i32, i32, i64, i64]
+        lib.ufp4_moe_tokens_workspace_bytes.restype = ctypes.c_size_t
         lib.ufp4_codes_bytes.argtypes = [i64, i64]
         lib.ufp4_codes_bytes.restype = ctypes.c_size_t
         lib.ufp4_scales_bytes.argtypes = [i64, i64, cfgp]
@@ -719,6 +724,48 @@ def ufp4_linear_xent_bwd(h: torch.Tensor, w: torch.Tensor, targets: torch.Tensor
                                      _ptr(ws), ws.numel(), _stream(w))
     _check("ufp4_linear_xent_bwd", st)
     return dh, dw
+
+
+def ufp4_moe_tokens_workspace_bytes(T, E, top_k, H, F):
+    return int(_lib().ufp4_moe_tokens_workspace_bytes(int(T), int(E), int(top_k), int(H), int(F)))
+
+
+def ufp4_moe_tokens(x: torch.Tensor, logits: torch.Tensor, wg: QTensor, wu: QTensor, wd: QTensor,
+                    top_k: int, renorm=True, act=UFP4_ACT_SILU, out=None, workspace=None):
+    """A mixture-of-experts layer for up to 64 tokens on 4-bit weights: routing
+    from the router's logits [T, E] (float32), gate and up products (wg, wu
+    stacked [E*F, H]), activation, down product (wd stacked [E*H, F]) and the
+    weighted sum over the chosen experts.  x [T, H] bfloat16 in the unrotated
+    basis; returns y [T, H] bfloat16.  workspace: uint8 device buffer of
+    ufp4_moe_tokens_workspace_bytes (allocated when not given)."""
+    ldx = _check_input("x", x, None, torch.bfloat16)
+    T, H = x.shape
+    dev = x.device
+    ldl = _check_input("logits", logits, None, torch.float32, dev)
+    E = logits.shape[1]
+    if logits.shape[0] != T:
+        raise ValueError(f"logits has {logits.shape[0]} rows, x has {T}")
+    if wg.K != H:
+        raise ValueError(f"wg contracts {wg.K} elements, x has {H}")
+    a, b, c = wg.c(), wu.c(), wd.c()
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    ldy = _check_input("out", out, x.shape, torch.bfloat16, dev)
+    for name, q in (("wg", wg), ("wu", wu), ("wd", wd)):
+        if q.codes.device != dev:
+            raise ValueError(f"{name} must be on {dev}")
+    _on_gpu(x)
+    need = int(_lib().ufp4_moe_tokens_workspace_bytes(T, E, int(top_k), H, wd.K))
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _check_buffer("workspace", workspace, torch.uint8, need, dev)
+    st = _lib().ufp4_moe_tokens(_ptr(x), ldx, T, _ptr(logits), ldl, E, int(top_k),
+                                int(bool(renorm)), int(act), ctypes.byref(a), ctypes.byref(b),
+                                ctypes.byref(c), _ptr(out), ldy, _ptr(workspace),
+                                workspace.numel(), _stream(x))
+    _check("ufp4_moe_tokens", st)
+    return out
 
 
 def ufp4_codes_bytes(P, K):

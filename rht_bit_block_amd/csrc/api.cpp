@@ -335,6 +335,16 @@ namespace ufp4 {
 
 static_assert(kDiagWorkspaceBytes == UFP4_DIAG_WORKSPACE_BYTES, "diagnostics workspace size");
 
+int check_operand(const ufp4_qtensor* t) { return check_qtensor(t); }
+
+void sign_bits128(const ufp4_quant_cfg* c, uint32_t out[4]) {
+  sign_patterns(c, 32, out);
+  if (c->rht_n == 64) {   // two chunks
+    out[2] = out[0];
+    out[3] = out[1];
+  }
+}
+
 // Validation and launch description of a level-statistics call (shared by
 // ufp4_quant_diag and its variant on the library's own scratch array).
 int diag_prepare(const void* x, int64_t rows, int64_t cols, int64_t ld, const ufp4_quant_cfg* cfg,

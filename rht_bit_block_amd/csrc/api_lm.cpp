@@ -1,6 +1,7 @@
 // C ABI of the language-model operators around the 4-bit GEMMs: argument
 // validation and launch planning.  As in api.cpp every check runs before any
 // HIP call, so a rejected call has no side effect and needs no GPU.
+#include <cmath>
 #include <cstring>
 
 #include "../../include/ufp4.h"
@@ -40,9 +41,96 @@ int xent_matrix(const void* p, int64_t ld, int64_t cols) {
   return ld > ((int64_t)1 << 20) ? UFP4_ERR_UNSUPPORTED : UFP4_OK;
 }
 
+int moe_sizes(int64_t T, int64_t E, int64_t k, int64_t H, int64_t F) {
+  if (T < 0 || E < 1 || k < 1 || k > E || H < 1 || F < 1) return UFP4_ERR_INVALID_ARG;
+  if (H % 32 || F % 32) return UFP4_ERR_SHAPE;
+  if (T > kMoeMaxTokens || E > kMoeMaxExperts || k > kMoeMaxChoices || H > INT32_MAX / E ||
+      F > INT32_MAX / E)
+    return UFP4_ERR_UNSUPPORTED;
+  return UFP4_OK;
+}
+
+MoeWeight moe_weight(const ufp4_qtensor* t) {
+  MoeWeight w;
+  w.codes = t->codes;
+  w.scales = static_cast<const uint8_t*>(t->scales);
+  const bool e8 = t->cfg.scale_mode == UFP4_SCALE_POW2;
+  w.scale_pitch = t->K / t->cfg.block_cols * (e8 ? 1 : 4);
+  w.row_shift = t->cfg.block_rows == 32 ? 5 : t->cfg.block_rows == 16 ? 4 : 0;
+  w.grid = t->cfg.grid;
+  w.kind = (e8 ? 2 : 0) + (t->cfg.block_cols == 16 ? 1 : 0);
+  w.factor = t->cfg.tensor_scale != 0.0f ? t->cfg.tensor_scale : 1.0f;
+  return w;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t ufp4_moe_tokens_workspace_bytes(int64_t T, int32_t E, int32_t top_k, int64_t H, int64_t F) {
+  if (moe_sizes(T, E, top_k, H, F) || T == 0) return 0;
+  MoeLaunch p;
+  std::memset(&p, 0, sizeof(p));
+  p.T = T;
+  p.E = E;
+  p.k = top_k;
+  p.H = H;
+  p.F = F;
+  return (size_t)moe_plan(p, nullptr);
+}
+
+int ufp4_moe_tokens(const void* x, int64_t ldx, int64_t T, const float* logits, int64_t ldl,
+                    int32_t E, int32_t top_k, int32_t renorm, int32_t act, const ufp4_qtensor* Wg,
+                    const ufp4_qtensor* Wu, const ufp4_qtensor* Wd, void* y, int64_t ldy,
+                    void* workspace, size_t workspace_bytes, void* stream) {
+  if (!act_ok(act) || !Wg || !Wu || !Wd || E < 1) return UFP4_ERR_INVALID_ARG;
+  int st;
+  if ((st = check_operand(Wg)) || (st = check_operand(Wu)) || (st = check_operand(Wd))) return st;
+  if (Wg->P % E || Wd->P % E) return UFP4_ERR_SHAPE;
+  const int64_t H = Wg->K, F = Wg->P / E;
+  if ((st = moe_sizes(T, E, top_k, H, F))) return st;
+  const ufp4_quant_cfg &a = Wg->cfg, &b = Wu->cfg;
+  if (Wu->K != H || a.grid != b.grid || a.scale_mode != b.scale_mode ||
+      a.block_rows != b.block_rows || a.block_cols != b.block_cols || a.rht_n != b.rht_n ||
+      (a.rht_n > 1 && a.sign_seed != b.sign_seed))
+    return UFP4_ERR_MISMATCH;
+  if (Wu->P != Wg->P || Wd->P != E * H || Wd->K != F) return UFP4_ERR_SHAPE;
+  if (a.grid == UFP4_E4M3 || Wd->cfg.grid == UFP4_E4M3) return UFP4_ERR_UNSUPPORTED;
+  if (T == 0) return UFP4_OK;
+  if (!x || !logits || !y || !workspace) return UFP4_ERR_INVALID_ARG;
+  if (ldx < H || ldx % 8 || ldl < E || ldy < H || ldy % 2) return UFP4_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(logits, 4) || !aligned(y, 4) || !aligned(workspace, 256) ||
+      !aligned(Wg->codes, 16) || !aligned(Wu->codes, 16) || !aligned(Wd->codes, 16))
+    return UFP4_ERR_INVALID_ARG;
+  if (workspace_bytes < ufp4_moe_tokens_workspace_bytes(T, E, top_k, H, F))
+    return UFP4_ERR_INVALID_ARG;
+  MoeLaunch p;
+  std::memset(&p, 0, sizeof(p));
+  p.x = static_cast<const uint16_t*>(x);
+  p.logits = logits;
+  p.y = static_cast<uint16_t*>(y);
+  p.ldx = ldx;
+  p.ldl = ldl;
+  p.ldy = ldy;
+  p.T = T;
+  p.H = H;
+  p.F = F;
+  p.E = E;
+  p.k = top_k;
+  p.renorm = renorm != 0;
+  p.act = act;
+  p.wg = moe_weight(Wg);
+  p.wu = moe_weight(Wu);
+  p.wd = moe_weight(Wd);
+  p.nx = a.rht_n;
+  p.nh = Wd->cfg.rht_n;
+  p.cnx = (float)(1.0 / std::sqrt((double)p.nx));   // as the quantizer's c_n
+  p.cnh = (float)(1.0 / std::sqrt((double)p.nh));
+  sign_bits128(&a, p.sign_x);
+  sign_bits128(&Wd->cfg, p.sign_h);
+  moe_plan(p, static_cast<uint8_t*>(workspace));
+  return hip_status(launch_moe_tokens(p, (hipStream_t)stream));
+}
 
 size_t ufp4_linear_xent_workspace_bytes(int64_t T, int64_t V, int64_t D, int32_t backward) {
   if (xent_sizes(T, V, D) || T == 0) return 0;

@@ -1,5 +1,6 @@
 // Internal interface between the C ABI of the language-model operators
-// (api_lm.cpp: validation, planning) and their HIP kernels (glu.hip, xent.hip).
+// (api_lm.cpp: validation, planning) and their HIP kernels (glu.hip, xent.hip,
+// moe_tokens.hip).
 // Host-visible structs only; every pointer is a device pointer.
 #pragma once
 
@@ -59,5 +60,46 @@ struct XentPlan {
 XentPlan xent_plan(int64_t T, int64_t V, int64_t D);
 hipError_t launch_xent_fwd(const XentLaunch& x, hipStream_t s);
 hipError_t launch_xent_bwd(const XentLaunch& x, hipStream_t s);
+
+constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 256, kMoeMaxChoices = 16;
+
+// One expert matrix, stacked over the experts: codes of row r at r K / 2,
+// scales of row r at (r >> row_shift) * scale_pitch bytes.
+struct MoeWeight {
+  const uint8_t* codes;
+  const uint8_t* scales;
+  int64_t scale_pitch;
+  int32_t row_shift;
+  int32_t grid;
+  int32_t kind;      // 0 fp32 / 32, 1 fp32 / 16, 2 E8M0 / 32, 3 E8M0 / 16
+  float factor;      // per-tensor factor of two-level scaling, else 1
+};
+
+struct MoeLaunch {
+  const uint16_t* x;       // bf16 [T][ldx]
+  const float* logits;     // [T][ldl]
+  uint16_t* y;             // bf16 [T][ldy]
+  int64_t ldx, ldl, ldy;
+  int64_t T, H, F;
+  int32_t E, k, renorm, act;
+  MoeWeight wg, wu, wd;
+  int32_t nx, nh;          // rotation of x and of the intermediate
+  float cnx, cnh;
+  uint32_t sign_x[4], sign_h[4];   // sign bits of 128 consecutive elements
+  // set by moe_plan
+  int32_t splits, by_pair;
+  int* ids;                // [T][k] chosen experts, -1: none
+  float* share;            // [T][k]
+  int* count;              // [E] tokens of each expert
+  int* list;               // [E][T] those tokens
+  int* done;               // [H / 16] finished splits of an output tile
+  uint8_t* xr;             // rotated x: [T][H], 4 bytes an element
+  uint8_t* hr;             // rotated intermediate: [E][T][F], 4 bytes an element
+  float* partial;          // [H / 16][splits][T][16]
+};
+
+// Fills the plan and returns the workspace's size in bytes (ws may be null).
+int64_t moe_plan(MoeLaunch& p, uint8_t* ws);
+hipError_t launch_moe_tokens(const MoeLaunch& p, hipStream_t s);
 
 }  // namespace ufp4
