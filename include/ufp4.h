@@ -452,7 +452,7 @@ size_t ufp4_linear_xent_workspace_bytes(int64_t T, int64_t V, int64_t D, int32_t
  * not in 1 .. E, a small workspace); UFP4_ERR_SHAPE (H or F not a multiple of
  * 32, P not E times the other matrix's K); UFP4_ERR_MISMATCH (Wg and Wu differ
  * in K, grid, scale mode, blocks, rht_n or sign_seed); UFP4_ERR_UNSUPPORTED
- * (T > 64, E > 256, top_k > 16, E4M3 weights, E F or E H above 2^31 - 1). */
+ * (T > 64, E > 256, top_k > 16, H or F > 2^20, E4M3 weights). */
 int ufp4_moe_tokens(const void* x, int64_t ldx, int64_t T, const float* logits, int64_t ldl,
                     int32_t E, int32_t top_k, int32_t renorm, int32_t act, const ufp4_qtensor* Wg,
                     const ufp4_qtensor* Wu, const ufp4_qtensor* Wd, void* y, int64_t ldy,

@@ -44,8 +44,8 @@ int xent_matrix(const void* p, int64_t ld, int64_t cols) {
 int moe_sizes(int64_t T, int64_t E, int64_t k, int64_t H, int64_t F) {
   if (T < 0 || E < 1 || k < 1 || k > E || H < 1 || F < 1) return UFP4_ERR_INVALID_ARG;
   if (H % 32 || F % 32) return UFP4_ERR_SHAPE;
-  if (T > kMoeMaxTokens || E > kMoeMaxExperts || k > kMoeMaxChoices || H > INT32_MAX / E ||
-      F > INT32_MAX / E)
+  if (T > kMoeMaxTokens || E > kMoeMaxExperts || k > kMoeMaxChoices || H > kMoeMaxWidth ||
+      F > kMoeMaxWidth)
     return UFP4_ERR_UNSUPPORTED;
   return UFP4_OK;
 }

@@ -32,6 +32,16 @@ __device__ __forceinline__ void lds_load16(uint32_t lds_addr, const sgpr4& r, ui
                : "memory");
 }
 
+// The same, 4 bytes per lane.
+__device__ __forceinline__ void lds_load4(uint32_t lds_addr, const sgpr4& r, uint32_t voff,
+                                          uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_dword %1, %2, %3 offen lds"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(lds_addr)), "v"(voff), "s"(r),
+                 "s"(__builtin_amdgcn_readfirstlane(soff))
+               : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void wait_vmcnt() {
   asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");

@@ -62,6 +62,9 @@ hipError_t launch_xent_fwd(const XentLaunch& x, hipStream_t s);
 hipError_t launch_xent_bwd(const XentLaunch& x, hipStream_t s);
 
 constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 256, kMoeMaxChoices = 16;
+constexpr int64_t kMoeMaxWidth = 1 << 20;   // 32-bit offsets inside a 16-row tile and x
+// Up to here the up product's workgroups route and rotate x themselves.
+constexpr int kMoeFusedTokens = 8;
 
 // One expert matrix, stacked over the experts: codes of row r at r K / 2,
 // scales of row r at (r >> row_shift) * scale_pitch bytes.
@@ -87,15 +90,16 @@ struct MoeLaunch {
   float cnx, cnh;
   uint32_t sign_x[4], sign_h[4];   // sign bits of 128 consecutive elements
   // set by moe_plan
-  int32_t splits, by_pair;
+  int32_t by_pair, fused, slots;   // slots: the T k choices, or all experts if fewer
+  int32_t run_up, run_down;        // columns per workgroup of the two products
   int* ids;                // [T][k] chosen experts, -1: none
   float* share;            // [T][k]
-  int* count;              // [E] tokens of each expert
-  int* list;               // [E][T] those tokens
-  int* done;               // [H / 16] finished splits of an output tile
+  int* expert;             // [slots] a slot's expert
+  int* count;              // [slots] its tokens
+  int* place;              // [T][k] row slot T + i of a choice, -1: none
   uint8_t* xr;             // rotated x: [T][H], 4 bytes an element
-  uint8_t* hr;             // rotated intermediate: [E][T][F], 4 bytes an element
-  float* partial;          // [H / 16][splits][T][16]
+  float* h;                // weighted intermediate: [slots][T][F]
+  float* partial;          // down products: [slots][T][H]
 };
 
 // Fills the plan and returns the workspace's size in bytes (ws may be null).

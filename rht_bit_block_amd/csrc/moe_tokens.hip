@@ -12,13 +12,14 @@
 // lane, straight from HBM into registers, and everything else is sized to
 // hide behind that.
 //
-// Three launches:
-//   k_moe_route  one workgroup per token: routing, and R x
-//   k_moe_up     one workgroup per chosen expert and run of max(32, n) columns:
-//                both products, the activation, the weight p and the rotation
-//                of the run for the down product
-//   k_moe_down   one workgroup per 16 output columns (and a share of the
-//                experts): the down product summed over the experts
+// Launches:
+//   k_moe_up     one workgroup per chosen expert and run of NF columns: both
+//                products, the activation and the weight p.  For a handful of
+//                tokens the routing and the rotation of x run in front, in
+//                every workgroup; otherwise k_moe_route has done both once.
+//   k_moe_down   one workgroup per chosen expert and run of output columns,
+//                behind the rotation of its tokens' intermediate
+//   k_moe_join   a token's experts added up
 //
 // Products: v_mfma_f32_16x16x32_bf16 with 16 tokens as rows and 16 weight rows
 // as columns.  A code's level is exact in bf16; an activation is split into
@@ -28,13 +29,17 @@
 // by the block's scale, which is the same for a lane's four values (one weight
 // row), so that scales never enter the bf16 operands.
 //
-// A lane loads 16 bytes = 32 codes of one weight row: lanes l, l + 16, l + 32,
-// l + 48 hold four consecutive 32-element blocks of row l % 16.  The matrix
-// instruction wants 8 codes of ONE block from each of the four, so the 4 x 4
-// words of the four lanes are transposed in registers (two lane-half swaps and
-// two row swaps).
+// The weights go HBM -> LDS (buffer_load ... lds) in steps of 128 of K, three
+// steps per wave in a ring of its own, so that no barrier or register holds a
+// load back: a lane copies 16 bytes and four neighbouring lanes a row's 64.
+// Straight into registers in the layout of the instruction (neighbouring lanes
+// in different rows) every lane's 16 bytes were a cache access of their own,
+// and the address unit, not HBM, set the pace (200 us against 35 for the up
+// product of 16 tokens).  The activations of the workgroup's tokens lie in LDS,
+// 64 KB of them at a time.
 #include <type_traits>
 
+#include "lds_copy.h"
 #include "lm_internal.h"
 
 namespace ufp4 {
@@ -45,11 +50,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32u __attribute__((aligned(1)));
-typedef unsigned long long u64u __attribute__((aligned(1)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
@@ -61,10 +62,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 
 // --- codes -> bf16 levels ------------------------------------------------------
-// E4M3 bytes of the level magnitudes 0..7 (INT4: of the nibbles 0..7 and 8..15).
+// E4M3 bytes of the level magnitudes 0..7 of E1M2, and of INT4's nibbles 0..7
+// and 8..15.
 template <int GRID> struct Lut;
 template <> struct Lut<0> { static constexpr uint32_t lo = 0x34302800u, hi = 0x3E3C3A38u; };
-template <> struct Lut<2> { static constexpr uint32_t lo = 0x3C383000u, hi = 0x4C484440u; };
 template <> struct Lut<1> {
   static constexpr uint32_t lo = 0x44403800u, hi = 0x4E4C4A48u;
   static constexpr uint32_t nlo = 0xCACCCED0u, nhi = 0xB8C0C4C8u;
@@ -83,23 +84,28 @@ __device__ __forceinline__ uint32_t nib_to_e4m3(uint32_t v) {
   }
 }
 
-// The bf16 levels of 8 codes in the order 0 2 4 6 1 3 5 7 (activations are
-// stored in the same order).
+// The bf16 levels of 8 codes.  E2M1 codes are FP4 values, which convert by
+// themselves, two at a time; the uniform grids go through E4M3 bytes, the even
+// codes first (the activations are stored in the same order).
 template <int GRID>
 __device__ __forceinline__ u32x4 levels8(uint32_t w) {
-  const uint32_t ev = nib_to_e4m3<GRID>(w & 0x0F0F0F0Fu);
-  const uint32_t od = nib_to_e4m3<GRID>((w >> 4) & 0x0F0F0F0Fu);
   auto two = [](bf16x2 v) { return __builtin_bit_cast(uint32_t, v); };
-  return u32x4{two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(ev, 1.0f, false)),
-               two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(ev, 1.0f, true)),
-               two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(od, 1.0f, false)),
-               two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(od, 1.0f, true))};
+  if constexpr (GRID == 2) {
+    return u32x4{two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0)),
+                 two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1)),
+                 two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2)),
+                 two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3))};
+  } else {
+    const uint32_t ev = nib_to_e4m3<GRID>(w & 0x0F0F0F0Fu);
+    const uint32_t od = nib_to_e4m3<GRID>((w >> 4) & 0x0F0F0F0Fu);
+    return u32x4{two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(ev, 1.0f, false)),
+                 two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(ev, 1.0f, true)),
+                 two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(od, 1.0f, false)),
+                 two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(od, 1.0f, true))};
+  }
 }
 
-// Position of element i of an 8-group in that order.
-__device__ __forceinline__ int slot8(int i) { return 4 * (i & 1) + (i >> 1); }
-
-// --- scales ---------------------------------------------------------------------
+// --- weights in LDS -----------------------------------------------------------
 // Scale kinds: fp32 or E8M0, 32- or 16-element blocks along K.
 enum { kF32b32 = 0, kF32b16 = 1, kE8b32 = 2, kE8b16 = 3 };
 template <int SK> struct Sk {
@@ -107,92 +113,130 @@ template <int SK> struct Sk {
   static constexpr int per = (SK & 1) ? 2 : 1;   // scales per 32 elements
 };
 
-__device__ __forceinline__ float e8m0(uint32_t byte) {
-  return __uint_as_float(byte ? byte << 23 : 0x00400000u);   // 0 is 2^-127
-}
+// A wave's ring: kRing steps of two 16-row tiles, each 1 KB of codes and up to
+// 512 bytes of scales.
+constexpr int kRing = 3, kTileBytes = 1024 + 512, kStepBytes = 2 * kTileBytes;
+constexpr int kCopies = 4;   // loads per wave and step
+constexpr int kActBytes = 64 * 1024;
+constexpr int kLdsBytes = kActBytes + kWaves * kRing * kStepBytes;
 
-// One 16-row tile's codes and scales of four 32-element blocks (128 of K).
-template <int SK>
-struct Tile {
-  u32x4 codes;               // this lane's block: row l % 16, block l / 16
-  float s[4 * Sk<SK>::per];  // the row's scales of all four blocks
+// Where a 16-row tile comes from.
+struct TileSource {
+  sgpr4 codes, scales;
+  uint32_t vcodes, vscales;   // this lane's offsets at step 0
+  uint32_t shift;             // E8M0: where in its word this lane's row starts
 };
 
-// crow, srow: this lane's row; b0: first of the four blocks, nb: blocks of K.
+// row0: the tile's first row (a multiple of 16) in the stacked matrix of K
+// columns.  Past the tile's end the loads give zeros; between rows they give
+// the next row's bytes, which no block below K / 32 meets.
 template <int SK>
-__device__ __forceinline__ void load_tile(Tile<SK>& t, const uint8_t* crow, const uint8_t* srow,
-                                          int b0, int nb, int g) {
+__device__ __forceinline__ TileSource tile_source(const MoeWeight& w, int64_t row0, int64_t K,
+                                                  int lane) {
   constexpr int P = Sk<SK>::per;
-  t.codes = u32x4{0, 0, 0, 0};
-  if (b0 + g < nb)   // each byte is read once: past the caches' keeping
-    t.codes = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(crow + 16 * (int64_t)(b0 + g)));
-  if (b0 + 4 <= nb) {
-    if constexpr (Sk<SK>::e8) {
-      if constexpr (P == 1) {
-        const uint32_t w = *reinterpret_cast<const u32u*>(srow + b0);
+  TileSource t;
+  const uint32_t half = (uint32_t)(K / 2);
+  t.codes = rsrc4(w.codes + row0 * half, 16 * half);
+  // lane l: row l / 4, its 16-byte chunk in the place l % 4 of the row's 64
+  // bytes; places are exchanged by row / 4 so that the 64 lanes' word reads
+  // below fall on 64 banks
+  const int r = lane >> 2;
+  t.vcodes = (uint32_t)r * half + 16u * (uint32_t)((lane & 3) ^ (r >> 2));
+  const uint8_t* s = w.scales + (row0 >> w.row_shift) * w.scale_pitch;
+  const uint32_t pitch = w.row_shift ? 0u : (uint32_t)w.scale_pitch;   // square blocks: one row
+  t.shift = 0;
+  if constexpr (!Sk<SK>::e8) {
+    t.scales = rsrc4(s, 15 * pitch + (uint32_t)w.scale_pitch);
+    // 16 bytes of fp32 scales per lane, one (b32) or two (b16) lanes per row
+    t.vscales = (uint32_t)(lane / P) * pitch + 16u * (uint32_t)(lane % P);
+  } else {
+    // bytes at any alignment: whole words around them, two (b32) or four (b16)
+    // per row
+    const uint32_t off = (uint32_t)((uintptr_t)s & 3);
+    t.scales = rsrc4(s - off, (off + 15 * pitch + (uint32_t)w.scale_pitch + 3) & ~3u);
+    constexpr int W = 2 * P;
+    t.vscales = ((off + (uint32_t)(lane / W) * pitch) & ~3u) + 4u * (uint32_t)(lane % W);
+    t.shift = (off + (uint32_t)(lane & 15) * pitch) & 3;
+  }
+  return t;
+}
+
+// Copies step `step` (elements 128 step ..) of a tile to LDS address `to`.
+template <int SK>
+__device__ __forceinline__ void copy_tile(const TileSource& t, uint32_t to, int step, int lane) {
+  constexpr int P = Sk<SK>::per;
+  lds_load16(to, t.codes, t.vcodes, 64u * (uint32_t)step);
+  if constexpr (!Sk<SK>::e8) {
+    if (lane < 16 * P) lds_load16(to + 1024, t.scales, t.vscales, 16u * P * (uint32_t)step);
+  } else {
+    if (lane < 32 * P) lds_load4(to + 1024, t.scales, t.vscales, 4u * P * (uint32_t)step);
+  }
+}
+
+// The four blocks' scales of this lane's row (column of the instruction).
+template <int SK>
+__device__ __forceinline__ void read_scales(const uint8_t* tile, uint32_t shift, int r16,
+                                            float (&s)[4 * Sk<SK>::per]) {
+  constexpr int P = Sk<SK>::per;
+  if constexpr (!Sk<SK>::e8) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) t.s[j] = e8m0((w >> (8 * j)) & 255u);
-      } else {
-        const unsigned long long w = *reinterpret_cast<const u64u*>(srow + 2 * b0);
+    for (int q = 0; q < P; ++q) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(tile + 1024 + 16 * (P * r16 + q));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t.s[j] = e8m0((uint32_t)(w >> (8 * j)) & 255u);
-      }
-    } else {
-#pragma unroll
-      for (int q = 0; q < P; ++q) {
-        const f32x4u v = reinterpret_cast<const f32x4u*>(srow + 4 * P * (int64_t)b0)[q];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) t.s[4 * q + j] = v[j];
-      }
+      for (int i = 0; i < 4; ++i) s[4 * q + i] = v[i];
     }
   } else {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(tile + 1024 + 8 * P * r16);
 #pragma unroll
-    for (int j = 0; j < 4 * P; ++j) {
-      const int64_t at = (int64_t)P * b0 + j;
-      t.s[j] = 0.0f;
-      if (at < (int64_t)P * nb)
-        t.s[j] = Sk<SK>::e8 ? e8m0(srow[at]) : reinterpret_cast<const float*>(srow)[at];
+    for (int q = 0; q < P; ++q) {
+      const uint32_t b = __builtin_amdgcn_alignbyte(w[q + 1], w[q], shift);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)   // 2^(byte - 127)
+        s[4 * q + i] = __builtin_ldexpf(1.0f, (int)__builtin_amdgcn_ubfe(b, 8 * i, 8) - 127);
     }
   }
 }
 
-// Transposes the 4 x 4 words that lanes l, l + 16, l + 32, l + 48 hold: lane
-// group g then holds word g of blocks 0..3.
-__device__ __forceinline__ void turn4(u32x4& c) {
-  const u32x2 a = __builtin_amdgcn_permlane32_swap(c[0], c[2], false, false);
-  const u32x2 b = __builtin_amdgcn_permlane32_swap(c[1], c[3], false, false);
-  const u32x2 x = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-  const u32x2 y = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-  c = u32x4{x[0], x[1], y[0], y[1]};
+// --- activations in LDS ---------------------------------------------------------
+// Row i, 32 bytes per 8 elements: the upper bf16 pieces and then the lower ones;
+// the 16-byte chunks of a row are exchanged by its number, so that 16 rows read
+// at one place fall on all banks (row_bytes is a multiple of 16 chunks).
+__device__ __forceinline__ uint32_t act_chunk(int row, int row_bytes, int chunk) {
+  return (uint32_t)(row * row_bytes + 16 * (chunk ^ (row & 15)));
 }
 
-// Adds four blocks of NM weight tiles against TT 16-token tiles.  act[tt]:
-// this lane's token row (null: no token), at K element 0: 32 bytes per
-// 8 elements, the upper bf16 pieces and then the lower ones.
-template <int GRID, int SK, int NM, int TT>
-__device__ __forceinline__ void add_blocks(f32x4 (&acc)[NM][TT], Tile<SK> (&w)[NM],
-                                           const uint8_t* const (&act)[TT], int b0, int nb, int g) {
+// One step of both tiles against TT tiles of 16 tokens.  acts: LDS; arow[t]:
+// this lane's row of token tile t; blk0: block of acts' first column.
+template <int GRID, int SK, int TT>
+__device__ __forceinline__ void add_step(f32x4 (&acc)[2][TT], const uint8_t* ring,
+                                         const TileSource (&src)[2], const uint8_t* acts,
+                                         const int (&arow)[TT], int row_bytes, int blk0, int step,
+                                         int nb, int lane) {
   constexpr int P = Sk<SK>::per;
+  const int g = lane >> 4, r16 = lane & 15;
+  uint32_t code[2][4];
+  float s[2][4 * P];
 #pragma unroll
-  for (int m = 0; m < NM; ++m) turn4(w[m].codes);
+  for (int m = 0; m < 2; ++m) {
+    const uint8_t* t = ring + m * kTileBytes;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      code[m][j] = *reinterpret_cast<const uint32_t*>(t + 64 * r16 + 16 * (j ^ (r16 >> 2)) + 4 * g);
+    read_scales<SK>(t, src[m].shift, r16, s[m]);
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    if (b0 + j >= nb) break;
+    if (4 * step + j >= nb) break;
+    const int c = 8 * (4 * step + j - blk0) + 2 * g;
     bf16x8 hi[TT], lo[TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-      u32x4 a = {0, 0, 0, 0}, b = {0, 0, 0, 0};
-      if (act[t]) {
-        const u32x4* p = reinterpret_cast<const u32x4*>(act[t] + 128 * (int64_t)(b0 + j) + 32 * g);
-        a = p[0];
-        b = p[1];
-      }
-      hi[t] = __builtin_bit_cast(bf16x8, a);
-      lo[t] = __builtin_bit_cast(bf16x8, b);
+      hi[t] = *reinterpret_cast<const bf16x8*>(acts + act_chunk(arow[t], row_bytes, c));
+      lo[t] = *reinterpret_cast<const bf16x8*>(acts + act_chunk(arow[t], row_bytes, c + 1));
     }
 #pragma unroll
-    for (int m = 0; m < NM; ++m) {
-      const u32x4 lv = levels8<GRID>(w[m].codes[j]);
+    for (int m = 0; m < 2; ++m) {
+      const u32x4 lv = levels8<GRID>(code[m][j]);
 #pragma unroll
       for (int q = 0; q < P; ++q) {
         u32x4 l = lv;
@@ -202,17 +246,84 @@ __device__ __forceinline__ void add_blocks(f32x4 (&acc)[NM][TT], Tile<SK> (&w)[N
           for (int i = 0; i < 4; ++i) l[i] &= keep;
         }
         const bf16x8 b = __builtin_bit_cast(bf16x8, l);
-        const float s = w[m].s[P * j + q];
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-          f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
-          c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[t], b, c, 0, 0, 0);
-          c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[t], b, c, 0, 0, 0);
+          f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+          x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[t], b, x, 0, 0, 0);
+          x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[t], b, x, 0, 0, 0);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[m][t][r] = __builtin_fmaf(c[r], s, acc[m][t][r]);
+          for (int r = 0; r < 4; ++r)
+            acc[m][t][r] = __builtin_fmaf(x[r], s[m][P * j + q], acc[m][t][r]);
         }
       }
     }
+  }
+}
+
+// LDS address of a pointer into LDS.
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)p;
+}
+
+// acc += the product over K of a workgroup's two tiles per wave (src) with its
+// tokens.  The waves are PT tile pairs times KS shares of K: a wave takes steps
+// ks, ks + KS, ..  fill(first block, blocks) puts the activations of a range of
+// K into `acts`, one range after another (what 64 KB hold).
+template <int GRID, int SK, int TT, int KS, class Fill>
+__device__ __forceinline__ void product(f32x4 (&acc)[2][TT], const TileSource (&src)[2],
+                                        uint8_t* acts, uint8_t* ring, const int (&arow)[TT],
+                                        int row_bytes, int range, int nb, int ks, Fill fill) {
+  const int lane = threadIdx.x & 63;
+  const int steps = (nb + 3) / 4;
+  const uint32_t ring0 = lds_addr(ring);
+  // the i-th step of this wave; past the last one the copies give zeros or
+  // bytes that nothing reads, and keep the count of loads in flight
+  auto copy = [&](int i) {
+    const uint32_t to = ring0 + (uint32_t)(i % kRing) * kStepBytes;
+    int step = ks + i * KS;
+    if (step >= steps) step = steps - 1;
+#pragma unroll
+    for (int m = 0; m < 2; ++m) copy_tile<SK>(src[m], to + m * kTileBytes, step, lane);
+  };
+#pragma unroll
+  for (int i = 0; i < kRing - 1; ++i) copy(i);
+  int i = 0;
+  for (int b0 = 0; b0 < nb; b0 += range) {
+    const int bn = nb - b0 < range ? nb - b0 : range;
+    if (b0) __syncthreads();   // everyone has read the range before
+    fill(b0, bn);
+    __syncthreads();
+    for (; ks + i * KS < (b0 + bn + 3) / 4; ++i) {
+      copy(i + kRing - 1);
+      wait_vmcnt<(kRing - 1) * kCopies>();   // step i is there; later ones need not be
+      add_step<GRID, SK, TT>(acc, ring + (i % kRing) * kStepBytes, src, acts, arow, row_bytes, b0,
+                             ks + i * KS, nb, lane);
+      // the ring's next copy overwrites what was just read
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    }
+  }
+  wait_vmcnt<0>();   // nothing may arrive after the ring is used for something else
+  __syncthreads();
+}
+
+// The shares of K added in order: part[matrix][token][RUN columns].
+template <int TT, int KS, int RUN>
+__device__ __forceinline__ void join_shares(const f32x4 (&acc)[2][TT], float* part, int pt, int ks) {
+  const int lane = threadIdx.x & 63, g = lane >> 4, r16 = lane & 15;
+  constexpr int ROWS = TT * 16;
+  for (int s = 0; s < KS; ++s) {
+    if (ks == s) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            float* d = part + (q * ROWS + t * 16 + 4 * g + r) * RUN + pt * 16 + r16;
+            *d = s == 0 ? acc[q][t][r] : *d + acc[q][t][r];
+          }
+    }
+    __syncthreads();
   }
 }
 
@@ -249,227 +360,243 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
 }
 
 // --- routing and the rotation of x -----------------------------------------------
-__global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeLaunch p) {
-  const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 63;
-  if (t == 0) {
-    for (int i = tid; i < p.E; i += kRouteThreads) p.count[i] = 0;
-    for (int64_t i = tid; i < p.H / 16; i += kRouteThreads) p.done[i] = 0;
+// One wave: the choices of token t into ids[r], share[r], r < k (-1: none).
+__device__ __forceinline__ void route_token(const MoeLaunch& p, int t, int* ids, float* shares) {
+  const int lane = threadIdx.x & 63;
+  constexpr int Q = kMoeMaxExperts / 64;   // expert lane + 64 q in register q
+  uint32_t key[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    const int e = lane + 64 * q;
+    key[q] = e < p.E ? logit_key(p.logits[(int64_t)t * p.ldl + e]) : 0u;
   }
-  if (tid < 64) {
-    // expert lane + 64 q in register q
-    constexpr int Q = kMoeMaxExperts / 64;
-    uint32_t key[Q];
+  uint32_t top = 0;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const int e = lane + 64 * q;
-      key[q] = e < p.E ? logit_key(p.logits[(int64_t)t * p.ldl + e]) : 0u;
-    }
-    uint32_t top = 0;
+  for (int q = 0; q < Q; ++q) top = key[q] > top ? key[q] : top;
+  top = wave_max(top);
+  const float first = key_logit(top);
+  float den = 0.0f;
+  if (!p.renorm) {
 #pragma unroll
-    for (int q = 0; q < Q; ++q) top = key[q] > top ? key[q] : top;
-    top = wave_max(top);
-    const float first = key_logit(top);
-    float den = 0.0f;
-    if (!p.renorm) {
+    for (int q = 0; q < Q; ++q)
+      if (key[q]) den += __builtin_amdgcn_exp2f((key_logit(key[q]) - first) * kLog2e);
 #pragma unroll
-      for (int q = 0; q < Q; ++q)
-        if (key[q]) den += __builtin_amdgcn_exp2f((key_logit(key[q]) - first) * kLog2e);
+    for (int m = 32; m > 0; m >>= 1) den += __shfl_xor(den, m);
+  }
+  int id = -1;   // lane r: the r-th choice and its share
+  float share = 0.0f;
+  for (int r = 0; r < p.k; ++r) {
+    uint32_t best = 0;
 #pragma unroll
-      for (int m = 32; m > 0; m >>= 1) den += __shfl_xor(den, m);
-    }
-    int id = -1;        // lane r: the r-th choice and its share
-    float share = 0.0f;
-    for (int r = 0; r < p.k; ++r) {
-      uint32_t best = 0;
+    for (int q = 0; q < Q; ++q) best = key[q] > best ? key[q] : best;
+    best = wave_max(best);
+    if (best == 0) break;
+    int e = -1;
 #pragma unroll
-      for (int q = 0; q < Q; ++q) best = key[q] > best ? key[q] : best;
-      best = wave_max(best);
-      if (best == 0) break;
-      int e = -1;
-#pragma unroll
-      for (int q = 0; q < Q; ++q) {   // ascending: the lowest index of a tie
-        const uint64_t has = __ballot(key[q] == best);
-        if (e < 0 && has) {
-          const int l = __builtin_ctzll(has);
-          e = l + 64 * q;
-          if (lane == l) key[q] = 0;
-        }
+    for (int q = 0; q < Q; ++q) {   // ascending: the lowest index of a tie
+      const uint64_t has = __ballot(key[q] == best);
+      if (e < 0 && has) {
+        const int l = __builtin_ctzll(has);
+        e = l + 64 * q;
+        if (lane == l) key[q] = 0;
       }
-      const float x = __builtin_amdgcn_exp2f((key_logit(best) - first) * kLog2e);
-      if (p.renorm) den += x;
-      if (lane == r) { id = e; share = x; }
     }
-    if (lane < p.k) {
-      p.ids[(int64_t)t * p.k + lane] = id;
-      p.share[(int64_t)t * p.k + lane] = id >= 0 ? share / den : 0.0f;
+    const float x = __builtin_amdgcn_exp2f((key_logit(best) - first) * kLog2e);
+    if (p.renorm) den += x;
+    if (lane == r) {
+      id = e;
+      share = x;
     }
   }
-  // rotation, 8 elements per thread: y = c_n (x S) H, split into two bf16 pieces
-  const int n = p.nx;
-  const float cn = p.cnx;
-  const int64_t groups = p.H / 8;
-  for (int64_t i0 = 0; i0 < groups; i0 += kRouteThreads) {
-    const int64_t i = i0 + tid;
-    float v[8] = {};
-    if (i < groups) {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(p.x + (int64_t)t * p.ldx + 8 * i);
-      const int o = (int)(8 * i) & 127;
-      const uint32_t sg = p.sign_x[o >> 5] >> (o & 31);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t b = (j & 1) ? w[j >> 1] & 0xFFFF0000u : w[j >> 1] << 16;
-        v[j] = __uint_as_float(b ^ ((sg >> j) << 31));
-      }
-    }
-#pragma unroll
-    for (int h = 1; h < 8; h <<= 1) {
-      if (n > h) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          if (!(j & h)) {
-            const float a = v[j], b = v[j + h];
-            v[j] = a + b;
-            v[j + h] = a - b;
-          }
-      }
-    }
-    for (int h = 8; h < n; h <<= 1) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float o = __shfl_xor(v[j], h >> 3);
-        v[j] = (lane & (h >> 3)) ? o - v[j] : v[j] + o;
-      }
-    }
-    if (i < groups) {
-      u32x4 hi, lo;
-      constexpr int order[8] = {0, 2, 4, 6, 1, 3, 5, 7};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float a = v[order[2 * j]] * cn, b = v[order[2 * j + 1]] * cn;
-        hi[j] = pack_bf16(a, b);
-        lo[j] = pack_bf16(a - __uint_as_float(hi[j] << 16),
-                          b - __uint_as_float(hi[j] & 0xFFFF0000u));
-      }
-      u32x4* o = reinterpret_cast<u32x4*>(p.xr + ((int64_t)t * p.H + 8 * i) * 4);
-      o[0] = hi;
-      o[1] = lo;
-    }
+  if (lane < p.k) {
+    ids[lane] = id;
+    shares[lane] = id >= 0 ? share / den : 0.0f;
   }
 }
 
-// --- gate and up products, activation ---------------------------------------------
-// NF: columns of the intermediate that a workgroup computes, max(32, n).
-template <int GRID, int SK, int NF, int TT>
-__device__ __forceinline__ void moe_up_body(const MoeLaunch& p, int e, int f0, int m,
-                                            const int* tok, const float* share, float* part) {
-  constexpr int PT = NF / 16, KS = kWaves / PT;   // 16-row pairs, shares of K
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int pt = wave % PT, ks = wave / PT, g = lane >> 4, r16 = lane & 15;
-  const int nb = (int)(p.H / 32);
-  const int64_t row = (int64_t)e * p.F + f0 + pt * 16 + r16;
-  const uint8_t* crow[2];
-  const uint8_t* srow[2];
+// One butterfly of eight values with the lane whose number differs in bit M:
+// the lower lane gets the sum, the upper one the difference.
+template <int M>
+__device__ __forceinline__ void butterfly(float (&v)[8], int lane) {
+  const float sign = (lane & M) ? -1.0f : 1.0f;
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const MoeWeight& w = q ? p.wu : p.wg;
-    crow[q] = w.codes + row * (p.H / 2);
-    srow[q] = w.scales + (row >> w.row_shift) * w.scale_pitch;
+  for (int j = 0; j < 8; ++j) {
+    int o = (int)__float_as_uint(v[j]);
+    if constexpr (M == 1) o = __builtin_amdgcn_mov_dpp(o, 0xB1, 0xF, 0xF, true);
+    if constexpr (M == 2) o = __builtin_amdgcn_mov_dpp(o, 0x4E, 0xF, 0xF, true);
+    if constexpr (M == 4)   // 7 - l, then 3 - l inside four
+      o = __builtin_amdgcn_mov_dpp(__builtin_amdgcn_mov_dpp(o, 0x141, 0xF, 0xF, true), 0x1B, 0xF,
+                                   0xF, true);
+    if constexpr (M == 8) o = __builtin_amdgcn_mov_dpp(o, 0x128, 0xF, 0xF, true);   // l + 8 of 16
+    v[j] = __builtin_fmaf(sign, v[j], __uint_as_float((uint32_t)o));   // exact product
   }
-  const uint8_t* act[TT];
+}
+
+// Eight neighbouring elements of a row rotated, y = c_n (v S) H, and split into
+// two bf16 pieces in the order of the weights' codebook.  i: which eight of the
+// row; every lane of the wave takes part, and lane l holds an i that is
+// congruent to l modulo 64, so a chunk's neighbours are neighbouring lanes.
+__device__ __forceinline__ void rotate8(float (&v)[8], int64_t i, int n, float cn,
+                                        const uint32_t (&signs)[4], int grid, u32x4& hi, u32x4& lo) {
+  const int lane = threadIdx.x & 63;
+  const int o = (int)(8 * i) & 127;
+  const uint32_t sg = signs[o >> 5] >> (o & 31);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    v[j] = __uint_as_float(__float_as_uint(v[j]) ^ ((sg >> j) << 31));
+#pragma unroll
+  for (int h = 1; h < 8; h <<= 1) {
+    if (n > h) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (!(j & h)) {
+          const float a = v[j], b = v[j + h];
+          v[j] = a + b;
+          v[j + h] = a - b;
+        }
+    }
+  }
+  if (n > 8) butterfly<1>(v, lane);
+  if (n > 16) butterfly<2>(v, lane);
+  if (n > 32) butterfly<4>(v, lane);
+  if (n > 64) butterfly<8>(v, lane);
+  constexpr int order[8] = {0, 2, 4, 6, 1, 3, 5, 7};
+  const bool natural = grid == 2;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float a = (natural ? v[2 * j] : v[order[2 * j]]) * cn;
+    const float b = (natural ? v[2 * j + 1] : v[order[2 * j + 1]]) * cn;
+    hi[j] = pack_bf16(a, b);
+    lo[j] = pack_bf16(a - __uint_as_float(hi[j] << 16), b - __uint_as_float(hi[j] & 0xFFFF0000u));
+  }
+}
+
+__device__ __forceinline__ void load_x8(const uint16_t* x, bool in, int64_t i, float (&v)[8]) {
+  u32x4 w = {0, 0, 0, 0};
+  if (in) w = *reinterpret_cast<const u32x4*>(x + 8 * i);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(w[j] << 16);
+    v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+}
+
+// Routing and rotation once for all: token blockIdx.x, 2048 elements of it.
+__global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeLaunch p) {
+  const int64_t t = blockIdx.x, i = (int64_t)blockIdx.y * kRouteThreads + threadIdx.x;
+  if (blockIdx.y == 0 && threadIdx.x < 64)
+    route_token(p, (int)t, p.ids + t * p.k, p.share + t * p.k);
+  const bool in = i < p.H / 8;
+  float v[8];
+  load_x8(p.x + t * p.ldx, in, i, v);
+  u32x4 hi, lo;
+  rotate8(v, i, p.nx, p.cnx, p.sign_x, p.wg.grid, hi, lo);
+  if (in) {
+    u32x4* o = reinterpret_cast<u32x4*>(p.xr + t * p.H * 4 + 32 * i);
+    o[0] = hi;
+    o[1] = lo;
+  }
+}
+
+// Bytes of a row of x in LDS where all of K is there.
+__host__ __device__ inline int fused_row(int64_t H) { return (int)((H * 4 + 255) / 256 * 256); }
+
+// Blocks of 32 columns of TT 16-token tiles that fit the activations' LDS.
+template <int TT> constexpr int range_of() { return kActBytes / (TT * 16 * 128); }
+
+// --- gate and up products, activation ---------------------------------------------
+// NF: columns of the intermediate that a workgroup computes, 16 per pair of a
+// gate and an up tile.  FUSED: x is in LDS already, row t for token t.
+template <int GRID, int SK, int NF, int TT, bool FUSED>
+__device__ __forceinline__ void moe_up_body(const MoeLaunch& p, int slot, int e, int f0, int m,
+                                            const int* tok, const float* share, uint8_t* lds) {
+  constexpr int PT = NF / 16, KS = kWaves / PT;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int pt = wave % PT, ks = wave / PT, r16 = lane & 15;
+  const int nb = (int)(p.H / 32);
+  const int64_t row0 = (int64_t)e * p.F + f0 + pt * 16;
+  const TileSource src[2] = {tile_source<SK>(p.wg, row0, p.H, lane),
+                             tile_source<SK>(p.wu, row0, p.H, lane)};
+  uint8_t* acts = lds;
+  uint8_t* ring = lds + kActBytes + wave * kRing * kStepBytes;
+  int arow[TT];
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
-    const int i = t * 16 + r16;
-    act[t] = i < m ? p.xr + (int64_t)tok[i] * p.H * 4 : nullptr;
+    const int i = t * 16 + r16;   // rows past the tokens give rows that nobody takes
+    arow[t] = i < m ? (FUSED ? tok[i] : i) : 0;
   }
   f32x4 acc[2][TT];
 #pragma unroll
   for (int q = 0; q < 2; ++q)
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[q][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-  Tile<SK> cur[2], nxt[2];
-#pragma unroll
-  for (int q = 0; q < 2; ++q) load_tile<SK>(cur[q], crow[q], srow[q], 4 * ks < nb ? 4 * ks : 0, nb, g);
-  for (int b0 = 4 * ks; b0 < nb; b0 += 4 * KS) {
-    const int bn = b0 + 4 * KS < nb ? b0 + 4 * KS : b0;   // past the end: this one again, unused
-#pragma unroll
-    for (int q = 0; q < 2; ++q) load_tile<SK>(nxt[q], crow[q], srow[q], bn, nb, g);
-    add_blocks<GRID, SK, 2, TT>(acc, cur, act, b0, nb, g);
-#pragma unroll
-    for (int q = 0; q < 2; ++q) cur[q] = nxt[q];
+  if constexpr (FUSED) {
+    product<GRID, SK, TT, KS>(acc, src, acts, ring, arow, fused_row(p.H), nb, nb, ks,
+                              [](int, int) {});
+  } else {
+    constexpr int range = range_of<TT>();
+    const sgpr4 xr = rsrc4(p.xr, (uint32_t)(p.T * p.H * 4));
+    const uint32_t to = lds_addr(acts);
+    product<GRID, SK, TT, KS>(acc, src, acts, ring, arow, range * 128, range, nb, ks, [&](int b0, int) {
+      // rows of 128 range bytes, 1 KB per copy; what lies past K is not read
+      constexpr int per_row = range * 128 / 1024;
+      for (int c = wave; c < m * per_row; c += kWaves) {
+        const int i = c / per_row, part = c % per_row;
+        lds_load16(to + (uint32_t)c * 1024u, xr,
+                   (uint32_t)tok[i] * (uint32_t)(p.H * 4) + (uint32_t)b0 * 128u +
+                       16u * (uint32_t)((part * 64 + lane) ^ (i & 15)), 0);
+      }
+      wait_vmcnt<0>();
+    });
   }
-
-  // the shares of K added in order: part[matrix][token][column]
+  float* part = reinterpret_cast<float*>(lds);
+  join_shares<TT, KS, NF>(acc, part, pt, ks);
   constexpr int ROWS = TT * 16;
-  for (int s = 0; s < KS; ++s) {
-    if (ks == s) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-#pragma unroll
-        for (int t = 0; t < TT; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            float* d = part + (q * ROWS + t * 16 + 4 * g + r) * NF + pt * 16 + r16;
-            *d = s == 0 ? acc[q][t][r] : *d + acc[q][t][r];
-          }
-    }
-    __syncthreads();
-  }
-
-  // h = p act(gate) up, rotated along the run, as two bf16 pieces; 128
-  // neighbouring elements of [token][column] per wave and pass
-  const int n = p.nh, total = m * NF;
-  for (int i0 = wave * 128; i0 < total; i0 += kWaves * 128) {
-    float v[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int i = i0 + 64 * q + lane;
-      v[q] = 0.0f;
-      if (i < total) {
-        const float a = part[i] * p.wg.factor, b = part[ROWS * NF + i] * p.wu.factor;
-        const float s = p.act == UFP4_ACT_GELU ? activation<1>(a) : activation<0>(a);
-        const int o = (f0 + i % NF) & 127;
-        v[q] = s * b * share[i / NF];
-        v[q] = __uint_as_float(__float_as_uint(v[q]) ^ ((p.sign_h[o >> 5] >> (o & 31)) << 31));
-      }
-    }
-    for (int h = 1; h < n && h < 64; h <<= 1) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const float o = __shfl_xor(v[q], h);
-        v[q] = (lane & h) ? o - v[q] : v[q] + o;
-      }
-    }
-    if (n == 128) {
-      const float a = v[0], b = v[1];
-      v[0] = a + b;
-      v[1] = a - b;
-    }
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int i = i0 + 64 * q + lane;
-      if (i < total) {
-        const int f = f0 + i % NF;
-        const float y = v[q] * p.cnh;
-        const uint32_t hi = pack_bf16(y, 0.0f) & 0xFFFFu;
-        const uint32_t lo = pack_bf16(y - __uint_as_float(hi << 16), 0.0f);
-        uint16_t* o = reinterpret_cast<uint16_t*>(
-                          p.hr + (((int64_t)e * p.T + i / NF) * p.F + (f & ~7)) * 4) + slot8(f & 7);
-        o[0] = (uint16_t)hi;
-        o[8] = (uint16_t)lo;
-      }
-    }
+  for (int i = tid; i < m * NF; i += kThreads) {
+    const float a = part[i] * p.wg.factor, b = part[ROWS * NF + i] * p.wu.factor;
+    const float s = p.act == UFP4_ACT_GELU ? activation<1>(a) : activation<0>(a);
+    p.h[((int64_t)slot * p.T + i / NF) * p.F + f0 + i % NF] = s * b * share[i / NF];
   }
 }
 
-template <int GRID, int SK, int NF>
+// FUSED: routing and rotation here, for a few tokens.  WIDE: an expert may have
+// more than 16 tokens.
+enum { kFused = 0, kNarrow = 1, kWide = 2 };
+template <int GRID, int SK, int NF, int MODE>
 __global__ __launch_bounds__(kThreads) void k_moe_up(MoeLaunch p) {
+  constexpr bool FUSED = MODE == kFused;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ int tok[kMoeMaxTokens];
   __shared__ float share[kMoeMaxTokens];
+  __shared__ int ids_here[FUSED ? kMoeFusedTokens * kMoeMaxChoices : 1];
+  __shared__ float share_here[FUSED ? kMoeFusedTokens * kMoeMaxChoices : 1];
   __shared__ int found[2];   // expert, tokens
-  const int tid = threadIdx.x, lane = tid & 63;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int fc = blockIdx.x, slot = blockIdx.y;
+  const int* ids = p.ids;
+  const float* shares = p.share;
+  if constexpr (FUSED) {
+    for (int t = wave; t < p.T; t += kWaves)
+      route_token(p, t, ids_here + t * p.k, share_here + t * p.k);
+    // the waves that route take the last part of x
+    const int bytes = fused_row(p.H);
+    for (int t = 0; t < p.T; ++t)
+      for (int64_t i0 = 0; i0 < p.H / 8; i0 += kThreads) {
+        const int64_t i = i0 + (kWaves - 1 - wave) * 64 + lane;
+        const bool in = i < p.H / 8;
+        float v[8];
+        load_x8(p.x + t * p.ldx, in, i, v);
+        u32x4 hi, lo;
+        rotate8(v, i, p.nx, p.cnx, p.sign_x, p.wg.grid, hi, lo);
+        if (in) {
+          *reinterpret_cast<u32x4*>(lds + act_chunk(t, bytes, (int)(2 * i))) = hi;
+          *reinterpret_cast<u32x4*>(lds + act_chunk(t, bytes, (int)(2 * i + 1))) = lo;
+        }
+      }
+    ids = ids_here;
+    shares = share_here;
+    __syncthreads();
+  }
   if (tid < 64) {
     const int pairs = (int)(p.T * p.k);
     // by_pair: slot s stands for the s-th choice, unless the same expert
@@ -477,186 +604,185 @@ __global__ __launch_bounds__(kThreads) void k_moe_up(MoeLaunch p) {
     int e = slot;
     bool mine = true;
     if (p.by_pair) {
-      e = p.ids[slot];
+      e = ids[slot];
       if (e < 0) {
         mine = false;
       } else {
         bool before = false;
         for (int i0 = 0; i0 < slot; i0 += 64) {
           const int i = i0 + lane;
-          before |= __any(i < slot && p.ids[i < slot ? i : 0] == e);
+          before |= __any(i < slot && ids[i < slot ? i : 0] == e);
         }
         mine = !before;
       }
     }
     int m = 0;
-    if (mine) {
-      for (int i0 = 0; i0 < pairs; i0 += 64) {
-        const int i = i0 + lane;
-        const bool hit = i < pairs && p.ids[i < pairs ? i : 0] == e;
-        const uint64_t mask = __ballot(hit);
-        if (hit) {
-          const int at = m + __builtin_popcountll(mask & (((uint64_t)1 << lane) - 1));
-          tok[at] = i / p.k;
-          share[at] = p.share[i];
-        }
-        m += __builtin_popcountll(mask);
+    for (int i0 = 0; i0 < pairs; i0 += 64) {
+      const int i = i0 + lane;
+      const int id = ids[i < pairs ? i : 0];
+      const bool hit = mine && i < pairs && id == e;
+      const uint64_t mask = __ballot(hit);
+      if (hit) {
+        const int at = m + __builtin_popcountll(mask & (((uint64_t)1 << lane) - 1));
+        tok[at] = i / p.k;
+        share[at] = shares[i];
+        if (fc == 0) p.place[i] = slot * (int)p.T + at;   // for the join
       }
+      if (fc == 0 && slot == 0 && i < pairs && id < 0) p.place[i] = -1;
+      m += __builtin_popcountll(mask);
     }
     if (lane == 0) {
       found[0] = e;
       found[1] = m;
+      if (fc == 0) {   // for the down product
+        p.expert[slot] = e;
+        p.count[slot] = m;
+      }
     }
   }
   __syncthreads();
-  const int e = found[0], m = found[1];
+  const int e = __builtin_amdgcn_readfirstlane(found[0]);
+  const int m = __builtin_amdgcn_readfirstlane(found[1]);
   if (m == 0) return;
-  if (fc == 0) {   // for the down product
-    if (tid < m) p.list[(int64_t)e * p.T + tid] = tok[tid];
-    if (tid == 0) p.count[e] = m;
+  auto body = [&](auto tt) {
+    moe_up_body<GRID, SK, NF, decltype(tt)::value, FUSED>(p, slot, e, fc * NF, m, tok, share, lds);
+  };
+  if (MODE != kWide || m <= 16) body(std::integral_constant<int, 1>{});
+  if constexpr (MODE == kWide) {
+    if (m > 16 && m <= 32) body(std::integral_constant<int, 2>{});
+    else if (m > 32) body(std::integral_constant<int, 4>{});
   }
-  float* part = reinterpret_cast<float*>(lds);
-  if (m <= 16) moe_up_body<GRID, SK, NF, 1>(p, e, fc * NF, m, tok, share, part);
-  else if (m <= 32) moe_up_body<GRID, SK, NF, 2>(p, e, fc * NF, m, tok, share, part);
-  else moe_up_body<GRID, SK, NF, 4>(p, e, fc * NF, m, tok, share, part);
 }
 
 // --- down product --------------------------------------------------------------------
-// A wave's run of (expert, 128 of F) items against one expert's tokens.
-template <int GRID, int SK, int TT>
-__device__ __forceinline__ void moe_down_run(const MoeLaunch& p, int e, int m, int s0, int s1,
-                                             int64_t col0, float* y) {
-  const int lane = threadIdx.x & 63, g = lane >> 4, r16 = lane & 15;
+// RUN: output columns per workgroup, 32 per pair of neighbouring tiles.
+template <int GRID, int SK, int RUN, int TT>
+__device__ __forceinline__ void moe_down_body(const MoeLaunch& p, int slot, int e, int m,
+                                              int64_t col0, uint8_t* lds) {
+  constexpr int PT = RUN / 32, KS = kWaves / PT;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int pt = wave % PT, ks = wave / PT, r16 = lane & 15;
   const int nb = (int)(p.F / 32);
-  const int64_t row = (int64_t)e * p.H + col0 + r16;
-  const uint8_t* crow = p.wd.codes + row * (p.F / 2);
-  const uint8_t* srow = p.wd.scales + (row >> p.wd.row_shift) * p.wd.scale_pitch;
-  const uint8_t* act[TT];
+  const int64_t row0 = (int64_t)e * p.H + col0 + pt * 16;   // and RUN / 2 further on
+  const TileSource src[2] = {tile_source<SK>(p.wd, row0, p.F, lane),
+                             tile_source<SK>(p.wd, row0 + RUN / 2, p.F, lane)};
+  uint8_t* acts = lds;
+  uint8_t* ring = lds + kActBytes + wave * kRing * kStepBytes;
+  int arow[TT];
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
     const int i = t * 16 + r16;
-    act[t] = i < m ? p.hr + ((int64_t)e * p.T + i) * p.F * 4 : nullptr;
+    arow[t] = i < m ? i : 0;
   }
-  f32x4 acc[1][TT];
+  f32x4 acc[2][TT];
 #pragma unroll
-  for (int t = 0; t < TT; ++t) acc[0][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  Tile<SK> cur[1], nxt[1];
-  load_tile<SK>(cur[0], crow, srow, 4 * s0, nb, g);
-  for (int s = s0; s < s1; ++s) {
-    load_tile<SK>(nxt[0], crow, srow, 4 * (s + 1 < s1 ? s + 1 : s), nb, g);
-    add_blocks<GRID, SK, 1, TT>(acc, cur, act, 4 * s, nb, g);
-    cur[0] = nxt[0];
-  }
+  for (int q = 0; q < 2; ++q)
 #pragma unroll
-  for (int t = 0; t < TT; ++t)
+    for (int t = 0; t < TT; ++t) acc[q][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  constexpr int range = range_of<TT>();
+  product<GRID, SK, TT, KS>(acc, src, acts, ring, arow, range * 128, range, nb, ks, [&](int b0, int bn) {
+    // one row after another, 64 times 8 neighbouring elements per wave
+    const int groups = 4 * bn, runs = (groups + 63) / 64;
+    for (int c = wave; c < m * runs; c += kWaves) {
+      const int row = c / runs, i = (c % runs) * 64 + lane;
+      float v[8] = {};
+      if (i < groups) {
+        const f32x4* h = reinterpret_cast<const f32x4*>(
+            p.h + ((int64_t)slot * p.T + row) * p.F + 32 * (int64_t)b0 + 8 * i);
+        const f32x4 a = h[0], b = h[1];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int i = t * 16 + 4 * g + r;
-      if (i < m) y[p.list[(int64_t)e * p.T + i] * 16 + r16] += acc[0][t][r];
+        for (int j = 0; j < 4; ++j) { v[j] = a[j]; v[4 + j] = b[j]; }
+      }
+      u32x4 hi, lo;
+      rotate8(v, 4 * (int64_t)b0 + i, p.nh, p.cnh, p.sign_h, p.wd.grid, hi, lo);
+      if (i < groups) {
+        *reinterpret_cast<u32x4*>(acts + act_chunk(row, range * 128, 2 * i)) = hi;
+        *reinterpret_cast<u32x4*>(acts + act_chunk(row, range * 128, 2 * i + 1)) = lo;
+      }
     }
+  });
+  float* part = reinterpret_cast<float*>(lds);
+  constexpr int HALF = RUN / 2, ROWS = TT * 16;
+  join_shares<TT, KS, HALF>(acc, part, pt, ks);
+  for (int i = tid; i < m * HALF; i += kThreads) {
+    float* o = p.partial + ((int64_t)slot * p.T + i / HALF) * p.H + col0 + i % HALF;
+    o[0] = part[i];
+    o[HALF] = part[ROWS * HALF + i];
+  }
 }
 
-template <int GRID, int SK>
+template <int GRID, int SK, int RUN, bool WIDE>
 __global__ __launch_bounds__(kThreads) void k_moe_down(MoeLaunch p) {
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];   // [wave][token][16]
-  __shared__ int active[kMoeMaxExperts];
-  __shared__ int tokens[kMoeMaxExperts];
-  __shared__ int nactive, last;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int tile = blockIdx.x, split = blockIdx.y, S = gridDim.y;
-  const int T = (int)p.T, cells = T * 16;
-  float* all = reinterpret_cast<float*>(lds);
-  for (int i = tid; i < kWaves * cells; i += kThreads) all[i] = 0.0f;
-  if (tid < 64) {
-    int n = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 64) {
-      const int e = e0 + lane;
-      const int m = e < p.E ? p.count[e] : 0;
-      const uint64_t mask = __ballot(m > 0);
-      if (m > 0) {
-        const int at = n + __builtin_popcountll(mask & (((uint64_t)1 << lane) - 1));
-        active[at] = e;
-        tokens[at] = m;
-      }
-      n += __builtin_popcountll(mask);
-    }
-    if (lane == 0) nactive = n;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int slot = blockIdx.y;
+  const int m = p.count[slot], e = p.expert[slot];
+  if (m == 0) return;
+  auto body = [&](auto tt) {
+    moe_down_body<GRID, SK, RUN, decltype(tt)::value>(p, slot, e, m, (int64_t)blockIdx.x * RUN, lds);
+  };
+  if (!WIDE || m <= 16) body(std::integral_constant<int, 1>{});
+  if constexpr (WIDE) {
+    if (m > 16 && m <= 32) body(std::integral_constant<int, 2>{});
+    else if (m > 32) body(std::integral_constant<int, 4>{});
   }
-  __syncthreads();
-  // items 0 .. n steps - 1 in equal runs over the splits' waves
-  const int steps = (int)((p.F + 127) / 128), items = nactive * steps;
-  const int parts = S * kWaves, me = split * kWaves + wave;
-  const int lo = (int)((int64_t)items * me / parts), hi = (int)((int64_t)items * (me + 1) / parts);
-  float* y = all + wave * cells;
-  for (int it = lo; it < hi;) {
-    const int a = it / steps, s0 = it - a * steps;
-    const int s1 = s0 + (hi - it) < steps ? s0 + (hi - it) : steps;
-    const int e = __builtin_amdgcn_readfirstlane(active[a]);
-    const int m = __builtin_amdgcn_readfirstlane(tokens[a]);
-    const int64_t col0 = (int64_t)tile * 16;
-    if (m <= 16) moe_down_run<GRID, SK, 1>(p, e, m, s0, s1, col0, y);
-    else if (m <= 32) moe_down_run<GRID, SK, 2>(p, e, m, s0, s1, col0, y);
-    else moe_down_run<GRID, SK, 4>(p, e, m, s0, s1, col0, y);
-    it += s1 - s0;
+}
+
+// y_t: its choices' sums in their order; two columns per thread.
+__global__ __launch_bounds__(kRouteThreads) void k_moe_join(MoeLaunch p) {
+  const int64_t col = 2 * ((int64_t)blockIdx.x * kRouteThreads + threadIdx.x), t = blockIdx.y;
+  if (col >= p.H) return;
+  f32x2 v = {0.0f, 0.0f};
+  for (int r = 0; r < p.k; ++r) {
+    const int at = p.place[t * p.k + r];
+    if (at >= 0) v += *reinterpret_cast<const f32x2*>(p.partial + (int64_t)at * p.H + col);
   }
-  __syncthreads();
-  // the waves' sums in order; several splits leave theirs in the workspace and
-  // the last workgroup of a tile to get there adds them, in order as well
-  for (int i = tid; i < cells; i += kThreads) {
-    float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += all[w * cells + i];
-    if (S == 1) all[i] = v;   // only this thread reads cell i of any wave
-    else p.partial[((int64_t)tile * S + split) * cells + i] = v;
-  }
-  if (S > 1) {
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) last = atomicAdd(&p.done[tile], 1) == S - 1;
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    for (int i = tid; i < cells; i += kThreads) {
-      float v = 0.0f;
-      for (int s = 0; s < S; ++s)
-        v += __hip_atomic_load(&p.partial[((int64_t)tile * S + s) * cells + i], __ATOMIC_RELAXED,
-                               __HIP_MEMORY_SCOPE_AGENT);
-      all[i] = v;
-    }
-  }
-  __syncthreads();
-  for (int i = tid; i < cells / 2; i += kThreads) {
-    const int t = i / 8, c = 2 * (i % 8);
-    *reinterpret_cast<uint32_t*>(p.y + (int64_t)t * p.ldy + (int64_t)tile * 16 + c) =
-        pack_bf16(all[t * 16 + c] * p.wd.factor, all[t * 16 + c + 1] * p.wd.factor);
-  }
+  *reinterpret_cast<uint32_t*>(p.y + t * p.ldy + col) =
+      pack_bf16(v[0] * p.wd.factor, v[1] * p.wd.factor);
 }
 
 template <int GRID, int SK, int NF>
 hipError_t launch_up_n(const MoeLaunch& p, hipStream_t s) {
-  const int tt = p.T <= 16 ? 1 : p.T <= 32 ? 2 : 4;
-  const int bytes = 2 * tt * 16 * NF * 4;
-  static std::atomic<uint64_t> lds_set{0};
-  const hipError_t e = set_lds_limit((const void*)k_moe_up<GRID, SK, NF>, 2 * 64 * NF * 4, lds_set);
-  if (e != hipSuccess) return e;
-  const unsigned slots = (unsigned)(p.by_pair ? p.T * p.k : p.E);
-  hipLaunchKernelGGL((k_moe_up<GRID, SK, NF>), dim3((unsigned)(p.F / NF), slots), dim3(kThreads),
-                     bytes, s, p);
-  return hipGetLastError();
+  const dim3 grid((unsigned)(p.F / NF), (unsigned)p.slots);
+  auto go = [&](auto mode) {
+    constexpr int MODE = decltype(mode)::value;
+    static std::atomic<uint64_t> lds_set{0};
+    const hipError_t e = set_lds_limit((const void*)k_moe_up<GRID, SK, NF, MODE>, kLdsBytes, lds_set);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_moe_up<GRID, SK, NF, MODE>), grid, dim3(kThreads), kLdsBytes, s, p);
+    return hipGetLastError();
+  };
+  if (p.fused) return go(std::integral_constant<int, kFused>{});
+  return p.T <= 16 ? go(std::integral_constant<int, kNarrow>{})
+                   : go(std::integral_constant<int, kWide>{});
+}
+
+template <int GRID, int SK, int RUN>
+hipError_t launch_down_n(const MoeLaunch& p, hipStream_t s) {
+  const dim3 grid((unsigned)(p.H / RUN), (unsigned)p.slots);
+  auto go = [&](auto wide) {
+    constexpr bool WIDE = decltype(wide)::value;
+    static std::atomic<uint64_t> lds_set{0};
+    const hipError_t e =
+        set_lds_limit((const void*)k_moe_down<GRID, SK, RUN, WIDE>, kLdsBytes, lds_set);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_moe_down<GRID, SK, RUN, WIDE>), grid, dim3(kThreads), kLdsBytes, s, p);
+    return hipGetLastError();
+  };
+  return p.T <= 16 ? go(std::false_type{}) : go(std::true_type{});
 }
 
 template <int GRID, int SK>
 hipError_t launch_up(const MoeLaunch& p, hipStream_t s) {
-  if (p.nh <= 32) return launch_up_n<GRID, SK, 32>(p, s);
-  if (p.nh == 64) return launch_up_n<GRID, SK, 64>(p, s);
+  if (p.run_up == 32) return launch_up_n<GRID, SK, 32>(p, s);
+  if (p.run_up == 64) return launch_up_n<GRID, SK, 64>(p, s);
   return launch_up_n<GRID, SK, 128>(p, s);
 }
 
 template <int GRID, int SK>
 hipError_t launch_down(const MoeLaunch& p, hipStream_t s) {
-  hipLaunchKernelGGL((k_moe_down<GRID, SK>), dim3((unsigned)(p.H / 16), (unsigned)p.splits),
-                     dim3(kThreads), kWaves * (size_t)p.T * 16 * 4, s, p);
-  return hipGetLastError();
+  if (p.run_down == 32) return launch_down_n<GRID, SK, 32>(p, s);
+  if (p.run_down == 64) return launch_down_n<GRID, SK, 64>(p, s);
+  return launch_down_n<GRID, SK, 128>(p, s);
 }
 
 template <typename F>
@@ -681,44 +807,68 @@ int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
 
+// Columns per workgroup, of `cols`: one workgroup fills a compute unit, so the
+// width whose last round of workgroups leaves least idle; of equals the widest,
+// whose waves share the activations most.
+int32_t run_width(int64_t cols, int64_t slots) {
+  constexpr int64_t kUnits = 256;
+  int32_t best = 32;
+  int64_t least = INT64_MAX;
+  for (int32_t w = 32; w <= 128; w *= 2) {
+    if (cols % w) break;
+    const int64_t rounds = (cols / w * slots + kUnits - 1) / kUnits;
+    if (rounds * w <= least) {
+      least = rounds * w;
+      best = w;
+    }
+  }
+  return best;
+}
+
 // Workspace parts, in this order, each 256-byte aligned.
 int64_t moe_plan(MoeLaunch& p, uint8_t* ws) {
-  // the down product: splits of the experts until two workgroups per compute
-  // unit are there, each wave at least two 128-element steps
-  const int64_t met = p.T * p.k < p.E ? p.T * p.k : p.E;
-  const int64_t items = met * ((p.F + 127) / 128);
-  int64_t splits = 512 / (p.H / 16 > 0 ? p.H / 16 : 1);
-  if (splits > items / (2 * kWaves)) splits = items / (2 * kWaves);
-  p.splits = (int32_t)(splits < 1 ? 1 : splits > 16 ? 16 : splits);
-  p.by_pair = p.T * p.k < p.E;
+  const int64_t pairs = p.T * p.k;
+  p.by_pair = pairs < p.E;
+  p.slots = (int32_t)(p.by_pair ? pairs : p.E);
+  p.fused = p.T <= kMoeFusedTokens && p.T * fused_row(p.H) <= kActBytes;
+  p.run_up = run_width(p.F, p.slots);
+  p.run_down = run_width(p.H, p.slots);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     uint8_t* q = ws ? ws + at : nullptr;
     at += up256(bytes);
     return q;
   };
-  p.ids = reinterpret_cast<int*>(take(4 * p.T * p.k));
-  p.share = reinterpret_cast<float*>(take(4 * p.T * p.k));
-  p.count = reinterpret_cast<int*>(take(4 * p.E));
-  p.list = reinterpret_cast<int*>(take(4 * p.E * p.T));
-  p.done = reinterpret_cast<int*>(take(4 * (p.H / 16)));
-  p.xr = take(4 * p.T * p.H);
-  p.hr = take(4 * (int64_t)p.E * p.T * p.F);
-  p.partial = reinterpret_cast<float*>(take(p.splits > 1 ? 4 * p.splits * p.T * p.H : 0));
+  p.ids = reinterpret_cast<int*>(take(p.fused ? 0 : 4 * pairs));
+  p.share = reinterpret_cast<float*>(take(p.fused ? 0 : 4 * pairs));
+  p.expert = reinterpret_cast<int*>(take(4 * p.slots));
+  p.count = reinterpret_cast<int*>(take(4 * p.slots));
+  p.place = reinterpret_cast<int*>(take(4 * pairs));
+  p.xr = take(p.fused ? 0 : 4 * p.T * p.H);
+  p.h = reinterpret_cast<float*>(take(4 * p.slots * p.T * p.F));
+  p.partial = reinterpret_cast<float*>(take(4 * p.slots * p.T * p.H));
   return at;
 }
 
 hipError_t launch_moe_tokens(const MoeLaunch& p, hipStream_t s) {
-  hipLaunchKernelGGL(k_moe_route, dim3((unsigned)p.T), dim3(kRouteThreads), 0, s, p);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  hipError_t e = hipSuccess;
+  if (!p.fused) {
+    const unsigned runs = (unsigned)((p.H / 8 + kRouteThreads - 1) / kRouteThreads);
+    hipLaunchKernelGGL(k_moe_route, dim3((unsigned)p.T, runs), dim3(kRouteThreads), 0, s, p);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
   e = by_format(p.wg, [&](auto g, auto k) {
     return launch_up<decltype(g)::value, decltype(k)::value>(p, s);
   });
   if (e != hipSuccess) return e;
-  return by_format(p.wd, [&](auto g, auto k) {
+  e = by_format(p.wd, [&](auto g, auto k) {
     return launch_down<decltype(g)::value, decltype(k)::value>(p, s);
   });
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(k_moe_join,
+                     dim3((unsigned)((p.H / 2 + kRouteThreads - 1) / kRouteThreads), (unsigned)p.T),
+                     dim3(kRouteThreads), 0, s, p);
+  return hipGetLastError();
 }
 
 }  // namespace ufp4
