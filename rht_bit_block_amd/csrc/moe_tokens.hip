@@ -51,6 +51,8 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
@@ -71,7 +73,8 @@ template <> struct Lut<1> {
   static constexpr uint32_t nlo = 0xCACCCED0u, nhi = 0xB8C0C4C8u;
 };
 
-// Nibbles in the low half of each byte of v -> E4M3 bytes.
+// Nibbles in the low half of each byte of v (the high halves are not looked at)
+// -> E4M3 bytes.
 template <int GRID>
 __device__ __forceinline__ uint32_t nib_to_e4m3(uint32_t v) {
   const uint32_t m = v & 0x07070707u;
@@ -84,9 +87,9 @@ __device__ __forceinline__ uint32_t nib_to_e4m3(uint32_t v) {
   }
 }
 
-// The bf16 levels of 8 codes.  E2M1 codes are FP4 values, which convert by
-// themselves, two at a time; the uniform grids go through E4M3 bytes, the even
-// codes first (the activations are stored in the same order).
+// The bf16 levels of 8 codes as four pairs.  E2M1 codes are FP4 values, which
+// convert by themselves, two neighbours at a time: (0 1) (2 3) (4 5) (6 7); the
+// uniform grids go through E4M3 bytes: (0 2) (4 6) (1 3) (5 7).
 template <int GRID>
 __device__ __forceinline__ u32x4 levels8(uint32_t w) {
   auto two = [](bf16x2 v) { return __builtin_bit_cast(uint32_t, v); };
@@ -96,13 +99,20 @@ __device__ __forceinline__ u32x4 levels8(uint32_t w) {
                  two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2)),
                  two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3))};
   } else {
-    const uint32_t ev = nib_to_e4m3<GRID>(w & 0x0F0F0F0Fu);
-    const uint32_t od = nib_to_e4m3<GRID>((w >> 4) & 0x0F0F0F0Fu);
+    const uint32_t ev = nib_to_e4m3<GRID>(w), od = nib_to_e4m3<GRID>(w >> 4);
     return u32x4{two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(ev, 1.0f, false)),
                  two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(ev, 1.0f, true)),
                  two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(od, 1.0f, false)),
                  two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(od, 1.0f, true))};
   }
+}
+
+// The same with the codes 0..3 in the first two words and 4..7 in the others.
+template <int GRID>
+__device__ __forceinline__ u32x4 levels4x2(uint32_t w) {
+  const u32x4 l = levels8<GRID>(w);
+  if constexpr (GRID == 2) return l;
+  else return u32x4{l[0], l[2], l[1], l[3]};   // (0 2) (1 3), (4 6) (5 7)
 }
 
 // --- weights in LDS -----------------------------------------------------------
@@ -113,12 +123,16 @@ template <int SK> struct Sk {
   static constexpr int per = (SK & 1) ? 2 : 1;   // scales per 32 elements
 };
 
-// A wave's ring: kRing steps of two 16-row tiles, each 1 KB of codes and up to
-// 512 bytes of scales.
-constexpr int kRing = 3, kTileBytes = 1024 + 512, kStepBytes = 2 * kTileBytes;
+// A wave's ring: kRing steps of two 16-row tiles, each 1 KB of codes and the
+// scales of 16 rows.  Two steps and 28 KB of activations let two workgroups
+// share a compute unit: while one waits for its tokens' activations or adds
+// up, the other one reads.
+constexpr int kRing = 2;
+template <int SK> constexpr int scale_bytes() { return (Sk<SK>::e8 ? 128 : 256) * Sk<SK>::per; }
+template <int SK> constexpr int tile_bytes() { return 1024 + scale_bytes<SK>(); }
+template <int SK> constexpr int ring_bytes() { return kRing * 2 * tile_bytes<SK>(); }
 constexpr int kCopies = 4;   // loads per wave and step
-constexpr int kActBytes = 64 * 1024;
-constexpr int kLdsBytes = kActBytes + kWaves * kRing * kStepBytes;
+constexpr int kActBytes = 28 * 1024;
 
 // Where a 16-row tile comes from.
 struct TileSource {
@@ -198,62 +212,101 @@ __device__ __forceinline__ void read_scales(const uint8_t* tile, uint32_t shift,
 }
 
 // --- activations in LDS ---------------------------------------------------------
-// Row i, 32 bytes per 8 elements: the upper bf16 pieces and then the lower ones;
-// the 16-byte chunks of a row are exchanged by its number, so that 16 rows read
-// at one place fall on all banks (row_bytes is a multiple of 16 chunks).
+// Row i, 32 bytes per 8 elements: the upper bf16 pieces and then the lower ones
+// of what lane group g of the instruction takes of a 32-element block: its
+// elements 8 g .. 8 g + 7 where the block has one scale (MFMA over 32 of K);
+// 4 g .. 4 g + 3 of the first 16 and of the second 16 where it has two (two
+// MFMAs over 16).  The 16-byte chunks of a row are exchanged by its number, so
+// that 16 rows read at one place fall on all banks (row_bytes is a multiple
+// of 16 chunks).
 __device__ __forceinline__ uint32_t act_chunk(int row, int row_bytes, int chunk) {
   return (uint32_t)(row * row_bytes + 16 * (chunk ^ (row & 15)));
 }
 
-// One step of both tiles against TT tiles of 16 tokens.  acts: LDS; arow[t]:
-// this lane's row of token tile t; blk0: block of acts' first column.
-template <int GRID, int SK, int TT>
+// Where this lane reads, of its row of token tile t: [t][parity of the block]
+// [upper, lower], without the step's 512 bytes and the block pair's 256.
+template <int TT>
+struct ActReads {
+  uint32_t at[TT][2][2];
+};
+template <int TT>
+__device__ __forceinline__ ActReads<TT> act_reads(const int (&arow)[TT], int row_bytes, int g) {
+  ActReads<TT> a;
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) a.at[t][q][b] = act_chunk(arow[t], row_bytes, 8 * q + 2 * g + b);
+  return a;
+}
+
+// One step of both tiles against TT tiles of 16 tokens.  acts: LDS, at the
+// step's activations.  WHOLE: all four blocks are inside K.
+template <int GRID, int SK, int TT, bool WHOLE>
 __device__ __forceinline__ void add_step(f32x4 (&acc)[2][TT], const uint8_t* ring,
                                          const TileSource (&src)[2], const uint8_t* acts,
-                                         const int (&arow)[TT], int row_bytes, int blk0, int step,
-                                         int nb, int lane) {
+                                         const ActReads<TT>& reads, int blocks, int lane) {
   constexpr int P = Sk<SK>::per;
   const int g = lane >> 4, r16 = lane & 15;
   uint32_t code[2][4];
   float s[2][4 * P];
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
-    const uint8_t* t = ring + m * kTileBytes;
+    const uint8_t* t = ring + m * tile_bytes<SK>();
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      code[m][j] = *reinterpret_cast<const uint32_t*>(t + 64 * r16 + 16 * (j ^ (r16 >> 2)) + 4 * g);
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t* w =
+          reinterpret_cast<const uint32_t*>(t + 64 * r16 + 16 * (j ^ (r16 >> 2)));
+      if constexpr (P == 1) code[m][j] = w[g];
+      else   // half of a word of each 16: codes 4 g .. 4 g + 3 of both
+        code[m][j] = __builtin_amdgcn_perm(w[2 + (g >> 1)], w[g >> 1],
+                                           (g & 1) ? 0x07060302u : 0x05040100u);
+    }
     read_scales<SK>(t, src[m].shift, r16, s[m]);
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    if (4 * step + j >= nb) break;
-    const int c = 8 * (4 * step + j - blk0) + 2 * g;
-    bf16x8 hi[TT], lo[TT];
+    if (!WHOLE && j >= blocks) break;
+    // several token tiles: one block's activations at a time fit the registers
+    if constexpr (TT > 1) __builtin_amdgcn_sched_barrier(0);
+    u32x4 hi[TT], lo[TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-      hi[t] = *reinterpret_cast<const bf16x8*>(acts + act_chunk(arow[t], row_bytes, c));
-      lo[t] = *reinterpret_cast<const bf16x8*>(acts + act_chunk(arow[t], row_bytes, c + 1));
+      const uint8_t* a = acts + 256 * (j >> 1);
+      hi[t] = *reinterpret_cast<const u32x4*>(a + reads.at[t][j & 1][0]);
+      lo[t] = *reinterpret_cast<const u32x4*>(a + reads.at[t][j & 1][1]);
     }
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      const u32x4 lv = levels8<GRID>(code[m][j]);
-#pragma unroll
-      for (int q = 0; q < P; ++q) {
-        u32x4 l = lv;
-        if constexpr (P == 2) {   // lane groups 0, 1 hold the first 16 of the 32, 2, 3 the others
-          const uint32_t keep = (g >> 1) == q ? 0xFFFFFFFFu : 0u;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) l[i] &= keep;
-        }
-        const bf16x8 b = __builtin_bit_cast(bf16x8, l);
+      if constexpr (P == 1) {
+        const bf16x8 b = __builtin_bit_cast(bf16x8, levels8<GRID>(code[m][j]));
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
           f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-          x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo[t], b, x, 0, 0, 0);
-          x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi[t], b, x, 0, 0, 0);
+          x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, lo[t]), b, x, 0, 0,
+                                                      0);
+          x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, hi[t]), b, x, 0, 0,
+                                                      0);
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            acc[m][t][r] = __builtin_fmaf(x[r], s[m][P * j + q], acc[m][t][r]);
+          for (int r = 0; r < 4; ++r) acc[m][t][r] = __builtin_fmaf(x[r], s[m][j], acc[m][t][r]);
+        }
+      } else {
+        const u32x4 l = levels4x2<GRID>(code[m][j]);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          auto half = [q](const u32x4& v) {
+            return __builtin_bit_cast(i16x4, u32x2{v[2 * q], v[2 * q + 1]});
+          };
+#pragma unroll
+          for (int t = 0; t < TT; ++t) {
+            f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+            x = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(half(lo[t]), half(l), x, 0, 0, 0);
+            x = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(half(hi[t]), half(l), x, 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[m][t][r] = __builtin_fmaf(x[r], s[m][2 * j + q], acc[m][t][r]);
+          }
         }
       }
     }
@@ -276,14 +329,15 @@ __device__ __forceinline__ void product(f32x4 (&acc)[2][TT], const TileSource (&
   const int lane = threadIdx.x & 63;
   const int steps = (nb + 3) / 4;
   const uint32_t ring0 = lds_addr(ring);
+  const ActReads<TT> reads = act_reads<TT>(arow, row_bytes, lane >> 4);
   // the i-th step of this wave; past the last one the copies give zeros or
   // bytes that nothing reads, and keep the count of loads in flight
   auto copy = [&](int i) {
-    const uint32_t to = ring0 + (uint32_t)(i % kRing) * kStepBytes;
+    const uint32_t to = ring0 + (uint32_t)(i % kRing) * (2 * tile_bytes<SK>());
     int step = ks + i * KS;
     if (step >= steps) step = steps - 1;
 #pragma unroll
-    for (int m = 0; m < 2; ++m) copy_tile<SK>(src[m], to + m * kTileBytes, step, lane);
+    for (int m = 0; m < 2; ++m) copy_tile<SK>(src[m], to + m * tile_bytes<SK>(), step, lane);
   };
 #pragma unroll
   for (int i = 0; i < kRing - 1; ++i) copy(i);
@@ -296,8 +350,13 @@ __device__ __forceinline__ void product(f32x4 (&acc)[2][TT], const TileSource (&
     for (; ks + i * KS < (b0 + bn + 3) / 4; ++i) {
       copy(i + kRing - 1);
       wait_vmcnt<(kRing - 1) * kCopies>();   // step i is there; later ones need not be
-      add_step<GRID, SK, TT>(acc, ring + (i % kRing) * kStepBytes, src, acts, arow, row_bytes, b0,
-                             ks + i * KS, nb, lane);
+      const int step = ks + i * KS;
+      const uint8_t* from = ring + (i % kRing) * (2 * tile_bytes<SK>());
+      const uint8_t* a = acts + 512 * (step - b0 / 4);
+      if (4 * step + 4 <= nb)
+        add_step<GRID, SK, TT, true>(acc, from, src, a, reads, 4, lane);
+      else
+        add_step<GRID, SK, TT, false>(acc, from, src, a, reads, nb - 4 * step, lane);
       // the ring's next copy overwrites what was just read
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     }
@@ -433,11 +492,13 @@ __device__ __forceinline__ void butterfly(float (&v)[8], int lane) {
 }
 
 // Eight neighbouring elements of a row rotated, y = c_n (v S) H, and split into
-// two bf16 pieces in the order of the weights' codebook.  i: which eight of the
+// two bf16 pieces in the order of the weights' codebook and scales (per 32
+// elements).  i: which eight of the
 // row; every lane of the wave takes part, and lane l holds an i that is
 // congruent to l modulo 64, so a chunk's neighbours are neighbouring lanes.
 __device__ __forceinline__ void rotate8(float (&v)[8], int64_t i, int n, float cn,
-                                        const uint32_t (&signs)[4], int grid, u32x4& hi, u32x4& lo) {
+                                        const uint32_t (&signs)[4], int grid, int per, u32x4& hi,
+                                        u32x4& lo) {
   const int lane = threadIdx.x & 63;
   const int o = (int)(8 * i) & 127;
   const uint32_t sg = signs[o >> 5] >> (o & 31);
@@ -460,14 +521,37 @@ __device__ __forceinline__ void rotate8(float (&v)[8], int64_t i, int n, float c
   if (n > 16) butterfly<2>(v, lane);
   if (n > 32) butterfly<4>(v, lane);
   if (n > 64) butterfly<8>(v, lane);
-  constexpr int order[8] = {0, 2, 4, 6, 1, 3, 5, 7};
-  const bool natural = grid == 2;
+  // the pairs of levels8 or levels4x2
+  constexpr int order8[8] = {0, 2, 4, 6, 1, 3, 5, 7}, order4[8] = {0, 2, 1, 3, 4, 6, 5, 7};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const float a = (natural ? v[2 * j] : v[order[2 * j]]) * cn;
-    const float b = (natural ? v[2 * j + 1] : v[order[2 * j + 1]]) * cn;
+    float a = v[2 * j], b = v[2 * j + 1];
+    if (grid != 2) {
+      a = per == 1 ? v[order8[2 * j]] : v[order4[2 * j]];
+      b = per == 1 ? v[order8[2 * j + 1]] : v[order4[2 * j + 1]];
+    }
+    a *= cn;
+    b *= cn;
     hi[j] = pack_bf16(a, b);
     lo[j] = pack_bf16(a - __uint_as_float(hi[j] << 16), b - __uint_as_float(hi[j] & 0xFFFF0000u));
+  }
+}
+
+// The pieces of the i-th eight elements of a row into the activations' layout;
+// at(chunk) is the address of a 16-byte chunk of the row.
+template <class At>
+__device__ __forceinline__ void put8(const u32x4& hi, const u32x4& lo, int64_t i, int per, At at) {
+  if (per == 1) {
+    *reinterpret_cast<u32x4*>(at(2 * i)) = hi;
+    *reinterpret_cast<u32x4*>(at(2 * i + 1)) = lo;
+  } else {
+    // elements 0..3 go to lane group g, 4..7 to g + 1, the first or second half
+    const int64_t c = 8 * (i >> 2) + 4 * (i & 1);   // chunk of lane group 2 (i & 1)
+    const int h = 8 * (int)(i >> 1 & 1);
+    *reinterpret_cast<u32x2*>(at(c) + h) = u32x2{hi[0], hi[1]};
+    *reinterpret_cast<u32x2*>(at(c + 1) + h) = u32x2{lo[0], lo[1]};
+    *reinterpret_cast<u32x2*>(at(c + 2) + h) = u32x2{hi[2], hi[3]};
+    *reinterpret_cast<u32x2*>(at(c + 3) + h) = u32x2{lo[2], lo[3]};
   }
 }
 
@@ -490,19 +574,19 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeLaunch p) {
   float v[8];
   load_x8(p.x + t * p.ldx, in, i, v);
   u32x4 hi, lo;
-  rotate8(v, i, p.nx, p.cnx, p.sign_x, p.wg.grid, hi, lo);
-  if (in) {
-    u32x4* o = reinterpret_cast<u32x4*>(p.xr + t * p.H * 4 + 32 * i);
-    o[0] = hi;
-    o[1] = lo;
-  }
+  const int per = 1 + (p.wg.kind & 1);
+  rotate8(v, i, p.nx, p.cnx, p.sign_x, p.wg.grid, per, hi, lo);
+  if (in) put8(hi, lo, i, per, [&](int64_t c) { return p.xr + t * p.H * 4 + 16 * c; });
 }
 
 // Bytes of a row of x in LDS where all of K is there.
 __host__ __device__ inline int fused_row(int64_t H) { return (int)((H * 4 + 255) / 256 * 256); }
 
-// Blocks of 32 columns of TT 16-token tiles that fit the activations' LDS.
-template <int TT> constexpr int range_of() { return kActBytes / (TT * 16 * 128); }
+// Blocks of 32 columns of m tokens that fit the activations' LDS, whole steps.
+__device__ __forceinline__ int range_of(int act_bytes, int m, int nb) {
+  const int fit = act_bytes / (m * 128) & ~3, all = (nb + 3) & ~3;
+  return fit < all ? fit : all;
+}
 
 // --- gate and up products, activation ---------------------------------------------
 // NF: columns of the intermediate that a workgroup computes, 16 per pair of a
@@ -511,14 +595,14 @@ template <int GRID, int SK, int NF, int TT, bool FUSED>
 __device__ __forceinline__ void moe_up_body(const MoeLaunch& p, int slot, int e, int f0, int m,
                                             const int* tok, const float* share, uint8_t* lds) {
   constexpr int PT = NF / 16, KS = kWaves / PT;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int pt = wave % PT, ks = wave / PT, r16 = lane & 15;
   const int nb = (int)(p.H / 32);
   const int64_t row0 = (int64_t)e * p.F + f0 + pt * 16;
   const TileSource src[2] = {tile_source<SK>(p.wg, row0, p.H, lane),
                              tile_source<SK>(p.wu, row0, p.H, lane)};
   uint8_t* acts = lds;
-  uint8_t* ring = lds + kActBytes + wave * kRing * kStepBytes;
+  uint8_t* ring = lds + p.act_bytes + wave * ring_bytes<SK>();
   int arow[TT];
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
@@ -534,17 +618,18 @@ __device__ __forceinline__ void moe_up_body(const MoeLaunch& p, int slot, int e,
     product<GRID, SK, TT, KS>(acc, src, acts, ring, arow, fused_row(p.H), nb, nb, ks,
                               [](int, int) {});
   } else {
-    constexpr int range = range_of<TT>();
+    const int range = range_of(p.act_bytes, m, nb);
     const sgpr4 xr = rsrc4(p.xr, (uint32_t)(p.T * p.H * 4));
     const uint32_t to = lds_addr(acts);
     product<GRID, SK, TT, KS>(acc, src, acts, ring, arow, range * 128, range, nb, ks, [&](int b0, int) {
-      // rows of 128 range bytes, 1 KB per copy; what lies past K is not read
-      constexpr int per_row = range * 128 / 1024;
-      for (int c = wave; c < m * per_row; c += kWaves) {
-        const int i = c / per_row, part = c % per_row;
-        lds_load16(to + (uint32_t)c * 1024u, xr,
-                   (uint32_t)tok[i] * (uint32_t)(p.H * 4) + (uint32_t)b0 * 128u +
-                       16u * (uint32_t)((part * 64 + lane) ^ (i & 15)), 0);
+      // rows of 128 range bytes, 512 bytes per half wave; past K nothing is read
+      const int per_row = range / 4, halves = m * per_row, hl = lane & 31;
+      for (int c = 2 * wave; c < halves; c += 2 * kWaves) {
+        const int h = c + (lane >> 5), i = h / per_row, part = h % per_row;
+        if (h < halves)
+          lds_load16(to + (uint32_t)c * 512u, xr,
+                     (uint32_t)tok[i] * (uint32_t)(p.H * 4) + (uint32_t)b0 * 128u +
+                         16u * (uint32_t)((part * 32 + hl) ^ (i & 15)), 0);
       }
       wait_vmcnt<0>();
     });
@@ -563,7 +648,7 @@ __device__ __forceinline__ void moe_up_body(const MoeLaunch& p, int slot, int e,
 // more than 16 tokens.
 enum { kFused = 0, kNarrow = 1, kWide = 2 };
 template <int GRID, int SK, int NF, int MODE>
-__global__ __launch_bounds__(kThreads) void k_moe_up(MoeLaunch p) {
+__global__ __launch_bounds__(kThreads, 4) void k_moe_up(MoeLaunch p) {
   constexpr bool FUSED = MODE == kFused;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ int tok[kMoeMaxTokens];
@@ -571,7 +656,7 @@ __global__ __launch_bounds__(kThreads) void k_moe_up(MoeLaunch p) {
   __shared__ int ids_here[FUSED ? kMoeFusedTokens * kMoeMaxChoices : 1];
   __shared__ float share_here[FUSED ? kMoeFusedTokens * kMoeMaxChoices : 1];
   __shared__ int found[2];   // expert, tokens
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int fc = blockIdx.x, slot = blockIdx.y;
   const int* ids = p.ids;
   const float* shares = p.share;
@@ -587,11 +672,9 @@ __global__ __launch_bounds__(kThreads) void k_moe_up(MoeLaunch p) {
         float v[8];
         load_x8(p.x + t * p.ldx, in, i, v);
         u32x4 hi, lo;
-        rotate8(v, i, p.nx, p.cnx, p.sign_x, p.wg.grid, hi, lo);
-        if (in) {
-          *reinterpret_cast<u32x4*>(lds + act_chunk(t, bytes, (int)(2 * i))) = hi;
-          *reinterpret_cast<u32x4*>(lds + act_chunk(t, bytes, (int)(2 * i + 1))) = lo;
-        }
+        rotate8(v, i, p.nx, p.cnx, p.sign_x, p.wg.grid, Sk<SK>::per, hi, lo);
+        if (in)
+          put8(hi, lo, i, Sk<SK>::per, [&](int64_t c) { return lds + act_chunk(t, bytes, (int)c); });
       }
     ids = ids_here;
     shares = share_here;
@@ -660,14 +743,14 @@ template <int GRID, int SK, int RUN, int TT>
 __device__ __forceinline__ void moe_down_body(const MoeLaunch& p, int slot, int e, int m,
                                               int64_t col0, uint8_t* lds) {
   constexpr int PT = RUN / 32, KS = kWaves / PT;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int pt = wave % PT, ks = wave / PT, r16 = lane & 15;
   const int nb = (int)(p.F / 32);
   const int64_t row0 = (int64_t)e * p.H + col0 + pt * 16;   // and RUN / 2 further on
   const TileSource src[2] = {tile_source<SK>(p.wd, row0, p.F, lane),
                              tile_source<SK>(p.wd, row0 + RUN / 2, p.F, lane)};
   uint8_t* acts = lds;
-  uint8_t* ring = lds + kActBytes + wave * kRing * kStepBytes;
+  uint8_t* ring = lds + p.act_bytes + wave * ring_bytes<SK>();
   int arow[TT];
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
@@ -679,7 +762,7 @@ __device__ __forceinline__ void moe_down_body(const MoeLaunch& p, int slot, int 
   for (int q = 0; q < 2; ++q)
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[q][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  constexpr int range = range_of<TT>();
+  const int range = range_of(p.act_bytes, m, nb);
   product<GRID, SK, TT, KS>(acc, src, acts, ring, arow, range * 128, range, nb, ks, [&](int b0, int bn) {
     // one row after another, 64 times 8 neighbouring elements per wave
     const int groups = 4 * bn, runs = (groups + 63) / 64;
@@ -694,11 +777,10 @@ __device__ __forceinline__ void moe_down_body(const MoeLaunch& p, int slot, int 
         for (int j = 0; j < 4; ++j) { v[j] = a[j]; v[4 + j] = b[j]; }
       }
       u32x4 hi, lo;
-      rotate8(v, 4 * (int64_t)b0 + i, p.nh, p.cnh, p.sign_h, p.wd.grid, hi, lo);
-      if (i < groups) {
-        *reinterpret_cast<u32x4*>(acts + act_chunk(row, range * 128, 2 * i)) = hi;
-        *reinterpret_cast<u32x4*>(acts + act_chunk(row, range * 128, 2 * i + 1)) = lo;
-      }
+      rotate8(v, 4 * (int64_t)b0 + i, p.nh, p.cnh, p.sign_h, p.wd.grid, Sk<SK>::per, hi, lo);
+      if (i < groups)
+        put8(hi, lo, i, Sk<SK>::per,
+             [&](int64_t c) { return acts + act_chunk(row, range * 128, (int)c); });
     }
   });
   float* part = reinterpret_cast<float*>(lds);
@@ -712,7 +794,7 @@ __device__ __forceinline__ void moe_down_body(const MoeLaunch& p, int slot, int 
 }
 
 template <int GRID, int SK, int RUN, bool WIDE>
-__global__ __launch_bounds__(kThreads) void k_moe_down(MoeLaunch p) {
+__global__ __launch_bounds__(kThreads, 4) void k_moe_down(MoeLaunch p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int slot = blockIdx.y;
   const int m = p.count[slot], e = p.expert[slot];
@@ -740,15 +822,34 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_join(MoeLaunch p) {
       pack_bf16(v[0] * p.wd.factor, v[1] * p.wd.factor);
 }
 
+// LDS of a product: activations and rings, or the shares of K of the widest run
+// (two matrices, 128 columns) that take their place.
+constexpr int kPartBytes = 2 * 128 * 4;   // per token
+template <int SK>
+int lds_of(const MoeLaunch& p) {
+  const int tokens = p.T <= 16 ? 16 : p.T <= 32 ? 32 : 64;
+  const int a = p.act_bytes + kWaves * ring_bytes<SK>(), b = tokens * kPartBytes;
+  return a > b ? a : b;
+}
+template <int SK>
+constexpr int lds_most() {
+  return (kMoeMaxTokens * 512 > kActBytes ? kMoeMaxTokens * 512 : kActBytes) +
+                     kWaves * ring_bytes<SK>() > kMoeMaxTokens * kPartBytes
+             ? (kMoeMaxTokens * 512 > kActBytes ? kMoeMaxTokens * 512 : kActBytes) +
+                   kWaves * ring_bytes<SK>()
+             : kMoeMaxTokens * kPartBytes;
+}
+
 template <int GRID, int SK, int NF>
 hipError_t launch_up_n(const MoeLaunch& p, hipStream_t s) {
   const dim3 grid((unsigned)(p.F / NF), (unsigned)p.slots);
   auto go = [&](auto mode) {
     constexpr int MODE = decltype(mode)::value;
     static std::atomic<uint64_t> lds_set{0};
-    const hipError_t e = set_lds_limit((const void*)k_moe_up<GRID, SK, NF, MODE>, kLdsBytes, lds_set);
+    const hipError_t e =
+        set_lds_limit((const void*)k_moe_up<GRID, SK, NF, MODE>, lds_most<SK>(), lds_set);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_moe_up<GRID, SK, NF, MODE>), grid, dim3(kThreads), kLdsBytes, s, p);
+    hipLaunchKernelGGL((k_moe_up<GRID, SK, NF, MODE>), grid, dim3(kThreads), lds_of<SK>(p), s, p);
     return hipGetLastError();
   };
   if (p.fused) return go(std::integral_constant<int, kFused>{});
@@ -763,9 +864,10 @@ hipError_t launch_down_n(const MoeLaunch& p, hipStream_t s) {
     constexpr bool WIDE = decltype(wide)::value;
     static std::atomic<uint64_t> lds_set{0};
     const hipError_t e =
-        set_lds_limit((const void*)k_moe_down<GRID, SK, RUN, WIDE>, kLdsBytes, lds_set);
+        set_lds_limit((const void*)k_moe_down<GRID, SK, RUN, WIDE>, lds_most<SK>(), lds_set);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_moe_down<GRID, SK, RUN, WIDE>), grid, dim3(kThreads), kLdsBytes, s, p);
+    hipLaunchKernelGGL((k_moe_down<GRID, SK, RUN, WIDE>), grid, dim3(kThreads), lds_of<SK>(p), s,
+                       p);
     return hipGetLastError();
   };
   return p.T <= 16 ? go(std::false_type{}) : go(std::true_type{});
@@ -807,18 +909,18 @@ int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
 
-// Columns per workgroup, of `cols`: one workgroup fills a compute unit, so the
-// width whose last round of workgroups leaves least idle; of equals the widest,
-// whose waves share the activations most.
+// Columns per workgroup, of `cols`: a round of workgroups (two to a compute unit)
+// costs about its columns and, for routing, activations and joining, as much
+// as 64 columns more; the width whose rounds cost least, of equals the widest.
 int32_t run_width(int64_t cols, int64_t slots) {
-  constexpr int64_t kUnits = 256;
+  constexpr int64_t kUnits = 2 * 256, kFixed = 64;
   int32_t best = 32;
   int64_t least = INT64_MAX;
   for (int32_t w = 32; w <= 128; w *= 2) {
     if (cols % w) break;
-    const int64_t rounds = (cols / w * slots + kUnits - 1) / kUnits;
-    if (rounds * w <= least) {
-      least = rounds * w;
+    const int64_t cost = (cols / w * slots + kUnits - 1) / kUnits * (w + kFixed);
+    if (cost <= least) {
+      least = cost;
       best = w;
     }
   }
@@ -830,6 +932,8 @@ int64_t moe_plan(MoeLaunch& p, uint8_t* ws) {
   const int64_t pairs = p.T * p.k;
   p.by_pair = pairs < p.E;
   p.slots = (int32_t)(p.by_pair ? pairs : p.E);
+  // one step of every token at least
+  p.act_bytes = (int32_t)(p.T * 512 > kActBytes ? p.T * 512 : kActBytes);
   p.fused = p.T <= kMoeFusedTokens && p.T * fused_row(p.H) <= kActBytes;
   p.run_up = run_width(p.F, p.slots);
   p.run_down = run_width(p.H, p.slots);
