@@ -92,7 +92,6 @@ struct MoeLaunch {
   // set by moe_plan
   int32_t by_pair, fused, slots;   // slots: the T k choices, or all experts if fewer
   int32_t run_up, run_down;        // columns per workgroup of the two products
-  int32_t act_bytes;               // LDS for activations
   int* ids;                // [T][k] chosen experts, -1: none
   float* share;            // [T][k]
   int* expert;             // [slots] a slot's expert

@@ -29,14 +29,14 @@
 // by the block's scale, which is the same for a lane's four values (one weight
 // row), so that scales never enter the bf16 operands.
 //
-// The weights go HBM -> LDS (buffer_load ... lds) in steps of 128 of K, three
+// The weights go HBM -> LDS (buffer_load ... lds) in steps of 128 of K, two
 // steps per wave in a ring of its own, so that no barrier or register holds a
 // load back: a lane copies 16 bytes and four neighbouring lanes a row's 64.
 // Straight into registers in the layout of the instruction (neighbouring lanes
 // in different rows) every lane's 16 bytes were a cache access of their own,
-// and the address unit, not HBM, set the pace (200 us against 35 for the up
+// and the address unit, not HBM, set the pace (200 us against 66 for the up
 // product of 16 tokens).  The activations of the workgroup's tokens lie in LDS,
-// 64 KB of them at a time.
+// 28 KB of them at a time.
 #include <type_traits>
 
 #include "lds_copy.h"
@@ -321,7 +321,7 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
 // acc += the product over K of a workgroup's two tiles per wave (src) with its
 // tokens.  The waves are PT tile pairs times KS shares of K: a wave takes steps
 // ks, ks + KS, ..  fill(first block, blocks) puts the activations of a range of
-// K into `acts`, one range after another (what 64 KB hold).
+// K into `acts`, one range after another (what kActBytes hold).
 template <int GRID, int SK, int TT, int KS, class Fill>
 __device__ __forceinline__ void product(f32x4 (&acc)[2][TT], const TileSource (&src)[2],
                                         uint8_t* acts, uint8_t* ring, const int (&arow)[TT],
@@ -583,17 +583,19 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeLaunch p) {
 __host__ __device__ inline int fused_row(int64_t H) { return (int)((H * 4 + 255) / 256 * 256); }
 
 // Blocks of 32 columns of m tokens that fit the activations' LDS, whole steps.
-__device__ __forceinline__ int range_of(int act_bytes, int m, int nb) {
-  const int fit = act_bytes / (m * 128) & ~3, all = (nb + 3) & ~3;
+__device__ __forceinline__ int range_of(int m, int nb) {
+  const int fit = kActBytes / (m * 128) & ~3, all = (nb + 3) & ~3;
   return fit < all ? fit : all;
 }
 
 // --- gate and up products, activation ---------------------------------------------
 // NF: columns of the intermediate that a workgroup computes, 16 per pair of a
-// gate and an up tile.  FUSED: x is in LDS already, row t for token t.
+// gate and an up tile.  Tokens first .. first + m - 1 of the expert's; FUSED: x is
+// in LDS already, row t for token t.
 template <int GRID, int SK, int NF, int TT, bool FUSED>
-__device__ __forceinline__ void moe_up_body(const MoeLaunch& p, int slot, int e, int f0, int m,
-                                            const int* tok, const float* share, uint8_t* lds) {
+__device__ __forceinline__ void moe_up_body(const MoeLaunch& p, int slot, int e, int f0, int first,
+                                            int m, const int* tok, const float* share,
+                                            uint8_t* lds) {
   constexpr int PT = NF / 16, KS = kWaves / PT;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int pt = wave % PT, ks = wave / PT, r16 = lane & 15;
@@ -602,7 +604,7 @@ __device__ __forceinline__ void moe_up_body(const MoeLaunch& p, int slot, int e,
   const TileSource src[2] = {tile_source<SK>(p.wg, row0, p.H, lane),
                              tile_source<SK>(p.wu, row0, p.H, lane)};
   uint8_t* acts = lds;
-  uint8_t* ring = lds + p.act_bytes + wave * ring_bytes<SK>();
+  uint8_t* ring = lds + kActBytes + wave * ring_bytes<SK>();
   int arow[TT];
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
@@ -618,7 +620,7 @@ __device__ __forceinline__ void moe_up_body(const MoeLaunch& p, int slot, int e,
     product<GRID, SK, TT, KS>(acc, src, acts, ring, arow, fused_row(p.H), nb, nb, ks,
                               [](int, int) {});
   } else {
-    const int range = range_of(p.act_bytes, m, nb);
+    const int range = range_of(m, nb);
     const sgpr4 xr = rsrc4(p.xr, (uint32_t)(p.T * p.H * 4));
     const uint32_t to = lds_addr(acts);
     product<GRID, SK, TT, KS>(acc, src, acts, ring, arow, range * 128, range, nb, ks, [&](int b0, int) {
@@ -640,8 +642,9 @@ __device__ __forceinline__ void moe_up_body(const MoeLaunch& p, int slot, int e,
   for (int i = tid; i < m * NF; i += kThreads) {
     const float a = part[i] * p.wg.factor, b = part[ROWS * NF + i] * p.wu.factor;
     const float s = p.act == UFP4_ACT_GELU ? activation<1>(a) : activation<0>(a);
-    p.h[((int64_t)slot * p.T + i / NF) * p.F + f0 + i % NF] = s * b * share[i / NF];
+    p.h[((int64_t)slot * p.T + first + i / NF) * p.F + f0 + i % NF] = s * b * share[i / NF];
   }
+  if constexpr (TT > 1) __syncthreads();   // the next tokens' activations go where `part` is
 }
 
 // FUSED: routing and rotation here, for a few tokens.  WIDE: an expert may have
@@ -727,20 +730,22 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_up(MoeLaunch p) {
   const int e = __builtin_amdgcn_readfirstlane(found[0]);
   const int m = __builtin_amdgcn_readfirstlane(found[1]);
   if (m == 0) return;
-  auto body = [&](auto tt) {
-    moe_up_body<GRID, SK, NF, decltype(tt)::value, FUSED>(p, slot, e, fc * NF, m, tok, share, lds);
+  auto body = [&](auto tt, int first, int n) {
+    moe_up_body<GRID, SK, NF, decltype(tt)::value, FUSED>(p, slot, e, fc * NF, first, n, tok + first,
+                                                          share + first, lds);
   };
-  if (MODE != kWide || m <= 16) body(std::integral_constant<int, 1>{});
-  if constexpr (MODE == kWide) {
-    if (m > 16 && m <= 32) body(std::integral_constant<int, 2>{});
-    else if (m > 32) body(std::integral_constant<int, 4>{});
+  if (MODE != kWide || m <= 16) {
+    body(std::integral_constant<int, 1>{}, 0, m);
+  } else if constexpr (MODE == kWide) {
+    for (int i = 0; i < m; i += 32) body(std::integral_constant<int, 2>{}, i, m - i < 32 ? m - i : 32);
   }
 }
 
 // --- down product --------------------------------------------------------------------
-// RUN: output columns per workgroup, 32 per pair of neighbouring tiles.
+// RUN: output columns per workgroup, 32 per pair of tiles.  hrow: the tokens' first
+// row of the intermediate and of the results.
 template <int GRID, int SK, int RUN, int TT>
-__device__ __forceinline__ void moe_down_body(const MoeLaunch& p, int slot, int e, int m,
+__device__ __forceinline__ void moe_down_body(const MoeLaunch& p, int64_t hrow, int e, int m,
                                               int64_t col0, uint8_t* lds) {
   constexpr int PT = RUN / 32, KS = kWaves / PT;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -750,7 +755,7 @@ __device__ __forceinline__ void moe_down_body(const MoeLaunch& p, int slot, int 
   const TileSource src[2] = {tile_source<SK>(p.wd, row0, p.F, lane),
                              tile_source<SK>(p.wd, row0 + RUN / 2, p.F, lane)};
   uint8_t* acts = lds;
-  uint8_t* ring = lds + p.act_bytes + wave * ring_bytes<SK>();
+  uint8_t* ring = lds + kActBytes + wave * ring_bytes<SK>();
   int arow[TT];
 #pragma unroll
   for (int t = 0; t < TT; ++t) {
@@ -762,7 +767,7 @@ __device__ __forceinline__ void moe_down_body(const MoeLaunch& p, int slot, int 
   for (int q = 0; q < 2; ++q)
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[q][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int range = range_of(p.act_bytes, m, nb);
+  const int range = range_of(m, nb);
   product<GRID, SK, TT, KS>(acc, src, acts, ring, arow, range * 128, range, nb, ks, [&](int b0, int bn) {
     // one row after another, 64 times 8 neighbouring elements per wave
     const int groups = 4 * bn, runs = (groups + 63) / 64;
@@ -771,7 +776,7 @@ __device__ __forceinline__ void moe_down_body(const MoeLaunch& p, int slot, int 
       float v[8] = {};
       if (i < groups) {
         const f32x4* h = reinterpret_cast<const f32x4*>(
-            p.h + ((int64_t)slot * p.T + row) * p.F + 32 * (int64_t)b0 + 8 * i);
+            p.h + (hrow + row) * p.F + 32 * (int64_t)b0 + 8 * i);
         const f32x4 a = h[0], b = h[1];
 #pragma unroll
         for (int j = 0; j < 4; ++j) { v[j] = a[j]; v[4 + j] = b[j]; }
@@ -787,10 +792,11 @@ __device__ __forceinline__ void moe_down_body(const MoeLaunch& p, int slot, int 
   constexpr int HALF = RUN / 2, ROWS = TT * 16;
   join_shares<TT, KS, HALF>(acc, part, pt, ks);
   for (int i = tid; i < m * HALF; i += kThreads) {
-    float* o = p.partial + ((int64_t)slot * p.T + i / HALF) * p.H + col0 + i % HALF;
+    float* o = p.partial + (hrow + i / HALF) * p.H + col0 + i % HALF;
     o[0] = part[i];
     o[HALF] = part[ROWS * HALF + i];
   }
+  if constexpr (TT > 1) __syncthreads();   // the next tokens' activations go where `part` is
 }
 
 template <int GRID, int SK, int RUN, bool WIDE>
@@ -799,13 +805,14 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_down(MoeLaunch p) {
   const int slot = blockIdx.y;
   const int m = p.count[slot], e = p.expert[slot];
   if (m == 0) return;
-  auto body = [&](auto tt) {
-    moe_down_body<GRID, SK, RUN, decltype(tt)::value>(p, slot, e, m, (int64_t)blockIdx.x * RUN, lds);
+  auto body = [&](auto tt, int first, int n) {
+    moe_down_body<GRID, SK, RUN, decltype(tt)::value>(p, (int64_t)slot * p.T + first, e, n,
+                                                      (int64_t)blockIdx.x * RUN, lds);
   };
-  if (!WIDE || m <= 16) body(std::integral_constant<int, 1>{});
-  if constexpr (WIDE) {
-    if (m > 16 && m <= 32) body(std::integral_constant<int, 2>{});
-    else if (m > 32) body(std::integral_constant<int, 4>{});
+  if (!WIDE || m <= 16) {
+    body(std::integral_constant<int, 1>{}, 0, m);
+  } else if constexpr (WIDE) {
+    for (int i = 0; i < m; i += 32) body(std::integral_constant<int, 2>{}, i, m - i < 32 ? m - i : 32);
   }
 }
 
@@ -822,23 +829,11 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_join(MoeLaunch p) {
       pack_bf16(v[0] * p.wd.factor, v[1] * p.wd.factor);
 }
 
-// LDS of a product: activations and rings, or the shares of K of the widest run
-// (two matrices, 128 columns) that take their place.
-constexpr int kPartBytes = 2 * 128 * 4;   // per token
-template <int SK>
-int lds_of(const MoeLaunch& p) {
-  const int tokens = p.T <= 16 ? 16 : p.T <= 32 ? 32 : 64;
-  const int a = p.act_bytes + kWaves * ring_bytes<SK>(), b = tokens * kPartBytes;
-  return a > b ? a : b;
-}
-template <int SK>
-constexpr int lds_most() {
-  return (kMoeMaxTokens * 512 > kActBytes ? kMoeMaxTokens * 512 : kActBytes) +
-                     kWaves * ring_bytes<SK>() > kMoeMaxTokens * kPartBytes
-             ? (kMoeMaxTokens * 512 > kActBytes ? kMoeMaxTokens * 512 : kActBytes) +
-                   kWaves * ring_bytes<SK>()
-             : kMoeMaxTokens * kPartBytes;
-}
+// LDS of a product: activations and rings; the shares of K of two tiles by 128
+// columns and 32 tokens take their place at the end.
+template <int SK> constexpr int lds_bytes() { return kActBytes + kWaves * ring_bytes<SK>(); }
+static_assert(lds_bytes<kE8b32>() >= 2 * 128 * 32 * 4, "the shares of K fit");
+static_assert(kActBytes >= 32 * 512, "one step of 32 tokens fits");
 
 template <int GRID, int SK, int NF>
 hipError_t launch_up_n(const MoeLaunch& p, hipStream_t s) {
@@ -847,9 +842,9 @@ hipError_t launch_up_n(const MoeLaunch& p, hipStream_t s) {
     constexpr int MODE = decltype(mode)::value;
     static std::atomic<uint64_t> lds_set{0};
     const hipError_t e =
-        set_lds_limit((const void*)k_moe_up<GRID, SK, NF, MODE>, lds_most<SK>(), lds_set);
+        set_lds_limit((const void*)k_moe_up<GRID, SK, NF, MODE>, lds_bytes<SK>(), lds_set);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_moe_up<GRID, SK, NF, MODE>), grid, dim3(kThreads), lds_of<SK>(p), s, p);
+    hipLaunchKernelGGL((k_moe_up<GRID, SK, NF, MODE>), grid, dim3(kThreads), lds_bytes<SK>(), s, p);
     return hipGetLastError();
   };
   if (p.fused) return go(std::integral_constant<int, kFused>{});
@@ -864,9 +859,9 @@ hipError_t launch_down_n(const MoeLaunch& p, hipStream_t s) {
     constexpr bool WIDE = decltype(wide)::value;
     static std::atomic<uint64_t> lds_set{0};
     const hipError_t e =
-        set_lds_limit((const void*)k_moe_down<GRID, SK, RUN, WIDE>, lds_most<SK>(), lds_set);
+        set_lds_limit((const void*)k_moe_down<GRID, SK, RUN, WIDE>, lds_bytes<SK>(), lds_set);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_moe_down<GRID, SK, RUN, WIDE>), grid, dim3(kThreads), lds_of<SK>(p), s,
+    hipLaunchKernelGGL((k_moe_down<GRID, SK, RUN, WIDE>), grid, dim3(kThreads), lds_bytes<SK>(), s,
                        p);
     return hipGetLastError();
   };
@@ -932,8 +927,6 @@ int64_t moe_plan(MoeLaunch& p, uint8_t* ws) {
   const int64_t pairs = p.T * p.k;
   p.by_pair = pairs < p.E;
   p.slots = (int32_t)(p.by_pair ? pairs : p.E);
-  // one step of every token at least
-  p.act_bytes = (int32_t)(p.T * 512 > kActBytes ? p.T * 512 : kActBytes);
   p.fused = p.T <= kMoeFusedTokens && p.T * fused_row(p.H) <= kActBytes;
   p.run_up = run_width(p.F, p.slots);
   p.run_down = run_width(p.H, p.slots);
