@@ -195,25 +195,31 @@ __global__ __launch_bounds__(kThreads) void k_prod(Prod p) {
 #pragma unroll
     for (int j = 0; j < S::NJ; ++j) acc[i][j] = floatx16{};
 
+  // Step i computes from stage i % 2.  Its last fragments are read before its
+  // last quarter of MFMAs; there every wave has read the stage, so behind one
+  // barrier the copy of step i + 2 starts into it, with a whole step to land,
+  // and the first fragments of step i + 1 arrive under that last quarter.
   issue<S>(c, 0, 0);
-  wait_vmcnt<0>();
+  issue<S>(c, 1, 1);
+  wait_vmcnt<S::LA + S::LB>();
   __syncthreads();
   bf16x8 a0[S::NI], b0[S::NJ], a1[S::NI], b1[S::NJ];
   frags<S>(lds, 0, lane, wm, wn, a0, b0);
   for (int step = 0; step < c.nsteps; ++step) {
     const uint8_t* cur = lds + (step & 1) * S::STAGE;
-    issue<S>(c, step + 1, (step + 1) & 1);
     frags<S>(cur, 1, lane, wm, wn, a1, b1);
     mfmas<S>(acc, a0, b0);
     frags<S>(cur, 2, lane, wm, wn, a0, b0);
     mfmas<S>(acc, a1, b1);
     frags<S>(cur, 3, lane, wm, wn, a1, b1);
     mfmas<S>(acc, a0, b0);
-    mfmas<S>(acc, a1, b1);
     wait_vmcnt<0>();
     __syncthreads();
+    issue<S>(c, step + 2, step & 1);
     frags<S>(lds + ((step + 1) & 1) * S::STAGE, 0, lane, wm, wn, a0, b0);
+    mfmas<S>(acc, a1, b1);
   }
+  wait_vmcnt<0>();
 
   // acc[i][j][r]: n = j 32 + lane % 32, m = i 32 + 8 (r / 4) + 4 (lane / 32) + r % 4
   const int mw = wm * S::NI * 32 + 4 * h, nw = wn * S::NJ * 32 + (lane & 31);
