@@ -18,9 +18,10 @@
 // operations' time).
 //
 // The products are bound by the matrix cores: v_mfma_f32_32x32x16_bf16, 256 x
-// 256 tiles, four waves of 128 x 128 (accumulators in AGPRs), operands copied
-// HBM -> LDS by buffer_load ... lds in 128-byte rows with XOR-swizzled 16-byte
-// chunks.  The output's contiguous dimension is m, because a lane of the
+// 256 tiles, eight waves of 128 x 64 (two to a SIMD: while one of them waits to
+// issue a copy or an LDS read, the other one feeds the matrix core), operands
+// copied HBM -> LDS by buffer_load ... lds in 128-byte rows with XOR-swizzled
+// 16-byte chunks.  The output's contiguous dimension is m, because a lane of the
 // instruction holds four consecutive m of one n: 8- and 16-byte stores, and
 // the softmax statistics of a token (an n) are almost all inside one lane.
 #include "gemm_epilogue.h"
@@ -84,15 +85,16 @@ struct Prod {
 };
 
 // Tile shape: WM x WN waves of (32 NI) x (32 NJ).
-template <int WM_, int WN_, int NI_, int NJ_, int ST_>
+template <int WM_, int WN_, int NI_, int NJ_>
 struct Shape {
-  static constexpr int WM = WM_, WN = WN_, NI = NI_, NJ = NJ_, ST = ST_;
+  static constexpr int WM = WM_, WN = WN_, NI = NI_, NJ = NJ_;
   static constexpr int TM = WM * NI * 32, TN = WN * NJ * 32;
   static constexpr int STAGE = (TM + TN) * 128;
-  static constexpr int LA = TM / 32, LB = TN / 32;   // 8-row loads per wave and step
-  static_assert(WM * WN == 4, "four waves");
+  static constexpr int W = WM * WN, THREADS = 64 * W;
+  static constexpr int LA = TM / 8 / W, LB = TN / 8 / W;   // 8-row copies per wave and step
+  static_assert(LA * 8 * W == TM && LB * 8 * W == TN, "the waves share the rows evenly");
 };
-using Big = Shape<2, 2, 4, 4, 2>;
+using Big = Shape<2, 4, 4, 2>;
 
 // The swizzle's part that differs between a wave's 8-row loads.
 __device__ __forceinline__ uint32_t chunk_flip(int row8) { return (uint32_t)(row8 & 1) << 6; }
@@ -106,58 +108,71 @@ struct Ctx {
   int wave, nsteps;
 };
 
-// Copy step `step` (64 k) into stage `st`.  Past the last step nothing is
-// copied that is read; chunks past K read as zeros.
+// The q-th of a wave's LA + LB copies of step `step` (64 k) into stage `st`.
+// Past the last step the last one is copied again, and not read; chunks past
+// K read as zeros.
 template <class S>
-__device__ __forceinline__ void issue(const Ctx<S>& c, int step, int st) {
+__device__ __forceinline__ void issue_one(const Ctx<S>& c, int step, int st, int q) {
   const int s = step < c.nsteps ? step : c.nsteps - 1;
-  const uint32_t base = c.lds0 + (uint32_t)st * S::STAGE;
   const uint32_t koff = (uint32_t)s * 128u;
-  const bool tail = koff + 128u > c.kbytes;
-  // outside every buffer: zeros
-  auto in_k = [&](uint32_t v, int row8) {
-    return tail && koff + (c.cbyte ^ chunk_flip(row8)) >= c.kbytes ? 0x7FFFFF00u : v;
-  };
-#pragma unroll
-  for (int q = 0; q < S::LA; ++q) {
-    const int row8 = c.wave * S::LA + q;
-    lds_load16(base + (uint32_t)row8 * 1024u, c.ra, in_k(c.va[q], row8), koff);
-  }
-#pragma unroll
-  for (int q = 0; q < S::LB; ++q) {
-    const int row8 = c.wave * S::LB + q;
-    lds_load16(base + (uint32_t)(S::TM / 8 + row8) * 1024u, c.rb, in_k(c.vb[q], row8), koff);
-  }
+  const bool in_a = q < S::LA;
+  const int row8 = in_a ? c.wave * S::LA + q : c.wave * S::LB + (q - S::LA);
+  uint32_t v = in_a ? c.va[in_a ? q : 0] : c.vb[in_a ? 0 : q - S::LA];
+  if (koff + 128u > c.kbytes && koff + (c.cbyte ^ chunk_flip(row8)) >= c.kbytes)
+    v = 0x7FFFFF00u;   // outside every buffer: zeros
+  const uint32_t to =
+      c.lds0 + (uint32_t)st * S::STAGE + (uint32_t)(in_a ? row8 : S::TM / 8 + row8) * 1024u;
+  if (in_a) lds_load16(to, c.ra, v, koff);
+  else lds_load16(to, c.rb, v, koff);
 }
 
 template <class S>
-__device__ __forceinline__ void frags(const uint8_t* stage, int s, int lane, int wm, int wn,
-                                      bf16x8 (&a)[S::NI], bf16x8 (&b)[S::NJ]) {
-  const int h = lane >> 5;
-#pragma unroll
-  for (int i = 0; i < S::NI; ++i)
-    a[i] = *reinterpret_cast<const bf16x8*>(
-        stage + off128(wm * S::NI * 32 + i * 32 + (lane & 31), 2 * s + h));
-#pragma unroll
-  for (int j = 0; j < S::NJ; ++j)
-    b[j] = *reinterpret_cast<const bf16x8*>(
-        stage + S::TM * 128 + off128(wn * S::NJ * 32 + j * 32 + (lane & 31), 2 * s + h));
+struct Frags {
+  bf16x8 a[S::NI], b[S::NJ];
+};
+
+// The q-th fragment of quarter s of a stage: the first row tile of A and all of
+// B, which the first MFMAs need, come first.
+template <class S>
+__device__ __forceinline__ void read_one(Frags<S>& f, const uint8_t* stage, int s, int q, int lane,
+                                         int wm, int wn) {
+  const int c = 2 * s + (lane >> 5), r = lane & 31;
+  if (q >= 1 && q <= S::NJ) {
+    f.b[q - 1] = *reinterpret_cast<const bf16x8*>(
+        stage + S::TM * 128 + off128(wn * S::NJ * 32 + (q - 1) * 32 + r, c));
+  } else {
+    const int i = q == 0 ? 0 : q - S::NJ;
+    f.a[i] = *reinterpret_cast<const bf16x8*>(stage + off128(wm * S::NI * 32 + i * 32 + r, c));
+  }
 }
 
-template <class S>
-__device__ __forceinline__ void mfmas(floatx16 (&acc)[S::NI][S::NJ], const bf16x8 (&a)[S::NI],
-                                      const bf16x8 (&b)[S::NJ]) {
+// A quarter's MFMAs on `f`, and among them the reads of the next quarter's
+// fragments (quarter s of `stage`) and COUNT copies from number FIRST on.
+template <class S, int FIRST, int COUNT>
+__device__ __forceinline__ void quarter(floatx16 (&acc)[S::NI][S::NJ], const Frags<S>& f,
+                                        Frags<S>& next, const uint8_t* stage, int s,
+                                        const Ctx<S>& c, int step, int st, int lane, int wm,
+                                        int wn) {
+  constexpr int M = S::NI * S::NJ, R = S::NI + S::NJ;
 #pragma unroll
-  for (int i = 0; i < S::NI; ++i)
+  for (int m = 0; m < M; ++m) {
 #pragma unroll
-    for (int j = 0; j < S::NJ; ++j)
-      acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+    for (int q = 0; q < R; ++q)
+      if (q * M / R == m) read_one<S>(next, stage, s, q, lane, wm, wn);
+    if constexpr (COUNT > 0) {
+#pragma unroll
+      for (int q = 0; q < COUNT; ++q)
+        if (q * M / COUNT == m) issue_one<S>(c, step, st, FIRST + q);
+    }
+    acc[m / S::NJ][m % S::NJ] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+        f.a[m / S::NJ], f.b[m % S::NJ], acc[m / S::NJ][m % S::NJ], 0, 0, 0);
+  }
 }
 
 template <class S, int EPI>
-__global__ __launch_bounds__(kThreads) void k_prod(Prod p) {
+__global__ __launch_bounds__(S::THREADS) void k_prod(Prod p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / S::WN, wn = wave % S::WN, h = lane >> 5;
   const int split = blockIdx.x / p.tiles, b = blockIdx.x % p.tiles;
   int tm, tn;
@@ -196,28 +211,29 @@ __global__ __launch_bounds__(kThreads) void k_prod(Prod p) {
     for (int j = 0; j < S::NJ; ++j) acc[i][j] = floatx16{};
 
   // Step i computes from stage i % 2.  Its last fragments are read before its
-  // last quarter of MFMAs; there every wave has read the stage, so behind one
-  // barrier the copy of step i + 2 starts into it, with a whole step to land,
-  // and the first fragments of step i + 1 arrive under that last quarter.
-  issue<S>(c, 0, 0);
-  issue<S>(c, 1, 1);
-  wait_vmcnt<S::LA + S::LB>();
+  // last quarter; there every wave has read the stage, so behind one barrier
+  // the copies of step i + 2 start into it: three quarters of them in that last
+  // quarter, the rest in the first quarter of step i + 1, and both have the two
+  // quarters after that to land.
+  constexpr int L = S::LA + S::LB, L3 = L * 3 / 4, L0 = L - L3;
+#pragma unroll
+  for (int q = 0; q < L; ++q) issue_one<S>(c, 0, 0, q);
+#pragma unroll
+  for (int q = 0; q < L3; ++q) issue_one<S>(c, 1, 1, q);
+  wait_vmcnt<L3>();
   __syncthreads();
-  bf16x8 a0[S::NI], b0[S::NJ], a1[S::NI], b1[S::NJ];
-  frags<S>(lds, 0, lane, wm, wn, a0, b0);
+  Frags<S> f0, f1;
+#pragma unroll
+  for (int q = 0; q < S::NI + S::NJ; ++q) read_one<S>(f0, lds, 0, q, lane, wm, wn);
   for (int step = 0; step < c.nsteps; ++step) {
-    const uint8_t* cur = lds + (step & 1) * S::STAGE;
-    frags<S>(cur, 1, lane, wm, wn, a1, b1);
-    mfmas<S>(acc, a0, b0);
-    frags<S>(cur, 2, lane, wm, wn, a0, b0);
-    mfmas<S>(acc, a1, b1);
-    frags<S>(cur, 3, lane, wm, wn, a1, b1);
-    mfmas<S>(acc, a0, b0);
+    const int st = step & 1;
+    const uint8_t* cur = lds + st * S::STAGE;
+    quarter<S, L3, L0>(acc, f0, f1, cur, 1, c, step + 1, st ^ 1, lane, wm, wn);
+    quarter<S, 0, 0>(acc, f1, f0, cur, 2, c, 0, 0, lane, wm, wn);
+    quarter<S, 0, 0>(acc, f0, f1, cur, 3, c, 0, 0, lane, wm, wn);
     wait_vmcnt<0>();
     __syncthreads();
-    issue<S>(c, step + 2, step & 1);
-    frags<S>(lds + ((step + 1) & 1) * S::STAGE, 0, lane, wm, wn, a0, b0);
-    mfmas<S>(acc, a1, b1);
+    quarter<S, 0, L3>(acc, f1, f0, lds + (st ^ 1) * S::STAGE, 0, c, step + 2, st, lane, wm, wn);
   }
   wait_vmcnt<0>();
 
@@ -439,7 +455,7 @@ int64_t up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
 
 template <class S, int EPI>
 hipError_t launch_prod(Prod p, hipStream_t s) {
-  constexpr int bytes = S::ST * S::STAGE;
+  constexpr int bytes = 2 * S::STAGE;
   static std::atomic<uint64_t> lds_set{0};
   const hipError_t e = set_lds_limit((const void*)k_prod<S, EPI>, bytes, lds_set);
   if (e != hipSuccess) return e;
@@ -449,8 +465,8 @@ hipError_t launch_prod(Prod p, hipStream_t s) {
   if (p.splits < 1) p.splits = 1;
   p.k_per_split = p.splits == 1 ? p.K : up(cdiv(p.K, p.splits), 64);
   p.splits = (int32_t)cdiv(p.K, p.k_per_split);
-  hipLaunchKernelGGL((k_prod<S, EPI>), dim3((unsigned)(p.tiles * p.splits)), dim3(kThreads), bytes,
-                     s, p);
+  hipLaunchKernelGGL((k_prod<S, EPI>), dim3((unsigned)(p.tiles * p.splits)), dim3(S::THREADS),
+                     bytes, s, p);
   return hipGetLastError();
 }
 
