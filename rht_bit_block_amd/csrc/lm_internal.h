@@ -53,7 +53,7 @@ struct XentPlan {
   int64_t parts;                 // statistics per token in the forward pass
   int64_t fwd_bytes, bwd_bytes;
   int64_t piece, pieces;         // classes per piece (a multiple of 256), pieces
-  int64_t Tp;                    // tokens rounded up to 64
+  int64_t Tp;                    // tokens rounded up to 8
   int32_t splits;                // of the dh product's K
   int64_t g, gt, wt, ht, slab;   // offsets of the backward workspace's parts
 };

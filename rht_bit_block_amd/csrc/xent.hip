@@ -14,8 +14,8 @@
 // half a step of rounding per element, averaged over the long sums), then dh
 // += G W in fp32 and dW = G^T h.  Every product runs as C[m][n] = sum_k
 // A[m][k] B[n][k] with both operands K-contiguous, so h, the piece of W and G
-// are also laid out transposed (plain tiled copies, 1/256 of the product's
-// operations' time).
+// are also laid out transposed (plain tiled copies, a hundredth of the products'
+// operations' time; G leaves its tiles in both orders).
 //
 // The products are bound by the matrix cores: v_mfma_f32_32x32x16_bf16, 256 x
 // 256 tiles, eight waves of 128 x 64 (two to a SIMD: while one of them waits to
@@ -67,7 +67,7 @@ struct Prod {
   int64_t lda, ldb;         // row pitches in elements
   int32_t tiles_m, tiles_n, tiles, splits;
   int64_t k_per_split;      // a multiple of 64
-  // kStats: partials [2 tiles_m][N] (maximum, sum), logits of the targets
+  // kStats: partials [WM tiles_m][N] (maximum, sum), logits of the targets
   float2* part;
   float* zt;
   // kStats, kGrad
@@ -79,22 +79,29 @@ struct Prod {
   // kGrad, kOut: bf16 [N][ldo], m contiguous, m < m_store written
   uint16_t* out;
   int64_t ldo, m_store, n_store;
+  uint16_t* out_t;          // kGrad: the same turned, [m_store][ldt], columns n < ldt
+  int64_t ldt;
   // kSlab: fp32 [splits][N][M], added to unless `first`
   float* slab;
   int32_t first;
 };
 
-// Tile shape: WM x WN waves of (32 NI) x (32 NJ).
-template <int WM_, int WN_, int NI_, int NJ_>
+// Tile shape: WM x WN waves of (32 NI) x (32 NJ), ST stages of 64 k in LDS.
+template <int WM_, int WN_, int NI_, int NJ_, int ST_>
 struct Shape {
-  static constexpr int WM = WM_, WN = WN_, NI = NI_, NJ = NJ_;
+  static constexpr int WM = WM_, WN = WN_, NI = NI_, NJ = NJ_, ST = ST_;
   static constexpr int TM = WM * NI * 32, TN = WN * NJ * 32;
   static constexpr int STAGE = (TM + TN) * 128;
   static constexpr int W = WM * WN, THREADS = 64 * W;
   static constexpr int LA = TM / 8 / W, LB = TN / 8 / W;   // 8-row copies per wave and step
   static_assert(LA * 8 * W == TM && LB * 8 * W == TN, "the waves share the rows evenly");
 };
-using Big = Shape<2, 4, 4, 2>;
+using Big = Shape<2, 4, 4, 2, 2>;
+// For up to 32 or 64 tokens, where reading W is all that counts: 128 classes per
+// workgroup and four stages, so that 60 KB of every compute unit's share are
+// in flight (the 256 x 256 tile on 7 tokens, 32003 classes, 2048 wide: 48 us)
+using Thin32 = Shape<4, 1, 1, 1, 4>;
+using Thin64 = Shape<4, 1, 1, 2, 4>;
 
 // The swizzle's part that differs between a wave's 8-row loads.
 __device__ __forceinline__ uint32_t chunk_flip(int row8) { return (uint32_t)(row8 & 1) << 6; }
@@ -169,6 +176,70 @@ __device__ __forceinline__ void quarter(floatx16 (&acc)[S::NI][S::NJ], const Fra
   }
 }
 
+// The tile as bf16 in LDS and from there to memory in whole rows.  store_nm:
+// rows n of m (a lane holds four neighbouring m of one n); store_mn: rows m of
+// n.  dst is the tile's first element; only m < m_end and n < n_end are written
+// (multiples of 8 along a row).  16-byte chunks of a row are exchanged by its
+// number, so that both the writes and the row reads spread over the banks.
+template <class S, int ROWS, int COLS>
+__device__ __forceinline__ void rows_out(const uint8_t* lds, uint16_t* dst, int64_t ld,
+                                         int64_t row_end, int64_t col_end) {
+  constexpr int C = COLS / 8;   // chunks of a row
+  for (int i = threadIdx.x; i < ROWS * C; i += S::THREADS) {
+    const int r = i / C, c = i % C;
+    if (r < row_end && 8 * c < col_end)
+      *reinterpret_cast<u32x4*>(dst + r * ld + 8 * c) =
+          *reinterpret_cast<const u32x4*>(lds + r * (COLS * 2) + 16 * (c ^ (r & (C - 1))));
+  }
+}
+
+template <class S>
+__device__ __forceinline__ void store_nm(const floatx16 (&acc)[S::NI][S::NJ], uint8_t* lds,
+                                         uint16_t* dst, int64_t ld, int64_t m_end, int64_t n_end,
+                                         int wm, int wn) {
+  const int lane = threadIdx.x & 63;
+  constexpr int C = S::TM / 8;
+#pragma unroll
+  for (int j = 0; j < S::NJ; ++j) {
+    const int n = wn * S::NJ * 32 + j * 32 + (lane & 31);
+#pragma unroll
+    for (int i = 0; i < S::NI; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c = (wm * S::NI * 32 + i * 32 + 8 * q) / 8;
+        const u32x2 w = {pack_bf16(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
+                         pack_bf16(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3])};
+        *reinterpret_cast<u32x2*>(lds + n * (S::TM * 2) + 16 * (c ^ (n & (C - 1))) +
+                                  8 * (lane >> 5)) = w;
+      }
+  }
+  __syncthreads();
+  rows_out<S, S::TN, S::TM>(lds, dst, ld, n_end, m_end);
+}
+
+template <class S>
+__device__ __forceinline__ void store_mn(const floatx16 (&acc)[S::NI][S::NJ], uint8_t* lds,
+                                         uint16_t* dst, int64_t ld, int64_t m_end, int64_t n_end,
+                                         int wm, int wn) {
+  const int lane = threadIdx.x & 63;
+  constexpr int C = S::TN / 8;
+#pragma unroll
+  for (int j = 0; j < S::NJ; ++j) {
+    const int n = wn * S::NJ * 32 + j * 32 + (lane & 31);
+#pragma unroll
+    for (int i = 0; i < S::NI; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        const int m = wm * S::NI * 32 + i * 32 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        *reinterpret_cast<uint16_t*>(lds + m * (S::TN * 2) + 16 * ((n >> 3) ^ (m & (C - 1))) +
+                                     2 * (n & 7)) =
+            (uint16_t)pack_bf16(acc[i][j][r], 0.0f);
+      }
+  }
+  __syncthreads();
+  rows_out<S, S::TM, S::TN>(lds, dst, ld, m_end, n_end);
+}
+
 template <class S, int EPI>
 __global__ __launch_bounds__(S::THREADS) void k_prod(Prod p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -210,32 +281,64 @@ __global__ __launch_bounds__(S::THREADS) void k_prod(Prod p) {
 #pragma unroll
     for (int j = 0; j < S::NJ; ++j) acc[i][j] = floatx16{};
 
-  // Step i computes from stage i % 2.  Its last fragments are read before its
-  // last quarter; there every wave has read the stage, so behind one barrier
-  // the copies of step i + 2 start into it: three quarters of them in that last
-  // quarter, the rest in the first quarter of step i + 1, and both have the two
-  // quarters after that to land.
-  constexpr int L = S::LA + S::LB, L3 = L * 3 / 4, L0 = L - L3;
+  if constexpr (S::ST == 2) {
+    // Step i computes from stage i % 2.  Its last fragments are read before its
+    // last quarter; there every wave has read the stage, so behind one barrier
+    // the copies of step i + 2 start into it: three quarters of them in that last
+    // quarter, the rest in the first quarter of step i + 1, and both have the two
+    // quarters after that to land.
+    constexpr int L = S::LA + S::LB, L3 = L * 3 / 4, L0 = L - L3;
 #pragma unroll
-  for (int q = 0; q < L; ++q) issue_one<S>(c, 0, 0, q);
+    for (int q = 0; q < L; ++q) issue_one<S>(c, 0, 0, q);
 #pragma unroll
-  for (int q = 0; q < L3; ++q) issue_one<S>(c, 1, 1, q);
-  wait_vmcnt<L3>();
-  __syncthreads();
-  Frags<S> f0, f1;
-#pragma unroll
-  for (int q = 0; q < S::NI + S::NJ; ++q) read_one<S>(f0, lds, 0, q, lane, wm, wn);
-  for (int step = 0; step < c.nsteps; ++step) {
-    const int st = step & 1;
-    const uint8_t* cur = lds + st * S::STAGE;
-    quarter<S, L3, L0>(acc, f0, f1, cur, 1, c, step + 1, st ^ 1, lane, wm, wn);
-    quarter<S, 0, 0>(acc, f1, f0, cur, 2, c, 0, 0, lane, wm, wn);
-    quarter<S, 0, 0>(acc, f0, f1, cur, 3, c, 0, 0, lane, wm, wn);
-    wait_vmcnt<0>();
+    for (int q = 0; q < L3; ++q) issue_one<S>(c, 1, 1, q);
+    wait_vmcnt<L3>();
     __syncthreads();
-    quarter<S, 0, L3>(acc, f1, f0, lds + (st ^ 1) * S::STAGE, 0, c, step + 2, st, lane, wm, wn);
+    Frags<S> f0, f1;
+#pragma unroll
+    for (int q = 0; q < S::NI + S::NJ; ++q) read_one<S>(f0, lds, 0, q, lane, wm, wn);
+    for (int step = 0; step < c.nsteps; ++step) {
+      const int st = step & 1;
+      const uint8_t* cur = lds + st * S::STAGE;
+      quarter<S, L3, L0>(acc, f0, f1, cur, 1, c, step + 1, st ^ 1, lane, wm, wn);
+      quarter<S, 0, 0>(acc, f1, f0, cur, 2, c, 0, 0, lane, wm, wn);
+      quarter<S, 0, 0>(acc, f0, f1, cur, 3, c, 0, 0, lane, wm, wn);
+      wait_vmcnt<0>();
+      __syncthreads();
+      quarter<S, 0, L3>(acc, f1, f0, lds + (st ^ 1) * S::STAGE, 0, c, step + 2, st, lane, wm, wn);
+    }
+    wait_vmcnt<0>();
+  } else {
+    // Memory-bound: step i + ST - 1 is copied while step i is computed.
+    constexpr int L = S::LA + S::LB;
+#pragma unroll
+    for (int i = 0; i < S::ST - 1; ++i)
+#pragma unroll
+      for (int q = 0; q < L; ++q) issue_one<S>(c, i, i, q);
+    for (int step = 0, st = 0; step < c.nsteps; ++step) {
+      wait_vmcnt<(S::ST - 2) * L>();
+      __syncthreads();   // the step is there, and the one before has been read
+      const int prev = st == 0 ? S::ST - 1 : st - 1;
+#pragma unroll
+      for (int q = 0; q < L; ++q) issue_one<S>(c, step + S::ST - 1, prev, q);
+      Frags<S> f[4];
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int q = 0; q < S::NI + S::NJ; ++q)
+          read_one<S>(f[s], lds + st * S::STAGE, s, q, lane, wm, wn);
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int i = 0; i < S::NI; ++i)
+#pragma unroll
+          for (int j = 0; j < S::NJ; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f[s].a[i], f[s].b[j], acc[i][j], 0,
+                                                                0, 0);
+      st = st + 1 == S::ST ? 0 : st + 1;
+    }
+    wait_vmcnt<0>();
   }
-  wait_vmcnt<0>();
 
   // acc[i][j][r]: n = j 32 + lane % 32, m = i 32 + 8 (r / 4) + 4 (lane / 32) + r % 4
   const int mw = wm * S::NI * 32 + 4 * h, nw = wn * S::NJ * 32 + (lane & 31);
@@ -301,26 +404,25 @@ __global__ __launch_bounds__(S::THREADS) void k_prod(Prod p) {
         l = p.lse[n];
       }
       const bool none = a == 0.0f && bt == 0.0f;   // whatever its logits hold
-      uint16_t* o = p.out + n * p.ldo + row0 + mw;
 #pragma unroll
       for (int i = 0; i < S::NI; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float g[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int m = i * 32 + 8 * q + r;
-            g[r] = a * __builtin_amdgcn_exp2f((acc[i][j][4 * q + r] - l) * kLog2e);
-            if (at == m) g[r] -= bt;
-            if (none || mw + m >= rows) g[r] = 0.0f;
-          }
-          const int64_t m = row0 + mw + i * 32 + 8 * q;
-          if (n < p.n_store && m < p.m_store) {
-            const u32x2 w = {pack_bf16(g[0], g[1]), pack_bf16(g[2], g[3])};
-            *reinterpret_cast<u32x2*>(o + i * 32 + 8 * q) = w;
-          }
+        for (int r = 0; r < 16; ++r) {
+          const int m = i * 32 + 8 * (r >> 2) + (r & 3);
+          float g = a * __builtin_amdgcn_exp2f((acc[i][j][r] - l) * kLog2e);
+          if (at == m) g -= bt;
+          acc[i][j][r] = none || mw + m >= rows ? 0.0f : g;
         }
     }
+    __syncthreads();   // the stages are done with
+    store_nm<S>(acc, lds, p.out + col0 * p.ldo + row0, p.ldo, p.m_store - row0, p.n_store - col0, wm,
+                wn);
+    __syncthreads();
+    store_mn<S>(acc, lds, p.out_t + row0 * p.ldt + col0, p.ldt, p.m_store - row0, p.ldt - col0, wm,
+                wn);
+  } else if constexpr (EPI == kOut) {
+    __syncthreads();
+    store_nm<S>(acc, lds, p.out + col0 * p.ldo + row0, p.ldo, p.M - row0, p.N - col0, wm, wn);
   } else {
 #pragma unroll
     for (int j = 0; j < S::NJ; ++j) {
@@ -332,55 +434,43 @@ __global__ __launch_bounds__(S::THREADS) void k_prod(Prod p) {
         for (int q = 0; q < 4; ++q) {
           const int64_t m = row0 + mw + i * 32 + 8 * q;
           if (m >= p.M) continue;   // M is a multiple of 8: four at a time are in or out
-          if constexpr (EPI == kSlab) {
-            f32x4* o = reinterpret_cast<f32x4*>(p.slab + ((int64_t)split * p.N + n) * p.M + m);
-            f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                       acc[i][j][4 * q + 3]};
-            if (!p.first) v += *o;
-            *o = v;
-          } else {
-            const u32x2 w = {pack_bf16(acc[i][j][4 * q], acc[i][j][4 * q + 1]),
-                             pack_bf16(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3])};
-            *reinterpret_cast<u32x2*>(p.out + n * p.ldo + m) = w;
-          }
+          f32x4* o = reinterpret_cast<f32x4*>(p.slab + ((int64_t)split * p.N + n) * p.M + m);
+          f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                     acc[i][j][4 * q + 3]};
+          if (!p.first) v += *o;
+          *o = v;
         }
     }
   }
 }
 
-// Joins the tiles' statistics: 8 tokens per workgroup, 32 threads each, their
-// partial results joined in a fixed order.
+// Joins the tiles' statistics: TB tokens per workgroup, 256 / TB threads each,
+// their partial results joined in a fixed order.
+template <int TB>
 __global__ __launch_bounds__(kThreads) void k_xent_join(const float2* part, const float* zt,
                                                         const int64_t* targets, int64_t T,
                                                         int64_t classes, int parts, float* loss,
                                                         float* lse) {
-  __shared__ float2 red[32][8];
-  const int tl = threadIdx.x & 7, sl = threadIdx.x >> 3;
-  const int64_t t = (int64_t)blockIdx.x * 8 + tl;
-  float m = -INFINITY, s = 0.0f;
-  if (t < T) {
-    for (int q = sl; q < parts; q += 32) {
-      const float2 v = part[(int64_t)q * T + t];
-      const float big = fmaxf(m, v.x);
-      if (big == -INFINITY) {
-        s += v.y;   // nothing yet (a NaN stays)
-      } else {
-        s = s * __builtin_amdgcn_exp2f((m - big) * kLog2e) +
-            v.y * __builtin_amdgcn_exp2f((v.x - big) * kLog2e);
-        m = big;
-      }
-    }
+  constexpr int SL = kThreads / TB;
+  __shared__ float2 red[SL][TB];
+  const int tl = threadIdx.x % TB, sl = threadIdx.x / TB;
+  const int64_t t = (int64_t)blockIdx.x * TB + tl;
+  auto add = [](float2 a, float2 b) {   // of two (maximum, sum)
+    const float m = fmaxf(a.x, b.x);
+    if (m == -INFINITY) return make_float2(m, a.y + b.y);   // nothing yet (a NaN stays)
+    return make_float2(m, a.y * __builtin_amdgcn_exp2f((a.x - m) * kLog2e) +
+                              b.y * __builtin_amdgcn_exp2f((b.x - m) * kLog2e));
+  };
+  float2 v = make_float2(-INFINITY, 0.0f);
+  if (t < T)
+    for (int q = sl; q < parts; q += SL) v = add(v, part[(int64_t)q * T + t]);
+  red[sl][tl] = v;
+  for (int h = SL / 2; h > 0; h /= 2) {
+    __syncthreads();
+    if (sl < h) red[sl][tl] = add(red[sl][tl], red[sl + h][tl]);
   }
-  red[sl][tl] = make_float2(m, s);
-  __syncthreads();
   if (sl == 0 && t < T) {
-    float top = -INFINITY;
-    for (int q = 0; q < 32; ++q) top = fmaxf(top, red[q][tl].x);
-    float sum = 0.0f;
-    for (int q = 0; q < 32; ++q)
-      sum += red[q][tl].y *
-             (red[q][tl].x == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((red[q][tl].x - top) * kLog2e));
-    const float l = top + __builtin_amdgcn_logf(sum) * kLn2;   // log2
+    const float l = red[0][tl].x + __builtin_amdgcn_logf(red[0][tl].y) * kLn2;   // log2
     lse[t] = l;
     const int64_t c = targets[t];
     loss[t] = c >= 0 && c < classes ? l - zt[t] : 0.0f;
@@ -455,7 +545,7 @@ int64_t up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
 
 template <class S, int EPI>
 hipError_t launch_prod(Prod p, hipStream_t s) {
-  constexpr int bytes = 2 * S::STAGE;
+  constexpr int bytes = S::ST * S::STAGE;
   static std::atomic<uint64_t> lds_set{0};
   const hipError_t e = set_lds_limit((const void*)k_prod<S, EPI>, bytes, lds_set);
   if (e != hipSuccess) return e;
@@ -469,6 +559,19 @@ hipError_t launch_prod(Prod p, hipStream_t s) {
                      bytes, s, p);
   return hipGetLastError();
 }
+
+// The product of the logits: by tokens, see the shapes.
+template <int EPI>
+hipError_t launch_logits(const Prod& p, hipStream_t s) {
+  if (p.N <= 32) return launch_prod<Thin32, EPI>(p, s);
+  if (p.N <= 64) return launch_prod<Thin64, EPI>(p, s);
+  return launch_prod<Big, EPI>(p, s);
+}
+// Rows of the forward statistics for V classes and T tokens.
+int64_t stat_rows(int64_t T, int64_t V) {
+  return T <= 64 ? Thin32::WM * cdiv(V, Thin32::TM) : Big::WM * cdiv(V, Big::TM);
+}
+static_assert(Thin32::TM == Thin64::TM && Thin32::WM == Thin64::WM, "one count for both");
 
 hipError_t launch_turn(const uint16_t* src, int64_t R, int64_t C, int64_t ld, uint16_t* dst,
                        int64_t Rp, int64_t Cp, const XentLaunch* dead, hipStream_t s) {
@@ -484,7 +587,7 @@ hipError_t launch_turn(const uint16_t* src, int64_t R, int64_t C, int64_t ld, ui
 // Backward plan: classes per piece, splits of the dh product, workspace parts.
 XentPlan xent_plan(int64_t T, int64_t V, int64_t D) {
   XentPlan p;
-  p.parts = 2 * cdiv(V, 256);
+  p.parts = stat_rows(T, V);
   p.fwd_bytes = up(8 * p.parts * T, 256) + up(4 * T, 256);
   // one piece holds at most 2^26 elements of G, whole tiles of classes
   int64_t piece = up(V, 256);
@@ -492,7 +595,7 @@ XentPlan xent_plan(int64_t T, int64_t V, int64_t D) {
   if (piece > most) piece = most < 256 ? 256 : most;
   p.pieces = cdiv(V, piece);
   p.piece = piece;
-  p.Tp = up(T, 64);
+  p.Tp = up(T, 8);
   // the dh product has few tiles and a long K: split it until the chip is
   // covered, at least 512 of K each
   const int64_t tiles = cdiv(D, 256) * cdiv(T, 256);
@@ -521,10 +624,16 @@ hipError_t launch_xent_fwd(const XentLaunch& x, hipStream_t s) {
   p.zt = reinterpret_cast<float*>(x.ws + up(8 * pl.parts * x.T, 256));
   p.targets = x.targets;
   p.classes = x.V;
-  hipError_t e = launch_prod<Big, kStats>(p, s);
+  hipError_t e = launch_logits<kStats>(p, s);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(k_xent_join, dim3((unsigned)cdiv(x.T, 8)), dim3(kThreads), 0, s, p.part, p.zt,
-                     x.targets, x.T, x.V, (int)pl.parts, x.loss, x.lse_out);
+  // up to 512 tokens a workgroup each (7 tokens, 1004 rows: 12 us with eight
+  // tokens to a workgroup, whose threads then walk 31 rows), else eight
+  if (x.T <= 512)
+    hipLaunchKernelGGL((k_xent_join<1>), dim3((unsigned)x.T), dim3(kThreads), 0, s, p.part, p.zt,
+                       x.targets, x.T, x.V, (int)pl.parts, x.loss, x.lse_out);
+  else
+    hipLaunchKernelGGL((k_xent_join<8>), dim3((unsigned)cdiv(x.T, 8)), dim3(kThreads), 0, s, p.part,
+                       p.zt, x.targets, x.T, x.V, (int)pl.parts, x.loss, x.lse_out);
   return hipGetLastError();
 }
 
@@ -561,8 +670,9 @@ hipError_t launch_xent_bwd(const XentLaunch& x, hipStream_t s) {
     p.ldo = vp;
     p.m_store = vp;
     p.n_store = x.T;
-    if ((e = launch_prod<Big, kGrad>(p, s)) != hipSuccess) return e;
-    if ((e = launch_turn(G, x.T, vp, vp, GT, pl.Tp, vp, nullptr, s)) != hipSuccess) return e;
+    p.out_t = GT;
+    p.ldt = pl.Tp;
+    if ((e = launch_logits<kGrad>(p, s)) != hipSuccess) return e;
     if ((e = launch_turn(W, vn, x.D, x.ldw, WT, vp, x.D, nullptr, s)) != hipSuccess) return e;
     Prod d = {};
     d.a = WT; d.lda = vp; d.M = x.D;
