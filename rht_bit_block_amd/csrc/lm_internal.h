@@ -55,7 +55,7 @@ struct XentPlan {
   int64_t piece, pieces;         // classes per piece (a multiple of 256), pieces
   int64_t Tp;                    // tokens rounded up to 8
   int32_t splits;                // of the dh product's K
-  int64_t g, gt, wt, ht, slab;   // offsets of the backward workspace's parts
+  int64_t g, gt, wt, ht, slab, scale;   // offsets of the backward workspace's parts
 };
 XentPlan xent_plan(int64_t T, int64_t V, int64_t D);
 hipError_t launch_xent_fwd(const XentLaunch& x, hipStream_t s);

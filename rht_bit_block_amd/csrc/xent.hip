@@ -10,9 +10,13 @@
 // Forward: one product whose 256 x 256 tiles end in a running maximum and sum
 // of exponentials per token instead of a store; a small kernel joins the tiles.
 // Backward, for one piece of the vocabulary after another: the product again,
-// whose tiles end in G (bf16: the operand type of the two products that follow;
-// half a step of rounding per element, averaged over the long sums), then dh
-// += G W in fp32 and dW = G^T h.  Every product runs as C[m][n] = sum_k
+// whose tiles end in G / s (bf16: the operand type of the two products that
+// follow; half a step of rounding per element, averaged over the long sums),
+// then dh += G W in fp32 and dW = G^T h, both times s where they are rounded.
+// s is the largest |dloss|: with the usual equal dloss G / s is p - [v =
+// target], whose heavy entries near -1 round to almost nothing, while the
+// rounding of dloss itself would be the same in every one of them (measured on
+// 8192 tokens: 3.4e-3 of the norm without, 1.8e-3 with s).  Every product runs as C[m][n] = sum_k
 // A[m][k] B[n][k] with both operands K-contiguous, so h, the piece of W and G
 // are also laid out transposed (plain tiled copies, a hundredth of the products'
 // operations' time; G leaves its tiles in both orders).
@@ -76,6 +80,7 @@ struct Prod {
   const float* lse;
   const float* dloss;
   const float* dlse;
+  const float* scale;       // kGrad, kOut: s
   // kGrad, kOut: bf16 [N][ldo], m contiguous, m < m_store written
   uint16_t* out;
   int64_t ldo, m_store, n_store;
@@ -400,7 +405,8 @@ __global__ __launch_bounds__(S::THREADS) void k_prod(Prod p) {
           bt = p.dloss[n];
           at = t - (p.m0 + row0) - mw;
         }
-        a = bt + (p.dlse ? p.dlse[n] : 0.0f);
+        a = (bt + (p.dlse ? p.dlse[n] : 0.0f)) / p.scale[0];
+        bt /= p.scale[0];
         l = p.lse[n];
       }
       const bool none = a == 0.0f && bt == 0.0f;   // whatever its logits hold
@@ -421,6 +427,13 @@ __global__ __launch_bounds__(S::THREADS) void k_prod(Prod p) {
     store_mn<S>(acc, lds, p.out_t + row0 * p.ldt + col0, p.ldt, p.m_store - row0, p.ldt - col0, wm,
                 wn);
   } else if constexpr (EPI == kOut) {
+    const float sc = p.scale[0];
+#pragma unroll
+    for (int i = 0; i < S::NI; ++i)
+#pragma unroll
+      for (int j = 0; j < S::NJ; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] *= sc;
     __syncthreads();
     store_nm<S>(acc, lds, p.out + col0 * p.ldo + row0, p.ldo, p.M - row0, p.N - col0, wm, wn);
   } else {
@@ -520,14 +533,45 @@ __global__ __launch_bounds__(kThreads) void k_turn(const uint16_t* src, int64_t 
   }
 }
 
-// out[n][m] = sum of the slabs, rounded to bf16; 4 elements per thread.
+// s: the largest finite |b| over the tokens, or where that is nothing next to
+// the largest |a| (or 0) that one, or 1; one workgroup.
+__global__ __launch_bounds__(kThreads) void k_xent_scale(const int64_t* targets, int64_t classes,
+                                                         const float* dloss, const float* dlse,
+                                                         int64_t T, float* scale) {
+  __shared__ float red[2][kThreads];
+  float mb = 0.0f, ma = 0.0f;
+  for (int64_t t = threadIdx.x; t < T; t += kThreads) {
+    const int64_t c = targets[t];
+    const float b = c >= 0 && c < classes ? dloss[t] : 0.0f, a = b + (dlse ? dlse[t] : 0.0f);
+    if (fabsf(b) < INFINITY) mb = fmaxf(mb, fabsf(b));
+    if (fabsf(a) < INFINITY) ma = fmaxf(ma, fabsf(a));
+  }
+  red[0][threadIdx.x] = mb;
+  red[1][threadIdx.x] = ma;
+  for (int h = kThreads / 2; h > 0; h /= 2) {
+    __syncthreads();
+    if ((int)threadIdx.x < h)
+      for (int k = 0; k < 2; ++k)
+        red[k][threadIdx.x] = fmaxf(red[k][threadIdx.x], red[k][threadIdx.x + h]);
+  }
+  if (threadIdx.x == 0) {
+    mb = red[0][0];
+    ma = red[1][0];
+    scale[0] = mb > 0.0f && mb >= ma * 0x1p-20f ? mb : ma > 0.0f ? ma : 1.0f;
+  }
+}
+
+// out[n][m] = s times the sum of the slabs, rounded to bf16; 4 elements per
+// thread.
 __global__ __launch_bounds__(kThreads) void k_slab_sum(const float* slab, int64_t N, int64_t M,
-                                                       int splits, uint16_t* out, int64_t ldo) {
+                                                       int splits, const float* scale,
+                                                       uint16_t* out, int64_t ldo) {
   const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
   if (i >= N * M) return;
   f32x4 v = *reinterpret_cast<const f32x4*>(slab + i);
   for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(slab + s * N * M + i);
   const int64_t n = i / M, m = i - n * M;
+  v *= scale[0];
   const u32x2 w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
   *reinterpret_cast<u32x2*>(out + n * ldo + m) = w;
 }
@@ -610,6 +654,7 @@ XentPlan xent_plan(int64_t T, int64_t V, int64_t D) {
   p.wt = take(2 * D * piece);
   p.ht = take(2 * D * p.Tp);
   p.slab = take(4 * (int64_t)p.splits * T * D);
+  p.scale = take(4);
   p.bwd_bytes = at;
   return p;
 }
@@ -649,6 +694,9 @@ hipError_t launch_xent_bwd(const XentLaunch& x, hipStream_t s) {
   uint16_t* WT = reinterpret_cast<uint16_t*>(x.ws + pl.wt);
   uint16_t* HT = reinterpret_cast<uint16_t*>(x.ws + pl.ht);
   float* slab = reinterpret_cast<float*>(x.ws + pl.slab);
+  float* scale = reinterpret_cast<float*>(x.ws + pl.scale);
+  hipLaunchKernelGGL(k_xent_scale, dim3(1), dim3(kThreads), 0, s, x.targets, x.V, x.dloss, x.dlse,
+                     x.T, scale);
   hipError_t e = launch_turn(x.h, x.T, x.D, x.ldh, HT, pl.Tp, x.D, &x, s);
   if (e != hipSuccess) return e;
   int32_t splits = 1;
@@ -666,6 +714,7 @@ hipError_t launch_xent_bwd(const XentLaunch& x, hipStream_t s) {
     p.lse = x.lse;
     p.dloss = x.dloss;
     p.dlse = x.dlse;
+    p.scale = scale;
     p.out = G;
     p.ldo = vp;
     p.m_store = vp;
@@ -686,13 +735,14 @@ hipError_t launch_xent_bwd(const XentLaunch& x, hipStream_t s) {
     w.a = HT; w.lda = pl.Tp; w.M = x.D;
     w.b = GT; w.ldb = pl.Tp; w.N = vn;
     w.K = pl.Tp;
+    w.scale = scale;
     w.out = x.dw + v0 * x.lddw;
     w.ldo = x.lddw;
     if ((e = launch_prod<Big, kOut>(w, s)) != hipSuccess) return e;
     if (c == 0) splits = (int32_t)cdiv(vp, pl.splits == 1 ? vp : up(cdiv(vp, pl.splits), 64));
   }
   hipLaunchKernelGGL(k_slab_sum, dim3((unsigned)cdiv(x.T * x.D, 4 * kThreads)), dim3(kThreads), 0, s,
-                     slab, x.T, x.D, splits, x.dh, x.lddh);
+                     slab, x.T, x.D, splits, scale, x.dh, x.lddh);
   return hipGetLastError();
 }
 
