@@ -43,6 +43,10 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef short i16x2 __attribute__((ext_vector_type(2)));
+// the same at the alignment of their elements (the hardware takes any)
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2u __attribute__((ext_vector_type(2), aligned(1)));
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const f32x2 v = {a, b};
@@ -52,8 +56,10 @@ __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w 
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 // Eight elements at p (n of them inside the row; the others read as 0).  VEC:
-// p is 16-byte aligned and n is 8 or <= 0.  The input is read once, so it
-// does not displace what other kernels left in the caches.
+// p is 16-byte aligned and n is 8 or <= 0; else whole eights are still one or
+// two wide accesses, at the elements' own alignment, and only a row's end goes
+// element by element.  The input is read once, so it does not displace what
+// other kernels left in the caches.
 template <bool F32, bool VEC>
 __device__ __forceinline__ void load8(const void* base, int64_t at, int n, float (&v)[kPer]) {
   if constexpr (VEC) {
@@ -65,6 +71,17 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, int n, float
     } else {
       const u32x4 a = __builtin_nontemporal_load(
           reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(base) + at));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) { v[2 * i] = bf16_lo(a[i]); v[2 * i + 1] = bf16_hi(a[i]); }
+    }
+  } else if (n >= kPer) {
+    if constexpr (F32) {
+      const f32x4u* p = reinterpret_cast<const f32x4u*>(static_cast<const float*>(base) + at);
+      const f32x4u a = p[0], b = p[1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
+    } else {
+      const u32x4u a = *reinterpret_cast<const u32x4u*>(static_cast<const uint16_t*>(base) + at);
 #pragma unroll
       for (int i = 0; i < 4; ++i) { v[2 * i] = bf16_lo(a[i]); v[2 * i + 1] = bf16_hi(a[i]); }
     }
@@ -87,6 +104,8 @@ __device__ __forceinline__ void store8_bf16(uint16_t* base, int64_t at, int n,
                    pack_bf16(v[6], v[7])};
   if constexpr (VEC) {
     *reinterpret_cast<u32x4*>(base + at) = w;
+  } else if (n >= kPer) {
+    *reinterpret_cast<u32x4u*>(base + at) = w;
   } else {
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
@@ -162,6 +181,8 @@ __device__ __forceinline__ void save8(uint8_t* codes, int64_t at, uint8_t* scale
   }
   if constexpr (VEC) {
     if (n > 0) *reinterpret_cast<u32x2*>(codes + at) = w;
+  } else if (n >= kPer) {
+    *reinterpret_cast<u32x2u*>(codes + at) = w;
   } else {
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
@@ -177,6 +198,8 @@ __device__ __forceinline__ void read8(const uint8_t* codes, int64_t at, const ui
   u32x2 w = {0, 0};
   if constexpr (VEC) {
     w = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(codes + at));
+  } else if (n >= kPer) {
+    w = *reinterpret_cast<const u32x2u*>(codes + at);
   } else {
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
