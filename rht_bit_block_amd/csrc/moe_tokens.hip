@@ -407,70 +407,71 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-  auto step = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
-  v = step(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));    // quad 1 0 3 2
-  v = step(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));    // quad 2 3 0 1
-  v = step(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true));   // half-row mirror
-  v = step(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x140, 0xF, 0xF, true));   // row mirror
-  const uint32_t a = step(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16));
-  const uint32_t b = step(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48));
-  return step(a, b);
-}
-
 // --- routing and the rotation of x -----------------------------------------------
-// One wave: the choices of token t into ids[r], share[r], r < k (-1: none).
+// One wave: the choices of token t into ids[r], share[r], r < k (-1: none).  An
+// expert's rank is the number of experts before it: larger logits, and equal
+// ones of lower index.  Every lane counts it for its experts against all others
+// at once.  The code runs once per wave, so its size counts as much as its
+// length: unrolled over 64 experts the instruction fetches took longer than
+// taking the largest k times over.  Q: experts per lane.
+template <int Q>
 __device__ __forceinline__ void route_token(const MoeLaunch& p, int t, int* ids, float* shares) {
-  const int lane = threadIdx.x & 63;
-  constexpr int Q = kMoeMaxExperts / 64;   // expert lane + 64 q in register q
+  const int lane = threadIdx.x & 63;   // expert lane + 64 q in register q
   uint32_t key[Q];
+  int rank[Q];
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
     const int e = lane + 64 * q;
     key[q] = e < p.E ? logit_key(p.logits[(int64_t)t * p.ldl + e]) : 0u;
+    rank[q] = 0;
   }
+#pragma unroll
+  for (int qo = 0; qo < Q; ++qo) {
+#pragma unroll 8
+    for (int j = 0; j < 64; ++j) {
+      const uint32_t other = (uint32_t)__builtin_amdgcn_readlane((int)key[qo], j);
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+        rank[q] += other > key[q] || (other == key[q] && j + 64 * qo < lane + 64 * q) ? 1 : 0;
+    }
+  }
+  // the largest logit is in the lane that holds rank 0
   uint32_t top = 0;
 #pragma unroll
-  for (int q = 0; q < Q; ++q) top = key[q] > top ? key[q] : top;
-  top = wave_max(top);
+  for (int q = 0; q < Q; ++q) {
+    const uint64_t has = __ballot(rank[q] == 0);
+    if (has) top = (uint32_t)__builtin_amdgcn_readlane((int)key[q], __builtin_ctzll(has));
+  }
   const float first = key_logit(top);
-  float den = 0.0f;
-  if (!p.renorm) {
+  float x[Q], den = 0.0f;
+  int chosen = 0;
 #pragma unroll
-    for (int q = 0; q < Q; ++q)
-      if (key[q]) den += __builtin_amdgcn_exp2f((key_logit(key[q]) - first) * kLog2e);
-#pragma unroll
-    for (int m = 32; m > 0; m >>= 1) den += __shfl_xor(den, m);
-  }
-  int id = -1;   // lane r: the r-th choice and its share
-  float share = 0.0f;
-  for (int r = 0; r < p.k; ++r) {
-    uint32_t best = 0;
-#pragma unroll
-    for (int q = 0; q < Q; ++q) best = key[q] > best ? key[q] : best;
-    best = wave_max(best);
-    if (best == 0) break;
-    int e = -1;
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {   // ascending: the lowest index of a tie
-      const uint64_t has = __ballot(key[q] == best);
-      if (e < 0 && has) {
-        const int l = __builtin_ctzll(has);
-        e = l + 64 * q;
-        if (lane == l) key[q] = 0;
-      }
+  for (int q = 0; q < Q; ++q) {
+    const bool in = key[q] != 0 && rank[q] < p.k;
+    x[q] = 0.0f;
+    if (key[q] != 0) {
+      x[q] = __builtin_amdgcn_exp2f((key_logit(key[q]) - first) * kLog2e);
+      if (in || !p.renorm) den += x[q];
     }
-    const float x = __builtin_amdgcn_exp2f((key_logit(best) - first) * kLog2e);
-    if (p.renorm) den += x;
-    if (lane == r) {
-      id = e;
-      share = x;
+    chosen += __builtin_popcountll(__ballot(in));
+  }
+#pragma unroll
+  for (int m = 32; m > 0; m >>= 1) den += __shfl_xor(den, m);
+#pragma unroll
+  for (int q = 0; q < Q; ++q)
+    if (key[q] != 0 && rank[q] < p.k) {
+      ids[rank[q]] = lane + 64 * q;
+      shares[rank[q]] = x[q] / den;
     }
+  if (lane >= chosen && lane < p.k) {
+    ids[lane] = -1;
+    shares[lane] = 0.0f;
   }
-  if (lane < p.k) {
-    ids[lane] = id;
-    shares[lane] = id >= 0 ? share / den : 0.0f;
-  }
+}
+
+__device__ __forceinline__ void route(const MoeLaunch& p, int t, int* ids, float* shares) {
+  if (p.E <= 64) route_token<1>(p, t, ids, shares);
+  else route_token<kMoeMaxExperts / 64>(p, t, ids, shares);
 }
 
 // One butterfly of eight values with the lane whose number differs in bit M:
@@ -569,7 +570,7 @@ __device__ __forceinline__ void load_x8(const uint16_t* x, bool in, int64_t i, f
 __global__ __launch_bounds__(kRouteThreads) void k_moe_route(MoeLaunch p) {
   const int64_t t = blockIdx.x, i = (int64_t)blockIdx.y * kRouteThreads + threadIdx.x;
   if (blockIdx.y == 0 && threadIdx.x < 64)
-    route_token(p, (int)t, p.ids + t * p.k, p.share + t * p.k);
+    route(p, (int)t, p.ids + t * p.k, p.share + t * p.k);
   const bool in = i < p.H / 8;
   float v[8];
   load_x8(p.x + t * p.ldx, in, i, v);
@@ -665,12 +666,12 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_up(MoeLaunch p) {
   const float* shares = p.share;
   if constexpr (FUSED) {
     for (int t = wave; t < p.T; t += kWaves)
-      route_token(p, t, ids_here + t * p.k, share_here + t * p.k);
+      route(p, t, ids_here + t * p.k, share_here + t * p.k);
     // the waves that route take the last part of x
     const int bytes = fused_row(p.H);
     for (int t = 0; t < p.T; ++t)
-      for (int64_t i0 = 0; i0 < p.H / 8; i0 += kThreads) {
-        const int64_t i = i0 + (kWaves - 1 - wave) * 64 + lane;
+      for (int64_t i0 = (kWaves - 1 - wave) * 64; i0 < p.H / 8; i0 += kThreads) {
+        const int64_t i = i0 + lane;
         const bool in = i < p.H / 8;
         float v[8];
         load_x8(p.x + t * p.ldx, in, i, v);
@@ -821,9 +822,19 @@ __global__ __launch_bounds__(kRouteThreads) void k_moe_join(MoeLaunch p) {
   const int64_t col = 2 * ((int64_t)blockIdx.x * kRouteThreads + threadIdx.x), t = blockIdx.y;
   if (col >= p.H) return;
   f32x2 v = {0.0f, 0.0f};
-  for (int r = 0; r < p.k; ++r) {
-    const int at = p.place[t * p.k + r];
-    if (at >= 0) v += *reinterpret_cast<const f32x2*>(p.partial + (int64_t)at * p.H + col);
+  for (int r0 = 0; r0 < p.k; r0 += 8) {   // eight rows in flight
+    int at[8];
+    f32x2 part[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) at[r] = r0 + r < p.k ? p.place[t * p.k + r0 + r] : -1;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      part[r] = f32x2{0.0f, 0.0f};
+      if (at[r] >= 0)
+        part[r] = *reinterpret_cast<const f32x2*>(p.partial + (int64_t)at[r] * p.H + col);
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r) v += part[r];
   }
   *reinterpret_cast<uint32_t*>(p.y + t * p.ldy + col) =
       pack_bf16(v[0] * p.wd.factor, v[1] * p.wd.factor);
