@@ -92,7 +92,7 @@ struct MoeLaunch {
   uint32_t sign_x[4], sign_h[4];   // sign bits of 128 consecutive elements
   // set by moe_plan
   int32_t by_pair, fused, slots;   // slots: the T k choices, or all experts if fewer
-  int32_t run_up, run_down;        // columns per workgroup of the two products
+  int32_t run_up, run_down;        // pairs of tiles per workgroup of the two products
   int* ids;                // [T][k] chosen experts, -1: none
   float* share;            // [T][k]
   int* expert;             // [slots] a slot's expert

@@ -9,11 +9,11 @@
 // dimension ([UFP4] Method: it cancels in the product); the activations stay
 // in high precision.  Few tokens mean that reading the chosen experts' codes
 // and scales is all that costs: the kernels stream them once, 16 bytes per
-// lane, straight from HBM into registers, and everything else is sized to
+// lane, straight from HBM into shared memory, and everything else is sized to
 // hide behind that.
 //
 // Launches:
-//   k_moe_up     one workgroup per chosen expert and run of NF columns: both
+//   k_moe_up     one workgroup per chosen expert and run of columns: both
 //                products, the activation and the weight p.  For a handful of
 //                tokens the routing and the rotation of x run in front, in
 //                every workgroup; otherwise k_moe_route has done both once.
@@ -37,6 +37,7 @@
 // and the address unit, not HBM, set the pace (200 us against 66 for the up
 // product of 16 tokens).  The activations of the workgroup's tokens lie in LDS,
 // 28 KB of them at a time.
+#include <cmath>
 #include <type_traits>
 
 #include "lds_copy.h"
@@ -318,14 +319,27 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)p;
 }
 
+// What a wave of a workgroup with `pairs` pairs of tiles does: of pair pt the
+// steps ks, ks + shares, .. of K.  Waves that are left over only help to fill.
+struct Share {
+  int pt, ks, shares;
+  bool works;
+};
+__device__ __forceinline__ Share share_of(int wave, int pairs) {
+  // kWaves / pairs and wave / pairs, by tables of the quotients and of 64 / pairs
+  // rounded up
+  const int shares = (int)(0x11112248u >> (4 * (pairs - 1)) & 15);
+  const int ks = wave * (int)(0x080A0B0D10162040ull >> (8 * (pairs - 1)) & 255) >> 6;
+  return Share{wave - ks * pairs, ks, shares, ks < shares};
+}
+
 // acc += the product over K of a workgroup's two tiles per wave (src) with its
-// tokens.  The waves are PT tile pairs times KS shares of K: a wave takes steps
-// ks, ks + KS, ..  fill(first block, blocks) puts the activations of a range of
-// K into `acts`, one range after another (what kActBytes hold).
-template <int GRID, int SK, int TT, int KS, class Fill>
+// tokens.  fill(first block, blocks) puts the activations of a range of K into
+// `acts`, one range after another (what kActBytes hold).
+template <int GRID, int SK, int TT, class Fill>
 __device__ __forceinline__ void product(f32x4 (&acc)[2][TT], const TileSource (&src)[2],
                                         uint8_t* acts, uint8_t* ring, const int (&arow)[TT],
-                                        int row_bytes, int range, int nb, int ks, Fill fill) {
+                                        int row_bytes, int range, int nb, const Share& w, Fill fill) {
   const int lane = threadIdx.x & 63;
   const int steps = (nb + 3) / 4;
   const uint32_t ring0 = lds_addr(ring);
@@ -334,23 +348,24 @@ __device__ __forceinline__ void product(f32x4 (&acc)[2][TT], const TileSource (&
   // bytes that nothing reads, and keep the count of loads in flight
   auto copy = [&](int i) {
     const uint32_t to = ring0 + (uint32_t)(i % kRing) * (2 * tile_bytes<SK>());
-    int step = ks + i * KS;
+    int step = w.ks + i * w.shares;
     if (step >= steps) step = steps - 1;
 #pragma unroll
     for (int m = 0; m < 2; ++m) copy_tile<SK>(src[m], to + m * tile_bytes<SK>(), step, lane);
   };
 #pragma unroll
-  for (int i = 0; i < kRing - 1; ++i) copy(i);
+  for (int i = 0; i < kRing - 1; ++i)
+    if (w.works) copy(i);
   int i = 0;
   for (int b0 = 0; b0 < nb; b0 += range) {
     const int bn = nb - b0 < range ? nb - b0 : range;
     if (b0) __syncthreads();   // everyone has read the range before
     fill(b0, bn);
     __syncthreads();
-    for (; ks + i * KS < (b0 + bn + 3) / 4; ++i) {
+    for (; w.works && w.ks + i * w.shares < (b0 + bn + 3) / 4; ++i) {
       copy(i + kRing - 1);
       wait_vmcnt<(kRing - 1) * kCopies>();   // step i is there; later ones need not be
-      const int step = ks + i * KS;
+      const int step = w.ks + i * w.shares;
       const uint8_t* from = ring + (i % kRing) * (2 * tile_bytes<SK>());
       const uint8_t* a = acts + 512 * (step - b0 / 4);
       if (4 * step + 4 <= nb)
@@ -365,20 +380,20 @@ __device__ __forceinline__ void product(f32x4 (&acc)[2][TT], const TileSource (&
   __syncthreads();
 }
 
-// The shares of K added in order: part[matrix][token][RUN columns].
-template <int TT, int KS, int RUN>
-__device__ __forceinline__ void join_shares(const f32x4 (&acc)[2][TT], float* part, int pt, int ks) {
+// The shares of K added in order: part[pair][matrix][token][16 columns].
+template <int TT>
+__device__ __forceinline__ void join_shares(const f32x4 (&acc)[2][TT], float* part, const Share& w) {
   const int lane = threadIdx.x & 63, g = lane >> 4, r16 = lane & 15;
   constexpr int ROWS = TT * 16;
-  for (int s = 0; s < KS; ++s) {
-    if (ks == s) {
+  for (int s = 0; s < w.shares; ++s) {
+    if (w.ks == s) {
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int t = 0; t < TT; ++t)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            float* d = part + (q * ROWS + t * 16 + 4 * g + r) * RUN + pt * 16 + r16;
+            float* d = part + ((w.pt * 2 + q) * ROWS + t * 16 + 4 * g + r) * 16 + r16;
             *d = s == 0 ? acc[q][t][r] : *d + acc[q][t][r];
           }
     }
@@ -590,18 +605,18 @@ __device__ __forceinline__ int range_of(int m, int nb) {
 }
 
 // --- gate and up products, activation ---------------------------------------------
-// NF: columns of the intermediate that a workgroup computes, 16 per pair of a
-// gate and an up tile.  Tokens first .. first + m - 1 of the expert's; FUSED: x is
+// A workgroup computes `pairs` times 16 columns of the intermediate from f0 on,
+// each a pair of a gate and an up tile.  Tokens first .. first + m - 1 of the expert's; FUSED: x is
 // in LDS already, row t for token t.
-template <int GRID, int SK, int NF, int TT, bool FUSED>
-__device__ __forceinline__ void moe_up_body(const MoeLaunch& p, int slot, int e, int f0, int first,
-                                            int m, const int* tok, const float* share,
+template <int GRID, int SK, int TT, bool FUSED>
+__device__ __forceinline__ void moe_up_body(const MoeLaunch& p, int slot, int e, int f0, int pairs,
+                                            int first, int m, const int* tok, const float* share,
                                             uint8_t* lds) {
-  constexpr int PT = NF / 16, KS = kWaves / PT;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int pt = wave % PT, ks = wave / PT, r16 = lane & 15;
+  const int r16 = lane & 15;
+  const Share w = share_of(wave, pairs);
   const int nb = (int)(p.H / 32);
-  const int64_t row0 = (int64_t)e * p.F + f0 + pt * 16;
+  const int64_t row0 = (int64_t)e * p.F + f0 + w.pt * 16;
   const TileSource src[2] = {tile_source<SK>(p.wg, row0, p.H, lane),
                              tile_source<SK>(p.wu, row0, p.H, lane)};
   uint8_t* acts = lds;
@@ -618,13 +633,13 @@ __device__ __forceinline__ void moe_up_body(const MoeLaunch& p, int slot, int e,
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[q][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   if constexpr (FUSED) {
-    product<GRID, SK, TT, KS>(acc, src, acts, ring, arow, fused_row(p.H), nb, nb, ks,
-                              [](int, int) {});
+    product<GRID, SK, TT>(acc, src, acts, ring, arow, fused_row(p.H), nb, nb, w,
+                          [](int, int) {});
   } else {
     const int range = range_of(m, nb);
     const sgpr4 xr = rsrc4(p.xr, (uint32_t)(p.T * p.H * 4));
     const uint32_t to = lds_addr(acts);
-    product<GRID, SK, TT, KS>(acc, src, acts, ring, arow, range * 128, range, nb, ks, [&](int b0, int) {
+    product<GRID, SK, TT>(acc, src, acts, ring, arow, range * 128, range, nb, w, [&](int b0, int) {
       // rows of 128 range bytes, 512 bytes per half wave; past K nothing is read
       const int per_row = range / 4, halves = m * per_row, hl = lane & 31;
       for (int c = 2 * wave; c < halves; c += 2 * kWaves) {
@@ -638,12 +653,15 @@ __device__ __forceinline__ void moe_up_body(const MoeLaunch& p, int slot, int e,
     });
   }
   float* part = reinterpret_cast<float*>(lds);
-  join_shares<TT, KS, NF>(acc, part, pt, ks);
+  join_shares<TT>(acc, part, w);
   constexpr int ROWS = TT * 16;
-  for (int i = tid; i < m * NF; i += kThreads) {
-    const float a = part[i] * p.wg.factor, b = part[ROWS * NF + i] * p.wu.factor;
+  const int col = tid % (16 * kWaves);   // of 16 pairs columns
+  for (int row = tid / (16 * kWaves); row < m; row += kThreads / (16 * kWaves)) {
+    if (col >= 16 * pairs) continue;
+    const float* at = part + ((col >> 4) * 2 * ROWS + row) * 16 + (col & 15);
+    const float a = at[0] * p.wg.factor, b = at[ROWS * 16] * p.wu.factor;
     const float s = p.act == UFP4_ACT_GELU ? activation<1>(a) : activation<0>(a);
-    p.h[((int64_t)slot * p.T + first + i / NF) * p.F + f0 + i % NF] = s * b * share[i / NF];
+    p.h[((int64_t)slot * p.T + first + row) * p.F + f0 + col] = s * b * share[row];
   }
   if constexpr (TT > 1) __syncthreads();   // the next tokens' activations go where `part` is
 }
@@ -651,7 +669,7 @@ __device__ __forceinline__ void moe_up_body(const MoeLaunch& p, int slot, int e,
 // FUSED: routing and rotation here, for a few tokens.  WIDE: an expert may have
 // more than 16 tokens.
 enum { kFused = 0, kNarrow = 1, kWide = 2 };
-template <int GRID, int SK, int NF, int MODE>
+template <int GRID, int SK, int MODE>
 __global__ __launch_bounds__(kThreads, 4) void k_moe_up(MoeLaunch p) {
   constexpr bool FUSED = MODE == kFused;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -731,9 +749,11 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_up(MoeLaunch p) {
   const int e = __builtin_amdgcn_readfirstlane(found[0]);
   const int m = __builtin_amdgcn_readfirstlane(found[1]);
   if (m == 0) return;
+  const int pair0 = fc * p.run_up, left = (int)(p.F / 16) - pair0;
+  const int pairs = left < p.run_up ? left : p.run_up;
   auto body = [&](auto tt, int first, int n) {
-    moe_up_body<GRID, SK, NF, decltype(tt)::value, FUSED>(p, slot, e, fc * NF, first, n, tok + first,
-                                                          share + first, lds);
+    moe_up_body<GRID, SK, decltype(tt)::value, FUSED>(p, slot, e, 16 * pair0, pairs, first, n,
+                                                      tok + first, share + first, lds);
   };
   if (MODE != kWide || m <= 16) {
     body(std::integral_constant<int, 1>{}, 0, m);
@@ -743,18 +763,18 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_up(MoeLaunch p) {
 }
 
 // --- down product --------------------------------------------------------------------
-// RUN: output columns per workgroup, 32 per pair of tiles.  hrow: the tokens' first
-// row of the intermediate and of the results.
-template <int GRID, int SK, int RUN, int TT>
+// A workgroup computes `pairs` times 32 output columns from col0 on, each a pair of
+// tiles.  hrow: the tokens' first row of the intermediate and of the results.
+template <int GRID, int SK, int TT>
 __device__ __forceinline__ void moe_down_body(const MoeLaunch& p, int64_t hrow, int e, int m,
-                                              int64_t col0, uint8_t* lds) {
-  constexpr int PT = RUN / 32, KS = kWaves / PT;
+                                              int64_t col0, int pairs, uint8_t* lds) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int pt = wave % PT, ks = wave / PT, r16 = lane & 15;
+  const int r16 = lane & 15;
+  const Share w = share_of(wave, pairs);
   const int nb = (int)(p.F / 32);
-  const int64_t row0 = (int64_t)e * p.H + col0 + pt * 16;   // and RUN / 2 further on
+  const int64_t row0 = (int64_t)e * p.H + col0 + w.pt * 32;
   const TileSource src[2] = {tile_source<SK>(p.wd, row0, p.F, lane),
-                             tile_source<SK>(p.wd, row0 + RUN / 2, p.F, lane)};
+                             tile_source<SK>(p.wd, row0 + 16, p.F, lane)};
   uint8_t* acts = lds;
   uint8_t* ring = lds + kActBytes + wave * ring_bytes<SK>();
   int arow[TT];
@@ -769,7 +789,7 @@ __device__ __forceinline__ void moe_down_body(const MoeLaunch& p, int64_t hrow, 
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[q][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   const int range = range_of(m, nb);
-  product<GRID, SK, TT, KS>(acc, src, acts, ring, arow, range * 128, range, nb, ks, [&](int b0, int bn) {
+  product<GRID, SK, TT>(acc, src, acts, ring, arow, range * 128, range, nb, w, [&](int b0, int bn) {
     // one row after another, 64 times 8 neighbouring elements per wave
     const int groups = 4 * bn, runs = (groups + 63) / 64;
     for (int c = wave; c < m * runs; c += kWaves) {
@@ -790,25 +810,26 @@ __device__ __forceinline__ void moe_down_body(const MoeLaunch& p, int64_t hrow, 
     }
   });
   float* part = reinterpret_cast<float*>(lds);
-  constexpr int HALF = RUN / 2, ROWS = TT * 16;
-  join_shares<TT, KS, HALF>(acc, part, pt, ks);
-  for (int i = tid; i < m * HALF; i += kThreads) {
-    float* o = p.partial + (hrow + i / HALF) * p.H + col0 + i % HALF;
-    o[0] = part[i];
-    o[HALF] = part[ROWS * HALF + i];
-  }
+  constexpr int ROWS = TT * 16;
+  join_shares<TT>(acc, part, w);
+  const int col = tid % (32 * kWaves);   // of 32 pairs columns
+  for (int row = tid / (32 * kWaves); row < m; row += kThreads / (32 * kWaves))
+    if (col < 32 * pairs)
+      p.partial[(hrow + row) * p.H + col0 + col] = part[((col >> 4) * ROWS + row) * 16 + (col & 15)];
   if constexpr (TT > 1) __syncthreads();   // the next tokens' activations go where `part` is
 }
 
-template <int GRID, int SK, int RUN, bool WIDE>
+template <int GRID, int SK, bool WIDE>
 __global__ __launch_bounds__(kThreads, 4) void k_moe_down(MoeLaunch p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int slot = blockIdx.y;
   const int m = p.count[slot], e = p.expert[slot];
   if (m == 0) return;
+  const int pair0 = (int)blockIdx.x * p.run_down, left = (int)(p.H / 32) - pair0;
+  const int pairs = left < p.run_down ? left : p.run_down;
   auto body = [&](auto tt, int first, int n) {
-    moe_down_body<GRID, SK, RUN, decltype(tt)::value>(p, (int64_t)slot * p.T + first, e, n,
-                                                      (int64_t)blockIdx.x * RUN, lds);
+    moe_down_body<GRID, SK, decltype(tt)::value>(p, (int64_t)slot * p.T + first, e, n,
+                                                 32 * (int64_t)pair0, pairs, lds);
   };
   if (!WIDE || m <= 16) {
     body(std::integral_constant<int, 1>{}, 0, m);
@@ -846,16 +867,16 @@ template <int SK> constexpr int lds_bytes() { return kActBytes + kWaves * ring_b
 static_assert(lds_bytes<kE8b32>() >= 2 * 128 * 32 * 4, "the shares of K fit");
 static_assert(kActBytes >= 32 * 512, "one step of 32 tokens fits");
 
-template <int GRID, int SK, int NF>
-hipError_t launch_up_n(const MoeLaunch& p, hipStream_t s) {
-  const dim3 grid((unsigned)(p.F / NF), (unsigned)p.slots);
+template <int GRID, int SK>
+hipError_t launch_up(const MoeLaunch& p, hipStream_t s) {
+  const dim3 grid((unsigned)((p.F / 16 + p.run_up - 1) / p.run_up), (unsigned)p.slots);
   auto go = [&](auto mode) {
     constexpr int MODE = decltype(mode)::value;
     static std::atomic<uint64_t> lds_set{0};
     const hipError_t e =
-        set_lds_limit((const void*)k_moe_up<GRID, SK, NF, MODE>, lds_bytes<SK>(), lds_set);
+        set_lds_limit((const void*)k_moe_up<GRID, SK, MODE>, lds_bytes<SK>(), lds_set);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_moe_up<GRID, SK, NF, MODE>), grid, dim3(kThreads), lds_bytes<SK>(), s, p);
+    hipLaunchKernelGGL((k_moe_up<GRID, SK, MODE>), grid, dim3(kThreads), lds_bytes<SK>(), s, p);
     return hipGetLastError();
   };
   if (p.fused) return go(std::integral_constant<int, kFused>{});
@@ -863,34 +884,20 @@ hipError_t launch_up_n(const MoeLaunch& p, hipStream_t s) {
                    : go(std::integral_constant<int, kWide>{});
 }
 
-template <int GRID, int SK, int RUN>
-hipError_t launch_down_n(const MoeLaunch& p, hipStream_t s) {
-  const dim3 grid((unsigned)(p.H / RUN), (unsigned)p.slots);
+template <int GRID, int SK>
+hipError_t launch_down(const MoeLaunch& p, hipStream_t s) {
+  const dim3 grid((unsigned)((p.H / 32 + p.run_down - 1) / p.run_down), (unsigned)p.slots);
   auto go = [&](auto wide) {
     constexpr bool WIDE = decltype(wide)::value;
     static std::atomic<uint64_t> lds_set{0};
     const hipError_t e =
-        set_lds_limit((const void*)k_moe_down<GRID, SK, RUN, WIDE>, lds_bytes<SK>(), lds_set);
+        set_lds_limit((const void*)k_moe_down<GRID, SK, WIDE>, lds_bytes<SK>(), lds_set);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_moe_down<GRID, SK, RUN, WIDE>), grid, dim3(kThreads), lds_bytes<SK>(), s,
+    hipLaunchKernelGGL((k_moe_down<GRID, SK, WIDE>), grid, dim3(kThreads), lds_bytes<SK>(), s,
                        p);
     return hipGetLastError();
   };
   return p.T <= 16 ? go(std::false_type{}) : go(std::true_type{});
-}
-
-template <int GRID, int SK>
-hipError_t launch_up(const MoeLaunch& p, hipStream_t s) {
-  if (p.run_up == 32) return launch_up_n<GRID, SK, 32>(p, s);
-  if (p.run_up == 64) return launch_up_n<GRID, SK, 64>(p, s);
-  return launch_up_n<GRID, SK, 128>(p, s);
-}
-
-template <int GRID, int SK>
-hipError_t launch_down(const MoeLaunch& p, hipStream_t s) {
-  if (p.run_down == 32) return launch_down_n<GRID, SK, 32>(p, s);
-  if (p.run_down == 64) return launch_down_n<GRID, SK, 64>(p, s);
-  return launch_down_n<GRID, SK, 128>(p, s);
 }
 
 template <typename F>
@@ -915,16 +922,27 @@ int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 
 }  // namespace
 
-// Columns per workgroup, of `cols`: a round of workgroups (two to a compute unit)
-// costs about its columns and, for routing, activations and joining, as much
-// as 64 columns more; the width whose rounds cost least, of equals the widest.
-int32_t run_width(int64_t cols, int64_t slots) {
-  constexpr int64_t kUnits = 2 * 256, kFixed = 64;
-  int32_t best = 32;
-  int64_t least = INT64_MAX;
-  for (int32_t w = 32; w <= 128; w *= 2) {
-    if (cols % w) break;
-    const int64_t cost = (cols / w * slots + kUnits - 1) / kUnits * (w + kFixed);
+// Pairs of tiles per workgroup, of `pairs` of each expert, where `experts` of them
+// have `tokens` each, in the mean.  The cost, in the time that a compute unit
+// takes for a pair: the fullest unit's workgroups, each with its pairs (half of one
+// more where there are three: two waves have nothing to do) and a fixed part for
+// routing, joining and the tokens' activations; and once the time that a wave
+// takes for its share of K with the unit to itself.  Three pairs have the two
+// shares of four, and pay for K long enough that the first copies' latency does not
+// count (down product of K = 1408, two tokens: 11.4 with 2, 15.4 with 3).  Of equals
+// the most pairs.
+// Measured, in us with 2 / 3 / 4 / 8 pairs: up product, 16 experts of 5120 x 1536
+// and 16 tokens: 65.7 / 61.4 / 67.2 / 69.8; 64 of 2048 x 1408, 16 tokens: 56.0 / 60.4 /
+// 55.1 / 68.1; 61 tokens: 74.8 / 68.5 / 62.0 / 58.4, and its down product 49.9 /
+// 46.1 / 39.0 / 35.6.
+int32_t run_pairs(int64_t pairs, int64_t K, double experts, double tokens) {
+  constexpr double kUnits = 256;
+  int32_t best = 1;
+  double least = 1e300;
+  for (int32_t w : {1, 2, 3, 4, 8}) {
+    if (w == 3 && K < 24 * 128) continue;
+    const double per_unit = std::ceil((double)((pairs + w - 1) / w) * experts / kUnits - 0.04);
+    const double cost = per_unit * (w + (w == 3 ? 0.5 : 0.0) + 1.5 + tokens / 8) + 4.0 / (kWaves / w);
     if (cost <= least) {
       least = cost;
       best = w;
@@ -939,8 +957,13 @@ int64_t moe_plan(MoeLaunch& p, uint8_t* ws) {
   p.by_pair = pairs < p.E;
   p.slots = (int32_t)(p.by_pair ? pairs : p.E);
   p.fused = p.T <= kMoeFusedTokens && p.T * fused_row(p.H) <= kActBytes;
-  p.run_up = run_width(p.F, p.slots);
-  p.run_down = run_width(p.H, p.slots);
+  // distinct experts that T evenly spread choices of k meet
+  double miss = 1.0;
+  for (int64_t t = 0; t < p.T; ++t) miss *= 1.0 - (double)p.k / (double)p.E;
+  const double experts = (1.0 - miss) * (double)p.E;
+  const double tokens = experts > 0.0 ? (double)pairs / experts : 0.0;
+  p.run_up = run_pairs(p.F / 16, p.H, experts, tokens);
+  p.run_down = run_pairs(p.H / 32, p.F, experts, tokens);
   int64_t at = 0;
   auto take = [&](int64_t bytes) {
     uint8_t* q = ws ? ws + at : nullptr;
