@@ -349,3 +349,40 @@ def test_moe_binding_refusals():
         U.ufp4_moe_tokens(x, lg[:3], *w, 2)
     with pytest.raises(ValueError, match="contracts"):
         U.ufp4_moe_tokens(x[:, :32], lg, *w, 2)
+
+
+class _Cycle:
+    """The rows of a few experts, repeated for all."""
+
+    def __init__(self, v, rows, experts):
+        self.v, self.rows, self.experts = v, rows, experts
+
+    def __getitem__(self, s):
+        e = s.start // self.rows % self.experts
+        return self.v[e * self.rows:(e + 1) * self.rows]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k,H,F", [
+    (33, 16, 4, 3200, 1472), (17, 32, 8, 512, 800), (34, 64, 4, 512, 800), (3, 32, 4, 1024, 1024)])
+def test_moe_runs(T, E, k, H, F):
+    """Sizes at which a workgroup takes two, three, four or eight pairs of tiles,
+    the last one of an expert fewer. Over such long sums the elementwise bound is
+    wide; the error of the whole is below a bf16 rounding of every element and, for
+    all that is summed in fp32 and split in two pieces, (K + 16) 2^-24 < 2^-12 and
+    2^-16 of the whole per product, together below 2^-10."""
+    print("case: moe runs", T, E, k, H, F, flush=True)
+    cfg, dcfg = mk(U.UFP4_INT4, 32, 32, 5), mk(U.UFP4_E2M1, 32, 16, 6, True)
+    some = 3
+    q, v = build(some, H, F, cfg, dcfg, T)
+    turns = (E + some - 1) // some
+    q = [U.QTensor(w.codes.repeat(turns, 1)[:E * P], w.scales.repeat(turns, 1)[:E * P], E * P, w.K, c)
+         for w, P, c in zip(q, (F, F, H), (cfg, cfg, dcfg))]
+    x, logits = inputs(T, E, H, 7)
+    y = U.ufp4_moe_tokens(x.cuda(), logits.cuda(), *q, k)
+    torch.cuda.synchronize()
+    v = [_Cycle(w, P, some) for w, P in zip(v, (F, F, H))]
+    v[2].shape = (E * H, F)
+    want, tol = formulas(x, logits, *v, cfg, dcfg, k, True, U.UFP4_ACT_SILU)
+    check(y, want, tol)
+    assert (y.double().cpu() - want).norm() <= (BF16 + 2.0 ** -10) * want.norm()
