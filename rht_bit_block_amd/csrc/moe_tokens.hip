@@ -419,9 +419,10 @@ __device__ __forceinline__ float activation(float g) {
   return g * (y < 0.0f ? t * p : p);
 }
 
-// Order-preserving key of a float, 0 for what is never chosen.
+// Order-preserving key of a float, 0 for what is never chosen; equal logits have
+// equal keys (the sum turns -0 into +0).
 __device__ __forceinline__ uint32_t logit_key(float l) {
-  const uint32_t b = __float_as_uint(l);
+  const uint32_t b = __float_as_uint(l + 0.0f);
   return l > -INFINITY ? (b & 0x80000000u ? ~b : b | 0x80000000u) : 0u;
 }
 __device__ __forceinline__ float key_logit(uint32_t k) {

@@ -386,3 +386,29 @@ def test_moe_runs(T, E, k, H, F):
     want, tol = formulas(x, logits, *v, cfg, dcfg, k, True, U.UFP4_ACT_SILU)
     check(y, want, tol)
     assert (y.double().cpu() - want).norm() <= (BF16 + 2.0 ** -10) * want.norm()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 12])
+@pytest.mark.parametrize("E", [8, 64, 70, 130])
+def test_moe_signed_zeros_tie(E, T):
+    """-0 and +0 are equal logits, so the lower index is chosen of the two, on
+    both sides of the 64 experts that one register per lane holds and with
+    routing inside the up product (few tokens) or in front of it."""
+    print("case: moe signed zeros", E, T, flush=True)
+    H, F = 64, 32
+    cfg, dcfg = mk(U.UFP4_INT4, 32, 32, 5), mk(U.UFP4_INT4, 32, 32, 6)
+    q, v = build(E, H, F, cfg, dcfg, 3)
+    x, logits = inputs(T, E, H, 4)
+    logits[0] = 0.0
+    logits[0, ::2] = -0.0                                   # -0 +0 -0 +0 ..
+    logits[1] = 0.0
+    logits[1, 1::2] = -0.0                                  # +0 -0 +0 -0 ..
+    logits[2] = -1.0
+    logits[2, [2, E - 2]] = -0.0
+    logits[2, [5, E - 1]] = 0.0                             # -> 2, 5, E - 2 in this order
+    for k in (1, 2, 3):
+        for renorm in (True, False):
+            y = U.ufp4_moe_tokens(x.cuda(), logits.cuda(), *q, k, renorm=renorm)
+            torch.cuda.synchronize()
+            check(y, *formulas(x, logits, *v, cfg, dcfg, k, renorm, U.UFP4_ACT_SILU))
