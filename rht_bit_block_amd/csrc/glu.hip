@@ -319,11 +319,11 @@ template <typename F> auto pick2(bool a, bool b, F f) {
            : (b ? f(std::false_type{}, std::true_type{}) : f(std::false_type{}, std::false_type{}));
 }
 
-// Launches over at most 2^30 threads each: `rows` at a time.
+// Launches of at most 2^30 threads each (HIP takes fewer than 2^32), `threads` for
+// a row: some rows at a time.
 template <typename F>
-hipError_t in_slices(const GluLaunch& g, uint32_t chunks, F one) {
-  const int64_t most = chunks > 0 ? ((int64_t)1 << 30) / chunks : (int64_t)1 << 30;
-  const int64_t step = most < 1 ? 1 : most;
+hipError_t in_slices(const GluLaunch& g, uint32_t chunks, uint32_t threads, F one) {
+  const int64_t step = ((int64_t)1 << 30) / threads;   // chunks <= 2^27
   const int64_t es = g.dtype == UFP4_BF16 ? 2 : 4, blocks = chunks / 4;
   for (int64_t r = 0; r < g.rows; r += step) {
     GluLaunch p = g;
@@ -363,7 +363,7 @@ hipError_t launch_glu_fwd(const GluLaunch& g, hipStream_t s) {
                    vec_ok(g.h, g.ldh, 2) &&
                    (!save || ((uintptr_t)g.gate_codes % 8 == 0 && (uintptr_t)g.up_codes % 8 == 0));
   const FastDiv div = make_fastdiv(chunks);
-  return in_slices(g, chunks, [&](const GluLaunch& p) {
+  return in_slices(g, chunks, chunks, [&](const GluLaunch& p) {
     const uint32_t total = (uint32_t)(p.rows * chunks);
     const dim3 grid((total + kThreads - 1) / kThreads);
     pick2(g.dtype != UFP4_BF16, vec, [&](auto f32, auto v) {
@@ -383,8 +383,8 @@ hipError_t launch_glu_bwd(const GluLaunch& g, hipStream_t s) {
                    vec_ok(g.dup, g.ldd, 2) && (!g.h || vec_ok(g.h, g.ldh, 2)) &&
                    (uintptr_t)g.gate_codes % 8 == 0 && (uintptr_t)g.up_codes % 8 == 0;
   const FastDiv div = make_fastdiv(chunks > 0 ? chunks : 1);
-  return in_slices(g, chunks, [&](const GluLaunch& p) {
-    const uint32_t total = (uint32_t)(p.rows * chunks);
+  return in_slices(g, chunks, g.drow ? 64 : chunks, [&](const GluLaunch& p) {
+    const uint32_t total = (uint32_t)(p.rows * chunks);   // unused with a wave per row
     pick2(g.dtype != UFP4_BF16, vec, [&](auto f32, auto v) {
       pick2(g.act == UFP4_ACT_GELU, g.h != nullptr, [&](auto gelu, auto ag) {
         constexpr bool F = decltype(f32)::value, V = decltype(v)::value, A = decltype(ag)::value;
@@ -393,7 +393,7 @@ hipError_t launch_glu_bwd(const GluLaunch& g, hipStream_t s) {
           hipLaunchKernelGGL((k_glu_bwd_row<F, V, ACT, A>),
                              dim3((unsigned)((p.rows + kThreads / 64 - 1) / (kThreads / 64))),
                              dim3(kThreads), 0, s, p, chunks);
-        else if (total)
+        else
           hipLaunchKernelGGL((k_glu_bwd<F, V, ACT, A>), dim3((total + kThreads - 1) / kThreads),
                              dim3(kThreads), 0, s, p, div, total);
       });

@@ -1,0 +1,83 @@
+"""Launches at the largest sizes that the language-model operators accept, on a
+machine without a GPU: a small program stands in for the HIP runtime, records
+every launch of a call and refuses what HIP refuses (2^32 threads or more in a
+grid's dimension).  Pointers are numbers that nobody follows."""
+import os
+import subprocess
+
+import pytest
+
+import rht_bit_block_amd as U
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+P = 1 << 44          # an address; arrays lie 2^44 apart
+
+pytestmark = pytest.mark.skipif(not os.path.exists(U.LIB_PATH), reason="library not built")
+
+
+@pytest.fixture(scope="module")
+def probe(tmp_path_factory):
+    exe = str(tmp_path_factory.mktemp("probe") / "launch_probe")
+    subprocess.run(["g++", "-O1", "-rdynamic", os.path.join(HERE, "launch_probe.cpp"), "-o", exe, "-ldl"],
+                   check=True)
+
+    def call(fn, *args, words=False):
+        """(status, [(kernel, grid x y z, block x y z, words of the first argument)])"""
+        env = dict(os.environ)
+        if words:
+            env["PROBE_WORDS"] = "1"
+        r = subprocess.run([exe, U.LIB_PATH, fn, *(str(int(a)) for a in args)], capture_output=True,
+                           text=True, check=True, env=env)
+        lines = [x.split() for x in r.stdout.splitlines()]
+        assert not [x for x in lines if x[0] == "refused"], [x for x in lines if x[0] == "refused"][:2]
+        got = [(x[1], [int(v) for v in x[2:8]], [int(v) for v in x[8:]]) for x in lines if x[0] == "launch"]
+        return int(lines[-1][1]), got
+
+    return call
+
+
+# Places of GluLaunch's fields among its 8-byte words
+GATE, UP, ROW, H, GC, GS, DH, DG, DU, DROW, ROWS = 0, 1, 3, 4, 6, 7, 10, 12, 13, 15, 16
+
+
+def glu_bwd(probe, rows, cols, dtype, drow, again):
+    return probe("ufp4_glu_bwd", P, 2 * P, 3 * P, 4 * P, rows, cols, 0, 5 * P, 6 * P, dtype, cols, 7 * P,
+                 8 * P, cols, 9 * P if drow else 0, 10 * P if again else 0, cols, 0, words=True)
+
+
+@pytest.mark.parametrize("rows,cols", [(1 << 26, 32), ((1 << 28) + 3, 1), (1 << 26, 128), (1 << 27, 129),
+                                       ((1 << 30) + 7, 0), (1, 1 << 30), (1 << 20, 4096)])
+@pytest.mark.parametrize("dtype", [U.UFP4_BF16, U.UFP4_FP32])
+def test_glu_backward_with_the_row_factors_gradient(probe, rows, cols, dtype):
+    """A wave per row, whatever the row's width; the slices follow one another."""
+    st, got = glu_bwd(probe, rows, cols, dtype, True, cols > 0)
+    assert st == U.UFP4_OK and got
+    at = 0
+    for name, g, w in got:
+        assert "k_glu_bwd_row" in name
+        n = w[ROWS]
+        assert g[0] * g[3] >= 64 * n and g[0] * g[3] - 64 * n < 4 * 64
+        assert w[DROW] == 9 * P + 4 * at and w[ROW] == 5 * P + 4 * at
+        if cols:
+            assert w[GC] == P + cols * at and w[GS] == 2 * P + (cols + 31) // 32 * at
+            assert w[DH] == 6 * P + (2, 4)[dtype] * cols * at and w[DG] == 7 * P + 2 * cols * at
+            assert w[DU] == 8 * P + 2 * cols * at and w[H] == 10 * P + 2 * cols * at
+        at += n
+    assert at == rows
+
+
+@pytest.mark.parametrize("rows,cols", [(1 << 26, 32), ((1 << 28) + 3, 1), (1 << 27, 129), (1, 1 << 30)])
+def test_glu_forward_and_backward_without_it(probe, rows, cols):
+    fwd = probe("ufp4_glu_fwd", P, 2 * P, 1, rows, cols, cols, 0, 3 * P, 4 * P, cols, 5 * P, 6 * P, 7 * P,
+                8 * P, 0, words=True)
+    chunks = 4 * ((cols + 31) // 32)
+    for st, got in (fwd, glu_bwd(probe, rows, cols, 1, False, False)):
+        assert st == U.UFP4_OK
+        at = 0
+        for name, g, w in got:
+            n = w[ROWS]
+            assert 0 <= g[0] * g[3] - chunks * n < 256
+            assert w[ROW] == (3 if "fwd" in name else 5) * P + 4 * at
+            assert w[GATE if "fwd" in name else DH] == (P if "fwd" in name else 6 * P) + 4 * cols * at
+            at += n
+        assert at == rows
