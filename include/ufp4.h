@@ -399,7 +399,7 @@ int ufp4_glu_bwd(const uint8_t* gate_codes, const uint8_t* gate_scales, const ui
  * T >= 0 (0: nothing to do), V >= 1, D >= 8.
  * Errors: UFP4_ERR_INVALID_ARG (sizes, pitches, alignment, null pointers, a
  * workspace that is too small), UFP4_ERR_SHAPE (D % 8), UFP4_ERR_UNSUPPORTED
- * (T > 2^21, V > 2^30, D or a pitch > 2^20). */
+ * (T > 2^21, V > 2^30, D or a pitch > 2^20, T D > 2^38). */
 int ufp4_linear_xent_fwd(const void* h, int64_t ldh, const void* w, int64_t ldw,
                          const int64_t* targets, int64_t T, int64_t V, int64_t D, float* loss,
                          float* lse, void* workspace, size_t workspace_bytes, void* stream);

@@ -26,12 +26,14 @@ uintptr_t elem_bytes(int32_t d) { return d == UFP4_BF16 ? 2 : 4; }
 
 constexpr int64_t kMaxGluCols = (int64_t)1 << 30;   // a row's 8-element chunks in one launch
 
-// Sizes of a linear cross entropy: 32-bit offsets inside a 256-row tile and
-// grids of a launch bound them.
+// Sizes of a linear cross entropy: 32-bit offsets inside a 256-row tile bound T
+// (a pitch of the turned operands) and D, 2^22 tiles of classes V, and as many
+// tiles of dh T D (512 GiB of h).
 int xent_sizes(int64_t T, int64_t V, int64_t D) {
   if (T < 0 || V < 1 || D < 1) return UFP4_ERR_INVALID_ARG;
   if (D % 8) return UFP4_ERR_SHAPE;
-  if (T > ((int64_t)1 << 21) || V > ((int64_t)1 << 30) || D > ((int64_t)1 << 20))
+  if (T > ((int64_t)1 << 21) || V > ((int64_t)1 << 30) || D > ((int64_t)1 << 20) ||
+      T * D > ((int64_t)1 << 38))
     return UFP4_ERR_UNSUPPORTED;
   return UFP4_OK;
 }

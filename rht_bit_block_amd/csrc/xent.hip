@@ -71,8 +71,9 @@ struct Prod {
   int64_t lda, ldb;         // row pitches in elements
   int32_t tiles_m, tiles_n, tiles, splits;
   int64_t k_per_split;      // a multiple of 64
-  // kStats: partials [WM tiles_m][N] (maximum, sum), logits of the targets
+  // kStats: partials [WM tiles_m][part_ld] (maximum, sum), logits of the targets
   float2* part;
+  int64_t part_ld;
   float* zt;
   // kStats, kGrad
   const int64_t* targets;   // class of n; m + m0 is the class of m
@@ -390,7 +391,7 @@ __global__ __launch_bounds__(S::THREADS) void k_prod(Prod p) {
           s += __builtin_amdgcn_exp2f((acc[i][j][r] - base) * kLog2e);
       s += __shfl_xor(s, 32);
       if (live && h == 0)
-        p.part[(int64_t)(tm * S::WM + wm) * p.N + n] = make_float2(m, s);
+        p.part[(int64_t)(tm * S::WM + wm) * p.part_ld + n] = make_float2(m, s);
     }
   } else if constexpr (EPI == kGrad) {
 #pragma unroll
@@ -562,30 +563,40 @@ __global__ __launch_bounds__(kThreads) void k_xent_scale(const int64_t* targets,
 }
 
 // out[n][m] = s times the sum of the slabs, rounded to bf16; 4 elements per
-// thread.
+// thread and round of the grid.
 __global__ __launch_bounds__(kThreads) void k_slab_sum(const float* slab, int64_t N, int64_t M,
                                                        int splits, const float* scale,
                                                        uint16_t* out, int64_t ldo) {
-  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
-  if (i >= N * M) return;
-  f32x4 v = *reinterpret_cast<const f32x4*>(slab + i);
-  for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(slab + s * N * M + i);
-  const int64_t n = i / M, m = i - n * M;
-  v *= scale[0];
-  const u32x2 w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-  *reinterpret_cast<u32x2*>(out + n * ldo + m) = w;
+  int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 4;
+  for (; i < N * M; i += (int64_t)gridDim.x * kThreads * 4) {
+    f32x4 v = *reinterpret_cast<const f32x4*>(slab + i);
+    for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(slab + s * N * M + i);
+    const int64_t n = i / M, m = i - n * M;
+    v *= scale[0];
+    const u32x2 w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    *reinterpret_cast<u32x2*>(out + n * ldo + m) = w;
+  }
 }
 
 __global__ __launch_bounds__(kThreads) void k_zero_rows(uint16_t* out, int64_t N, int64_t M,
                                                         int64_t ldo) {
-  const int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8;
-  if (i >= N * M) return;
-  const int64_t n = i / M, m = i - n * M;
-  *reinterpret_cast<u32x4*>(out + n * ldo + m) = u32x4{0, 0, 0, 0};
+  int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * 8;
+  for (; i < N * M; i += (int64_t)gridDim.x * kThreads * 8) {
+    const int64_t n = i / M, m = i - n * M;
+    *reinterpret_cast<u32x4*>(out + n * ldo + m) = u32x4{0, 0, 0, 0};
+  }
 }
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t up(int64_t a, int64_t b) { return cdiv(a, b) * b; }
+
+// HIP takes fewer than 2^32 threads in a launch: tiles of a product (of 512
+// threads), and workgroups of an elementwise kernel, which then goes round.
+constexpr int64_t kMaxTiles = (int64_t)1 << 22;
+dim3 grid_for(int64_t threads) {
+  const int64_t g = cdiv(threads, kThreads);
+  return dim3((unsigned)(g < kMaxTiles ? g : kMaxTiles));
+}
 
 template <class S, int EPI>
 hipError_t launch_prod(Prod p, hipStream_t s) {
@@ -604,12 +615,29 @@ hipError_t launch_prod(Prod p, hipStream_t s) {
   return hipGetLastError();
 }
 
-// The product of the logits: by tokens, see the shapes.
+// The product of the logits: by tokens, see the shapes.  Statistics of more tiles
+// than a launch takes (T V > 2^38) some tokens at a time; a piece of the backward
+// pass has at most 2^13 tiles.
 template <int EPI>
 hipError_t launch_logits(const Prod& p, hipStream_t s) {
   if (p.N <= 32) return launch_prod<Thin32, EPI>(p, s);
   if (p.N <= 64) return launch_prod<Thin64, EPI>(p, s);
-  return launch_prod<Big, EPI>(p, s);
+  if constexpr (EPI == kStats) {
+    const int64_t step = kMaxTiles / cdiv(p.M, Big::TM) * Big::TN;   // M <= 2^30: one tile or more
+    for (int64_t n = 0; n < p.N; n += step) {
+      Prod q = p;
+      q.N = p.N - n < step ? p.N - n : step;
+      q.b = p.b + n * p.ldb;
+      q.targets = p.targets + n;
+      q.part = p.part + n;
+      q.zt = p.zt + n;
+      const hipError_t e = launch_prod<Big, EPI>(q, s);
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+  } else {
+    return launch_prod<Big, EPI>(p, s);
+  }
 }
 // Rows of the forward statistics for V classes and T tokens.
 int64_t stat_rows(int64_t T, int64_t V) {
@@ -666,6 +694,7 @@ hipError_t launch_xent_fwd(const XentLaunch& x, hipStream_t s) {
   p.b = x.h; p.ldb = x.ldh; p.N = x.T;
   p.K = x.D;
   p.part = reinterpret_cast<float2*>(x.ws);
+  p.part_ld = x.T;
   p.zt = reinterpret_cast<float*>(x.ws + up(8 * pl.parts * x.T, 256));
   p.targets = x.targets;
   p.classes = x.V;
@@ -684,8 +713,8 @@ hipError_t launch_xent_fwd(const XentLaunch& x, hipStream_t s) {
 
 hipError_t launch_xent_bwd(const XentLaunch& x, hipStream_t s) {
   if (x.T == 0) {   // no token: dW is zero
-    hipLaunchKernelGGL(k_zero_rows, dim3((unsigned)cdiv(x.V * x.D, 8 * kThreads)), dim3(kThreads), 0,
-                       s, x.dw, x.V, x.D, x.lddw);
+    hipLaunchKernelGGL(k_zero_rows, grid_for(cdiv(x.V * x.D, 8)), dim3(kThreads), 0, s, x.dw,
+                       x.V, x.D, x.lddw);
     return hipGetLastError();
   }
   const XentPlan pl = xent_plan(x.T, x.V, x.D);
@@ -741,8 +770,8 @@ hipError_t launch_xent_bwd(const XentLaunch& x, hipStream_t s) {
     if ((e = launch_prod<Big, kOut>(w, s)) != hipSuccess) return e;
     if (c == 0) splits = (int32_t)cdiv(vp, pl.splits == 1 ? vp : up(cdiv(vp, pl.splits), 64));
   }
-  hipLaunchKernelGGL(k_slab_sum, dim3((unsigned)cdiv(x.T * x.D, 4 * kThreads)), dim3(kThreads), 0, s,
-                     slab, x.T, x.D, splits, scale, x.dh, x.lddh);
+  hipLaunchKernelGGL(k_slab_sum, grid_for(cdiv(x.T * x.D, 4)), dim3(kThreads), 0, s, slab,
+                     x.T, x.D, splits, scale, x.dh, x.lddh);
   return hipGetLastError();
 }
 

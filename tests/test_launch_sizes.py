@@ -81,3 +81,58 @@ def test_glu_forward_and_backward_without_it(probe, rows, cols):
             assert w[GATE if "fwd" in name else DH] == (P if "fwd" in name else 6 * P) + 4 * cols * at
             at += n
         assert at == rows
+
+
+# Places of the product's description among its 8-byte words
+B_, M_, N_, LDB = 1, 2, 3, 6
+W, HID, TG, WS = P, 2 * P, 3 * P, 4 * P
+
+
+def xent_fwd(probe, T, V, D, words=False):
+    return probe("ufp4_linear_xent_fwd", HID, D, W, D, TG, T, V, D, 5 * P, 6 * P, WS, 1 << 62, 0, words=words)
+
+
+@pytest.mark.parametrize("T,V,D", [(1 << 20, 1 << 20, 64), (1 << 21, 1 << 18, 64), (1 << 21, 1 << 30, 8),
+                                   ((1 << 20) + 33, (1 << 22) + 5, 64), (64, 1 << 30, 64), (1, 1 << 30, 8)])
+def test_xent_forward(probe, T, V, D):
+    """Every token in one launch of the product, whatever T V."""
+    st, got = xent_fwd(probe, T, V, D)
+    assert st == U.UFP4_OK
+    assert ["k_prod" in n for n, _, _ in got] == [True] * (len(got) - 1) + [False]
+    wide, tokens = (256, 256) if T > 64 else (128, 64)
+    tiles = sum(g[0] for _, g, _ in got[:-1])
+    assert tiles == -(-V // wide) * -(-T // tokens)
+
+
+def test_xent_forward_slices(probe):
+    """Slices of tokens follow one another, all with the tile shape that the
+    workspace is laid out for, a last one of 33 tokens too."""
+    T, V, D = (1 << 20) + 33, 1 << 20, 64
+    st, got = probe("ufp4_linear_xent_fwd", HID, D, W, D, TG, T, V, D, 5 * P, 6 * P, WS, 1 << 62, 0,
+                    words=True)
+    at = 0
+    assert st == U.UFP4_OK and len(got) > 2
+    for name, g, w in got[:-1]:
+        assert name == got[0][0] and w[M_] == V and w[B_] == HID + 2 * D * at and w[LDB] == D
+        at += w[N_]
+    assert at == T and got[-2][2][N_] == 33
+
+
+@pytest.mark.parametrize("T,V,D", [(0, 1 << 30, 64), (0, 1 << 21, 1 << 14), (1 << 21, 300, 1 << 13),
+                                   (1 << 21, 300, 1 << 17), (1 << 18, 300, 1 << 20), (1, 70000, 1 << 20),
+                                   (1 << 21, 3000, 64)])
+def test_xent_backward(probe, T, V, D):
+    st, got = probe("ufp4_linear_xent_bwd", HID, D, W, D, TG, T, V, D, 5 * P, 6 * P, 0, 7 * P, D, 8 * P, D,
+                    WS, 1 << 62, 0)
+    assert st == U.UFP4_OK
+    assert ("k_zero_rows" if T == 0 else "k_slab_sum") in got[-1][0]
+
+
+def test_xent_refuses_what_no_launch_takes():
+    lib = U.lib_handle()
+    for T, D in ((1 << 21, (1 << 17) + 8), ((1 << 18) + 1, 1 << 20)):
+        assert lib.ufp4_linear_xent_fwd(HID, D, W, D, TG, T, 300, D, 5 * P, 6 * P, WS, 1 << 62,
+                                        None) == U.UFP4_ERR_UNSUPPORTED
+        assert lib.ufp4_linear_xent_bwd(HID, D, W, D, TG, T, 300, D, 5 * P, 6 * P, None, 7 * P, D, 8 * P, D,
+                                        WS, 1 << 62, None) == U.UFP4_ERR_UNSUPPORTED
+        assert U.ufp4_linear_xent_workspace_bytes(T, 300, D) == 0
