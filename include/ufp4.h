@@ -444,7 +444,8 @@ size_t ufp4_linear_xent_workspace_bytes(int64_t T, int64_t V, int64_t D, int32_t
  *   aligned, ldy even, overwritten.
  * Activations carry 16 bits of mantissa or more up to the one rounding of y;
  * level products, scales and sums are fp32, added in a fixed order (equal
- * inputs give equal bits).  T = 0 is a no-op.
+ * inputs give equal bits).  Infinities and NaN of x show as in the formulas, in
+ * their own token only.  T = 0 is a no-op.
  * workspace: ufp4_moe_tokens_workspace_bytes(T, E, top_k, H, F) bytes,
  * 256-byte aligned, any contents; calls that share one must be ordered on one
  * stream.

@@ -62,6 +62,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kBf16Max = 0x1.FEp127f;
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
 constexpr int kRouteThreads = 256;
 
@@ -555,7 +556,10 @@ __device__ __forceinline__ void rotate8(float (&v)[8], int64_t i, int n, float c
     }
     a *= cn;
     b *= cn;
-    hi[j] = pack_bf16(a, b);
+    // the upper piece is held to bf16's largest, so that an infinity stays one in the
+    // lower piece and a float above that largest does not become one
+    hi[j] = pack_bf16(__builtin_amdgcn_fmed3f(a, -kBf16Max, kBf16Max),
+                      __builtin_amdgcn_fmed3f(b, -kBf16Max, kBf16Max));
     lo[j] = pack_bf16(a - __uint_as_float(hi[j] << 16), b - __uint_as_float(hi[j] & 0xFFFF0000u));
   }
 }

@@ -412,3 +412,43 @@ def test_moe_signed_zeros_tie(E, T):
             y = U.ufp4_moe_tokens(x.cuda(), logits.cuda(), *q, k, renorm=renorm)
             torch.cuda.synchronize()
             check(y, *formulas(x, logits, *v, cfg, dcfg, k, renorm, U.UFP4_ACT_SILU))
+
+
+def plain_weight(P, K, cfg, level, scale):
+    """A weight whose codes all stand for the same level (INT4)."""
+    q = U.QTensor(torch.full((P, K // 2), level * 17, dtype=torch.uint8),
+                  torch.full((P, K // cfg.block_cols), scale), P, K, cfg)
+    return U.QTensor(q.codes.cuda(), q.scales.cuda(), P, K, cfg)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 12])
+@pytest.mark.parametrize("block", [16, 32])
+def test_moe_infinite_and_largest_activations(block, T):
+    """An infinity in x gives infinities (positive weights, no rotation), not
+    NaN, a NaN gives NaN, and both only in their own tokens.  An intermediate
+    between the largest bf16 and the largest fp32 value, 2^128 (1 - 2^-10), times
+    2^-100 is 2^28 to within bf16's half step 2^-8."""
+    print("case: moe infinities", block, T, flush=True)
+    H, F, E = 64, 64, 2
+    c = mk(U.UFP4_INT4, block, 1, 0)
+    w = [plain_weight(E * P, K, c, 1, s) for P, K, s in ((F, H, 2.0 ** -6), (F, H, 2.0 ** -6), (H, F, 2.0 ** -6))]
+    x, logits = inputs(T, E, H, 4)
+    x = x.abs()
+    ref = U.ufp4_moe_tokens(x.cuda(), logits.cuda(), *w, 2)
+    x[0, 5] = float("inf")
+    x[1, 40] = float("nan")
+    y = U.ufp4_moe_tokens(x.cuda(), logits.cuda(), *w, 2)
+    torch.cuda.synchronize()
+    assert (y[0] == float("inf")).all()
+    assert torch.isnan(y[1]).all()
+    assert torch.isfinite(ref).all() and torch.equal(y[2:], ref[2:])
+
+    big = 2.0 ** 64
+    w = [plain_weight(P, K, c, 1, s) for P, K, s in ((F, H, big), (F, H, big * (1 - 2.0 ** -10)), (H, F, 2.0 ** -100))]
+    w[1].codes[1:] = 0                    # one column of the intermediate
+    x = torch.zeros(T, H, dtype=torch.bfloat16)
+    x[:, 3] = 1.0
+    y = U.ufp4_moe_tokens(x.cuda(), torch.zeros(T, 1).cuda(), *w, 1)
+    torch.cuda.synchronize()
+    assert ((y.double() - 2.0 ** 28 * (1 - 2.0 ** -10)).abs() <= BF16 * 2.0 ** 28).all()
