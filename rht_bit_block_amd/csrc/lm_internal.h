@@ -97,10 +97,11 @@ struct MoeLaunch {
   float* share;            // [T][k]
   int* expert;             // [slots] a slot's expert
   int* count;              // [slots] its tokens
-  int* place;              // [T][k] row slot T + i of a choice, -1: none
+  int* row0;               // [slots] first row of its tokens in h and partial
+  int* place;              // [T][k] row of a choice, -1: none
   uint8_t* xr;             // rotated x: [T][H], 4 bytes an element
-  float* h;                // weighted intermediate: [slots][T][F]
-  float* partial;          // down products: [slots][T][H]
+  float* h;                // weighted intermediate: [T k][F], by experts
+  float* partial;          // down products: [T k][H]
 };
 
 // Fills the plan and returns the workspace's size in bytes (ws may be null).

@@ -617,11 +617,11 @@ __device__ __forceinline__ int range_of(int m, int nb) {
 
 // --- gate and up products, activation ---------------------------------------------
 // A workgroup computes `pairs` times 16 columns of the intermediate from f0 on,
-// each a pair of a gate and an up tile.  Tokens first .. first + m - 1 of the expert's; FUSED: x is
-// in LDS already, row t for token t.
+// each a pair of a gate and an up tile, for m of the expert's tokens, whose rows of the
+// intermediate start at hrow; FUSED: x is in LDS already, row t for token t.
 template <int GRID, int SK, int TT, bool FUSED>
-__device__ __forceinline__ void moe_up_body(const MoeLaunch& p, int slot, int e, int f0, int pairs,
-                                            int first, int m, const int* tok, const float* share,
+__device__ __forceinline__ void moe_up_body(const MoeLaunch& p, int64_t hrow, int e, int f0,
+                                            int pairs, int m, const int* tok, const float* share,
                                             uint8_t* lds) {
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r16 = lane & 15;
@@ -672,7 +672,7 @@ __device__ __forceinline__ void moe_up_body(const MoeLaunch& p, int slot, int e,
     const float* at = part + ((col >> 4) * 2 * ROWS + row) * 16 + (col & 15);
     const float a = at[0] * p.wg.factor, b = at[ROWS * 16] * p.wu.factor;
     const float s = p.act == UFP4_ACT_GELU ? activation<1>(a) : activation<0>(a);
-    p.h[((int64_t)slot * p.T + first + row) * p.F + f0 + col] = s * b * share[row];
+    p.h[(hrow + row) * p.F + f0 + col] = s * b * share[row];
   }
   if constexpr (TT > 1) __syncthreads();   // the next tokens' activations go where `part` is
 }
@@ -686,9 +686,10 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_up(MoeLaunch p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ int tok[kMoeMaxTokens];
   __shared__ float share[kMoeMaxTokens];
+  __shared__ int choice[kMoeMaxTokens];
   __shared__ int ids_here[FUSED ? kMoeFusedTokens * kMoeMaxChoices : 1];
   __shared__ float share_here[FUSED ? kMoeFusedTokens * kMoeMaxChoices : 1];
-  __shared__ int found[2];   // expert, tokens
+  __shared__ int found[3];   // expert, tokens, their first row
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int fc = blockIdx.x, slot = blockIdx.y;
   const int* ids = p.ids;
@@ -732,7 +733,8 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_up(MoeLaunch p) {
         mine = !before;
       }
     }
-    int m = 0;
+    // the rows of the intermediate go by experts: those of lower ones come first
+    int m = 0, row0 = 0;
     for (int i0 = 0; i0 < pairs; i0 += 64) {
       const int i = i0 + lane;
       const int id = ids[i < pairs ? i : 0];
@@ -742,28 +744,33 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_up(MoeLaunch p) {
         const int at = m + __builtin_popcountll(mask & (((uint64_t)1 << lane) - 1));
         tok[at] = i / p.k;
         share[at] = shares[i];
-        if (fc == 0) p.place[i] = slot * (int)p.T + at;   // for the join
+        choice[at] = i;
       }
       if (fc == 0 && slot == 0 && i < pairs && id < 0) p.place[i] = -1;
       m += __builtin_popcountll(mask);
+      row0 += __builtin_popcountll(__ballot(i < pairs && id >= 0 && id < e));
     }
     if (lane == 0) {
       found[0] = e;
       found[1] = m;
+      found[2] = row0;
       if (fc == 0) {   // for the down product
         p.expert[slot] = e;
         p.count[slot] = m;
+        p.row0[slot] = row0;
       }
     }
   }
   __syncthreads();
   const int e = __builtin_amdgcn_readfirstlane(found[0]);
   const int m = __builtin_amdgcn_readfirstlane(found[1]);
+  const int row0 = __builtin_amdgcn_readfirstlane(found[2]);
   if (m == 0) return;
+  if (fc == 0 && tid < m) p.place[choice[tid]] = row0 + tid;   // for the join
   const int pair0 = fc * p.run_up, left = (int)(p.F / 16) - pair0;
   const int pairs = left < p.run_up ? left : p.run_up;
   auto body = [&](auto tt, int first, int n) {
-    moe_up_body<GRID, SK, decltype(tt)::value, FUSED>(p, slot, e, 16 * pair0, pairs, first, n,
+    moe_up_body<GRID, SK, decltype(tt)::value, FUSED>(p, row0 + first, e, 16 * pair0, pairs, n,
                                                       tok + first, share + first, lds);
   };
   if (MODE != kWide || m <= 16) {
@@ -834,12 +841,12 @@ template <int GRID, int SK, bool WIDE>
 __global__ __launch_bounds__(kThreads, 4) void k_moe_down(MoeLaunch p) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int slot = blockIdx.y;
-  const int m = p.count[slot], e = p.expert[slot];
+  const int m = p.count[slot], e = p.expert[slot], row0 = p.row0[slot];
   if (m == 0) return;
   const int pair0 = (int)blockIdx.x * p.run_down, left = (int)(p.H / 32) - pair0;
   const int pairs = left < p.run_down ? left : p.run_down;
   auto body = [&](auto tt, int first, int n) {
-    moe_down_body<GRID, SK, decltype(tt)::value>(p, (int64_t)slot * p.T + first, e, n,
+    moe_down_body<GRID, SK, decltype(tt)::value>(p, row0 + first, e, n,
                                                  32 * (int64_t)pair0, pairs, lds);
   };
   if (!WIDE || m <= 16) {
@@ -985,10 +992,11 @@ int64_t moe_plan(MoeLaunch& p, uint8_t* ws) {
   p.share = reinterpret_cast<float*>(take(p.fused ? 0 : 4 * pairs));
   p.expert = reinterpret_cast<int*>(take(4 * p.slots));
   p.count = reinterpret_cast<int*>(take(4 * p.slots));
+  p.row0 = reinterpret_cast<int*>(take(4 * p.slots));
   p.place = reinterpret_cast<int*>(take(4 * pairs));
   p.xr = take(p.fused ? 0 : 4 * p.T * p.H);
-  p.h = reinterpret_cast<float*>(take(4 * p.slots * p.T * p.F));
-  p.partial = reinterpret_cast<float*>(take(4 * p.slots * p.T * p.H));
+  p.h = reinterpret_cast<float*>(take(4 * pairs * p.F));
+  p.partial = reinterpret_cast<float*>(take(4 * pairs * p.H));
   return at;
 }
 

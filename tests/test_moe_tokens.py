@@ -452,3 +452,13 @@ def test_moe_infinite_and_largest_activations(block, T):
     y = U.ufp4_moe_tokens(x.cuda(), torch.zeros(T, 1).cuda(), *w, 1)
     torch.cuda.synchronize()
     assert ((y.double() - 2.0 ** 28 * (1 - 2.0 ** -10)).abs() <= BF16 * 2.0 ** 28).all()
+
+
+@pytest.mark.parametrize("T,E,k,H,F", [(1, 64, 6, 2048, 1408), (61, 64, 6, 2048, 1408), (16, 16, 8, 5120, 1536),
+                                       (64, 256, 16, 1 << 20, 1 << 20), (64, 256, 1, 64, 32)])
+def test_moe_workspace_holds_the_choices(T, E, k, H, F):
+    """A row of the intermediate and of the down products for each of the T k
+    choices (fp32), the rotated tokens (4 bytes an element) and small arrays."""
+    need = U.ufp4_moe_tokens_workspace_bytes(T, E, k, H, F)
+    rows = 4 * T * k * (H + F)
+    assert rows <= need <= rows + 4 * T * H + 16 * T * k + 16 * E + 8 * 256
