@@ -36,7 +36,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPer = 8;      // elements per thread
-constexpr int64_t kCacheBytes = (int64_t)128 << 20;   // half the last-level cache: one bf16 output
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -59,8 +58,10 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // Eight elements at p (n of them inside the row; the others read as 0).  VEC:
 // p is 16-byte aligned and n is 8 or <= 0; else whole eights are still one or
 // two wide accesses, at the elements' own alignment, and only a row's end goes
-// element by element.  The input is read once, so it does not displace what
-// other kernels left in the caches.
+// element by element.  Lines that one access reads whole, here and in read8, are read
+// past the caches' order of use: the backward pass of 262144 x 1536 rows with fp32 dh
+// takes 742 us instead of 760, with bf16 inputs 1 to 2 % more (forward 541 instead of
+// 536).  Stores past the caches gained nothing at any size (forward 884 us either way).
 template <bool F32, bool VEC>
 __device__ __forceinline__ void load8(const void* base, int64_t at, int n, float (&v)[kPer]) {
   if constexpr (VEC) {
@@ -98,17 +99,13 @@ __device__ __forceinline__ void load8(const void* base, int64_t at, int n, float
   }
 }
 
-// stream: the output is larger than the caches, so it passes them by (the
-// 262144 x 1536 rows: forward 901 -> 832 us with the loads above,
-// backward 930 -> 870 us); a smaller one stays for its reader.
 template <bool VEC>
-__device__ __forceinline__ void store8_bf16(uint16_t* base, int64_t at, int n, bool stream,
+__device__ __forceinline__ void store8_bf16(uint16_t* base, int64_t at, int n,
                                             const float (&v)[kPer]) {
   const u32x4 w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
                    pack_bf16(v[6], v[7])};
   if constexpr (VEC) {
-    if (stream) __builtin_nontemporal_store(w, reinterpret_cast<u32x4*>(base + at));
-    else *reinterpret_cast<u32x4*>(base + at) = w;
+    *reinterpret_cast<u32x4*>(base + at) = w;
   } else if (n >= kPer) {
     *reinterpret_cast<u32x4u*>(base + at) = w;
   } else {
@@ -163,7 +160,7 @@ __device__ __forceinline__ int scale_exponent(float m) {
 // Codes and scale of a thread's 8 elements (n inside the row).
 template <bool VEC>
 __device__ __forceinline__ void save8(uint8_t* codes, int64_t at, uint8_t* scales, int64_t sat,
-                                      int n, bool first, bool stream, const float (&x)[kPer]) {
+                                      int n, bool first, const float (&x)[kPer]) {
   const float m = block_absmax(x);
   const int e = scale_exponent(m);
   float v[kPer];
@@ -185,10 +182,7 @@ __device__ __forceinline__ void save8(uint8_t* codes, int64_t at, uint8_t* scale
     w[i] = mag | (b & ((mag + 0x7F7F7F7Fu) & 0x80808080u));
   }
   if constexpr (VEC) {
-    if (n > 0) {
-      if (stream) __builtin_nontemporal_store(w, reinterpret_cast<u32x2*>(codes + at));
-      else *reinterpret_cast<u32x2*>(codes + at) = w;
-    }
+    if (n > 0) *reinterpret_cast<u32x2*>(codes + at) = w;
   } else if (n >= kPer) {
     *reinterpret_cast<u32x2u*>(codes + at) = w;
   } else {
@@ -241,8 +235,8 @@ __global__ __launch_bounds__(kThreads) void k_glu_fwd(GluLaunch g, FastDiv chunk
   }
   if constexpr (SAVE) {
     const int64_t at = row * g.cols + col, sat = row * (chunks.d / 4) + c / 4;
-    save8<VEC>(g.gate_codes, at, g.gate_scales, sat, n, (c & 3) == 0, g.stream, a);
-    save8<VEC>(g.up_codes, at, g.up_scales, sat, n, (c & 3) == 0, g.stream, u);
+    save8<VEC>(g.gate_codes, at, g.gate_scales, sat, n, (c & 3) == 0, a);
+    save8<VEC>(g.up_codes, at, g.up_scales, sat, n, (c & 3) == 0, u);
   }
   if (n <= 0) return;
   const float r = g.row_scale ? g.row_scale[row] : 1.0f;
@@ -253,7 +247,7 @@ __global__ __launch_bounds__(kThreads) void k_glu_fwd(GluLaunch g, FastDiv chunk
     activation<ACT, false>(a[k], s, unused);
     h[k] = s * u[k] * r;
   }
-  store8_bf16<VEC>(g.h, row * g.ldh + col, n, g.stream, h);
+  store8_bf16<VEC>(g.h, row * g.ldh + col, n, h);
 }
 
 // One chunk of the backward pass; returns its part of dr.
@@ -279,9 +273,9 @@ __device__ __forceinline__ float bwd_chunk(const GluLaunch& g, int64_t row, uint
     if constexpr (AGAIN) oh[k] = s * u[k] * r;
     sum = __builtin_fmaf(d[k] * s, u[k], sum);   // past the row everything is 0
   }
-  store8_bf16<VEC>(g.dgate, row * g.ldd + col, n, g.stream, og);
-  store8_bf16<VEC>(g.dup, row * g.ldd + col, n, g.stream, ou);
-  if constexpr (AGAIN) store8_bf16<VEC>(g.h, row * g.ldh + col, n, g.stream, oh);
+  store8_bf16<VEC>(g.dgate, row * g.ldd + col, n, og);
+  store8_bf16<VEC>(g.dup, row * g.ldd + col, n, ou);
+  if constexpr (AGAIN) store8_bf16<VEC>(g.h, row * g.ldh + col, n, oh);
   return sum;
 }
 
@@ -327,7 +321,6 @@ hipError_t in_slices(const GluLaunch& g, uint32_t chunks, uint32_t threads, F on
   const int64_t es = g.dtype == UFP4_BF16 ? 2 : 4, blocks = chunks / 4;
   for (int64_t r = 0; r < g.rows; r += step) {
     GluLaunch p = g;
-    p.stream = g.rows * g.cols * 2 > kCacheBytes;
     p.rows = g.rows - r < step ? g.rows - r : step;
     auto bytes = [&](const void* b, int64_t off) {
       return b ? static_cast<const void*>(static_cast<const uint8_t*>(b) + off) : nullptr;

@@ -27,7 +27,6 @@ struct GluLaunch {
   float* drow;             // backward output, null to skip
   int64_t rows, cols;
   int32_t dtype, act;
-  int32_t stream;          // set by the launcher: outputs larger than the caches
 };
 
 hipError_t launch_glu_fwd(const GluLaunch& g, hipStream_t s);
