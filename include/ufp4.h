@@ -438,7 +438,7 @@ size_t ufp4_linear_xent_workspace_bytes(int64_t T, int64_t V, int64_t D, int32_t
  * that weight's quantization ([UFP4] Method: the rotation cancels in the
  * product), so that the weights are the ones ufp4_rht_quant(along = 0) or
  * ufp4_rht_quant_dual's row side wrote for FPROP.  A token with nothing to
- * choose has y = 0.
+ * choose has y = 0, one with a logit of +inf (whose softmax is none) y = NaN.
  *   x : bf16 [T][ldx], 16-byte aligned, ldx % 8 == 0;  logits : fp32 [T][ldl];
  *   Wg, Wu : stacked [E*F][H];  Wd : stacked [E*H][F];  y : bf16 [T][ldy], 4-byte
  *   aligned, ldy even, overwritten.

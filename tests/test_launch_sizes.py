@@ -136,3 +136,17 @@ def test_xent_refuses_what_no_launch_takes():
         assert lib.ufp4_linear_xent_bwd(HID, D, W, D, TG, T, 300, D, 5 * P, 6 * P, None, 7 * P, D, 8 * P, D,
                                         WS, 1 << 62, None) == U.UFP4_ERR_UNSUPPORTED
         assert U.ufp4_linear_xent_workspace_bytes(T, 300, D) == 0
+
+
+def test_xent_forward_slices_write_their_own_tokens(probe):
+    """A slice's statistics, target logits and targets start at its first token;
+    the statistics' rows keep the pitch of all tokens."""
+    T, V, D, part, part_ld, zt, targets = 1 << 21, 1 << 19, 8, 10, 11, 12, 13
+    st, got = xent_fwd(probe, T, V, D, words=True)
+    assert st == U.UFP4_OK and len(got) > 3
+    rows = V // 256 * 2
+    at = 0
+    for _, _, w in got[:-1]:
+        assert w[part] == WS + 8 * at and w[part_ld] == T
+        assert w[zt] == WS + 8 * rows * T + 4 * at and w[targets] == TG + 8 * at
+        at += w[N_]

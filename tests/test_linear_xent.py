@@ -330,3 +330,40 @@ def test_xent_binding_refusals():
         U.ufp4_linear_xent_bwd(h, w, t, f, f, dlse=f[:2])
     with pytest.raises(ValueError, match="dw has shape"):
         U.ufp4_linear_xent_bwd(h, w, t, f, f, out=(h, w[:8]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,V,D", [(5, 270001, 16), (40, 262200, 8), (70, 262401, 8)])
+def test_xent_few_tokens_in_pieces(T, V, D):
+    """Vocabularies of several pieces with each of the tile shapes of few tokens."""
+    print("case: xent few tokens in pieces", T, V, D, flush=True)
+    h, w, t, dloss, dlse = inputs(T, V, D, seed=T, device="cuda")
+    loss, lse = U.ufp4_linear_xent_fwd(h, w, t)
+    dh, dw = U.ufp4_linear_xent_bwd(h, w, t, lse, dloss, dlse)
+    torch.cuda.synchronize()
+    f = formulas(h, w, t, dloss, dlse)
+    check_fwd(loss, lse, f)
+    check_bwd(dh, dw, f, h, w)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [9, 50, 300])
+def test_xent_gradients_with_classes_at_minus_infinity(T):
+    """Classes whose logits fall below fp32's range (-2^200) have no probability:
+    their rows of dw are exactly 0 and the other gradients are those of the open
+    classes alone."""
+    print("case: xent closed classes", T, flush=True)
+    V, D, open_ = 700, 64, 300
+    h, w, t, dloss, dlse = inputs(T, V, D, seed=51)
+    t = torch.where(t >= 0, t.clamp(max=open_ - 1), t)
+    h[:, 0], w[:, 0] = 2.0 ** 100, 0.0
+    w[open_:, 0] = -2.0 ** 100
+    g = [x.cuda() for x in (h, w, t, dloss, dlse)]
+    loss, lse = U.ufp4_linear_xent_fwd(*g[:3])
+    dh, dw = U.ufp4_linear_xent_bwd(*g[:3], lse, g[3], dlse=g[4])
+    torch.cuda.synchronize()
+    few = w[:open_].contiguous()
+    f = formulas(h, few, t, dloss, dlse)
+    check_fwd(loss, lse, f)
+    check_bwd(dh, dw[:open_], f, h, few)
+    assert not dw[open_:].any()

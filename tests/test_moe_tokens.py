@@ -462,3 +462,44 @@ def test_moe_workspace_holds_the_choices(T, E, k, H, F):
     need = U.ufp4_moe_tokens_workspace_bytes(T, E, k, H, F)
     rows = 4 * T * k * (H + F)
     assert rows <= need <= rows + 4 * T * H + 16 * T * k + 16 * E + 8 * 256
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [3, 12])
+def test_moe_infinite_logits(T):
+    """A softmax over +inf is NaN, in its own token only."""
+    print("case: moe infinite logits", T, flush=True)
+    E, H, F, k = 8, 64, 32, 2
+    cfg, dcfg = mk(U.UFP4_INT4, 32, 32, 5), mk(U.UFP4_INT4, 32, 32, 6)
+    q, _ = build(E, H, F, cfg, dcfg, 3)
+    x, logits = inputs(T, E, H, 4)
+    ref = U.ufp4_moe_tokens(x.cuda(), logits.cuda(), *q, k)
+    logits[1, 5] = float("inf")
+    y = U.ufp4_moe_tokens(x.cuda(), logits.cuda(), *q, k)
+    torch.cuda.synchronize()
+    assert torch.isnan(y[1]).all()
+    rest = [t for t in range(T) if t != 1]
+    assert torch.isfinite(ref).all() and torch.equal(y[rest], ref[rest])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,k", [(16, 4), (33, 2)])
+def test_moe_three_pairs_of_the_down_product(T, k):
+    """47 pairs of column tiles of 16 experts over a contraction of 3200: a
+    workgroup of the down product takes three of them, the last one two.  Bounds
+    as for the runs of the other sizes."""
+    E, H, F, some = 16, 1504, 3200, 3
+    print("case: moe three pairs", T, k, flush=True)
+    cfg, dcfg = mk(U.UFP4_E2M1, 32, 16, 6, True), mk(U.UFP4_INT4, 32, 32, 5)
+    q, v = build(some, H, F, cfg, dcfg, T)
+    turns = (E + some - 1) // some
+    q = [U.QTensor(w.codes.repeat(turns, 1)[:E * P], w.scales.repeat(turns, 1)[:E * P], E * P, w.K, c)
+         for w, P, c in zip(q, (F, F, H), (cfg, cfg, dcfg))]
+    x, logits = inputs(T, E, H, 7)
+    y = U.ufp4_moe_tokens(x.cuda(), logits.cuda(), *q, k)
+    torch.cuda.synchronize()
+    v = [_Cycle(w, P, some) for w, P in zip(v, (F, F, H))]
+    v[2].shape = (E * H, F)
+    want, tol = formulas(x, logits, *v, cfg, dcfg, k, True, U.UFP4_ACT_SILU)
+    check(y, want, tol)
+    assert (y.double().cpu() - want).norm() <= (BF16 + 2.0 ** -10) * want.norm()
