@@ -58,9 +58,9 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 // Eight elements at p (n of them inside the row; the others read as 0).  VEC:
 // p is 16-byte aligned and n is 8 or <= 0; else whole eights are still one or
 // two wide accesses, at the elements' own alignment, and only a row's end goes
-// element by element.  Lines that one access reads whole, here and in read8, are read
-// past the caches' order of use: the backward pass of 262144 x 1536 rows with fp32 dh
-// takes 742 us instead of 760, with bf16 inputs 1 to 2 % more (forward 541 instead of
+// element by element.  What a whole wave reads line by line, here and in read8, is
+// loaded non-temporally: the backward pass of 262144 x 1536 rows with fp32 dh
+// takes 742 us instead of 760, with bf16 inputs 1 to 5 % more (forward 541 instead of
 // 536).  Stores past the caches gained nothing at any size (forward 884 us either way).
 template <bool F32, bool VEC>
 __device__ __forceinline__ void load8(const void* base, int64_t at, int n, float (&v)[kPer]) {

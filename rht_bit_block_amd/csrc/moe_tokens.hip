@@ -38,11 +38,13 @@
 // product of 16 tokens, four pairs of tiles to a workgroup).  The activations of the workgroup's tokens lie in LDS,
 // 28 KB of them at a time.
 //
-// What bounds them (16 tokens, 16 experts of 5120 x 1536 with 1 x 16 scales: up 59 us,
-// 3.2 TB/s; down 42): the copies alone took 49 and 31, the arithmetic alone, with
+// What bounds them (16 tokens, 16 experts of 5120 x 1536 with 1 x 16 scales: up 62 us,
+// 3.0 TB/s; down 43): the copies alone took 49 and 31, the arithmetic alone, with
 // four pairs to a workgroup, 54 and 38; neither is hidden whole behind the other.
-// Half the decoding's instructions (INT4 as unsigned levels, the offset in the
-// accumulator) gave 1 %, a third step in the ring nothing.
+// With four pairs and no copies of scales, whose requests are as many as the codes',
+// they took 56 and 38 instead of 65 and 42.  Half the decoding's instructions (INT4 as
+// unsigned levels, the offset in the accumulator) gave 1 %, a third step in the ring
+// nothing.
 #include <cmath>
 #include <type_traits>
 
@@ -945,10 +947,16 @@ int64_t up256(int64_t v) { return (v + 255) / 256 * 256; }
 // takes for a pair: the fullest unit's workgroups, each with its pairs (half of one
 // more where there are three: two waves have nothing to do) and a fixed part for
 // routing, joining and the tokens' activations; and once the time that a wave
-// takes for its share of K with the unit to itself.  Three pairs have the two
-// shares of four, and pay for K long enough that the first copies' latency does not
-// count (down product of K = 1408, two tokens: 11.4 with 2, 15.4 with 3).  Of equals
-// the most pairs.
+// takes for its share of K with the unit to itself.  Workgroups of up to 4 % of the
+// units more than a round share a unit with another and cost no round of their own
+// (one token, 264 workgroups of two pairs: up product 14.6 us, 15.1 with 132 of four).
+// Three pairs have the two shares of four, and pay for K long enough that the first
+// copies' latency does not count: of K = 1408 the down product of one token takes 10.6
+// with 3 and 8.7 with 2, of two tokens 15.4 and 11.4; of K = 5120 the up product below
+// gains.  The border lies between: from K = 1408 to 2944 three pairs would still gain
+// 2 to 7 % over four in the up product of 16 experts and 16 tokens, and lose 4 to 25 %
+// against two in the down product (K = 1536) of 64 experts and 4 tokens.  Of equals the
+// most pairs.
 // Measured, in us with 2 / 3 / 4 / 8 pairs: up product, 16 experts of 5120 x 1536
 // and 16 tokens: 65.7 / 61.4 / 67.2 / 69.8; 64 of 2048 x 1408, 16 tokens: 56.0 / 60.4 /
 // 55.1 / 68.1; 61 tokens: 74.8 / 68.5 / 62.0 / 58.4, and its down product 49.9 /

@@ -18,8 +18,9 @@
 // rounding of dloss itself would be the same in every one of them (measured on
 // 8192 tokens: 3.4e-3 of the norm without, 1.8e-3 with s).  Every product runs as C[m][n] = sum_k
 // A[m][k] B[n][k] with both operands K-contiguous, so h, the piece of W and G
-// are also laid out transposed (plain tiled copies, a hundredth of the products'
-// operations' time; G leaves its tiles in both orders).
+// are also laid out transposed (plain tiled copies: 16 us for h and 65 for each of four
+// pieces of W in a step of 4096 tokens, 65536 classes, 5120 wide, 2.6 % of its
+// 10.4 ms; G leaves its tiles in both orders).
 //
 // The products are bound by the matrix cores: v_mfma_f32_32x32x16_bf16, 256 x
 // 256 tiles, eight waves of 128 x 64 (two to a SIMD: while one of them waits to
