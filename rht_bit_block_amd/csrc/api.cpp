@@ -11,6 +11,7 @@
 #include <cstring>
 
 #include "../../include/ufp4.h"
+#include "lm_internal.h"
 #include "ufp4_internal.h"
 
 using namespace ufp4;

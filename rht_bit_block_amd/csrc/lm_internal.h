@@ -8,6 +8,13 @@
 
 namespace ufp4 {
 
+// Checks of a quantized operand shared by every entry point that takes one
+// (sizes, configuration, storage, alignment); UFP4_OK or a status (api.cpp).
+int check_operand(const ufp4_qtensor* t);
+// The sign bits of 128 consecutive elements that start a chunk (the n-bit
+// pattern of the configuration's seed, repeated), bit i of word i / 32 (api.cpp).
+void sign_bits128(const ufp4_quant_cfg* c, uint32_t out[4]);
+
 struct GluLaunch {
   const void* gate;        // forward inputs, dtype, row pitch ld
   const void* up;

@@ -142,13 +142,6 @@ int diag_prepare(const void* x, int64_t rows, int64_t cols, int64_t ld, const uf
 hipError_t launch_quant_cols(const QuantLaunch& q, hipStream_t s);
 hipError_t launch_quant_rows_2d(const QuantLaunch& q, hipStream_t s);
 
-// Checks of a quantized operand shared by every entry point that takes one
-// (sizes, configuration, storage, alignment); UFP4_OK or a status.
-int check_operand(const ufp4_qtensor* t);
-// The sign bits of 128 consecutive elements that start a chunk (the n-bit
-// pattern of the configuration's seed, repeated), bit i of word i / 32.
-void sign_bits128(const ufp4_quant_cfg* c, uint32_t out[4]);
-
 struct GemmLaunch {
   const uint8_t* a_codes;
   const void* a_scales;

@@ -29,3 +29,11 @@ def test_traffic_needs_matching_sources(monkeypatch):
     monkeypatch.setitem(bench.MEASURED_TRAFFIC, ("probe", "k"), (files, "0" * 16, 1000.0, 500.0))
     assert bench.measured_traffic("probe", "k") is None
     assert bench.measured_traffic("probe", "absent") is None
+
+
+def test_the_benchmark_steps_counters_are_those_of_the_present_sources():
+    """The step's kernels have HBM bytes to report: a change to their sources, the
+    headers they share included, comes with counters taken again."""
+    assert bench.MEASURED_TRAFFIC
+    for workload, kernel in bench.MEASURED_TRAFFIC:
+        assert bench.measured_traffic(workload, kernel) is not None, (workload, kernel)
