@@ -4,9 +4,9 @@
 // documents (threads per grid dimension below 2^32) and refuses the rest, as the
 // runtime does.
 //   launch_probe library function args...      (integers; pointers are integers)
-// prints "launch kernel gx gy gz bx by bz w0 .. w23" (the first words of the first
-// kernel argument, which every launch here has 192 bytes of or is not asked for)
-// per launch and "status n" at the end.
+// prints "launch kernel gx gy gz bx by bz" per launch and "status n" at the end; for
+// kernels with the text of PROBE_WORDS in their name, whose first argument has to
+// be a struct of 144 bytes or more, also that struct's first 18 words.
 #include <dlfcn.h>
 #include <stdint.h>
 #include <stdio.h>
@@ -75,8 +75,9 @@ int hipLaunchKernel(const void* f, Dim g, Dim b, void** args, size_t, void*) {
     return last;
   }
   printf("launch %s %u %u %u %u %u %u", names[f].c_str(), g.x, g.y, g.z, b.x, b.y, b.z);
-  if (getenv("PROBE_WORDS")) {   // only where the first argument is a struct
-    uint64_t w[24];
+  const char* with = getenv("PROBE_WORDS");
+  if (with && names[f].find(with) != std::string::npos) {
+    uint64_t w[18];
     memcpy(w, args[0], sizeof(w));
     for (uint64_t v : w) printf(" %llu", (unsigned long long)v);
   }

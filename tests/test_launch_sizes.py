@@ -21,11 +21,12 @@ def probe(tmp_path_factory):
     subprocess.run(["g++", "-O1", "-rdynamic", os.path.join(HERE, "launch_probe.cpp"), "-o", exe, "-ldl"],
                    check=True)
 
-    def call(fn, *args, words=False):
-        """(status, [(kernel, grid x y z, block x y z, words of the first argument)])"""
+    def call(fn, *args, words=None):
+        """(status, [(kernel, grid x y z, block x y z, words of the first argument)]);
+        words: part of the names of the kernels whose argument is asked for"""
         env = dict(os.environ)
         if words:
-            env["PROBE_WORDS"] = "1"
+            env["PROBE_WORDS"] = words
         r = subprocess.run([exe, U.LIB_PATH, fn, *(str(int(a)) for a in args)], capture_output=True,
                            text=True, check=True, env=env)
         lines = [x.split() for x in r.stdout.splitlines()]
@@ -42,7 +43,7 @@ GATE, UP, ROW, H, GC, GS, DH, DG, DU, DROW, ROWS = 0, 1, 3, 4, 6, 7, 10, 12, 13,
 
 def glu_bwd(probe, rows, cols, dtype, drow, again):
     return probe("ufp4_glu_bwd", P, 2 * P, 3 * P, 4 * P, rows, cols, 0, 5 * P, 6 * P, dtype, cols, 7 * P,
-                 8 * P, cols, 9 * P if drow else 0, 10 * P if again else 0, cols, 0, words=True)
+                 8 * P, cols, 9 * P if drow else 0, 10 * P if again else 0, cols, 0, words="k_glu")
 
 
 @pytest.mark.parametrize("rows,cols", [(1 << 26, 32), ((1 << 28) + 3, 1), (1 << 26, 128), (1 << 27, 129),
@@ -69,7 +70,7 @@ def test_glu_backward_with_the_row_factors_gradient(probe, rows, cols, dtype):
 @pytest.mark.parametrize("rows,cols", [(1 << 26, 32), ((1 << 28) + 3, 1), (1 << 27, 129), (1, 1 << 30)])
 def test_glu_forward_and_backward_without_it(probe, rows, cols):
     fwd = probe("ufp4_glu_fwd", P, 2 * P, 1, rows, cols, cols, 0, 3 * P, 4 * P, cols, 5 * P, 6 * P, 7 * P,
-                8 * P, 0, words=True)
+                8 * P, 0, words="k_glu")
     chunks = 4 * ((cols + 31) // 32)
     for st, got in (fwd, glu_bwd(probe, rows, cols, 1, False, False)):
         assert st == U.UFP4_OK
@@ -88,7 +89,7 @@ B_, M_, N_, LDB = 1, 2, 3, 6
 W, HID, TG, WS = P, 2 * P, 3 * P, 4 * P
 
 
-def xent_fwd(probe, T, V, D, words=False):
+def xent_fwd(probe, T, V, D, words=None):
     return probe("ufp4_linear_xent_fwd", HID, D, W, D, TG, T, V, D, 5 * P, 6 * P, WS, 1 << 62, 0, words=words)
 
 
@@ -108,8 +109,7 @@ def test_xent_forward_slices(probe):
     """Slices of tokens follow one another, all with the tile shape that the
     workspace is laid out for, a last one of 33 tokens too."""
     T, V, D = (1 << 20) + 33, 1 << 20, 64
-    st, got = probe("ufp4_linear_xent_fwd", HID, D, W, D, TG, T, V, D, 5 * P, 6 * P, WS, 1 << 62, 0,
-                    words=True)
+    st, got = xent_fwd(probe, T, V, D, words="k_prod")
     at = 0
     assert st == U.UFP4_OK and len(got) > 2
     for name, g, w in got[:-1]:
@@ -142,7 +142,7 @@ def test_xent_forward_slices_write_their_own_tokens(probe):
     """A slice's statistics, target logits and targets start at its first token;
     the statistics' rows keep the pitch of all tokens."""
     T, V, D, part, part_ld, zt, targets = 1 << 21, 1 << 19, 8, 10, 11, 12, 13
-    st, got = xent_fwd(probe, T, V, D, words=True)
+    st, got = xent_fwd(probe, T, V, D, words="k_prod")
     assert st == U.UFP4_OK and len(got) > 3
     rows = V // 256 * 2
     at = 0
