@@ -431,7 +431,7 @@ def _exact_quantized(x, case, turn):
         e = torch.where(size <= torch.exp2(e - 1), e - 1, e)
         size = torch.exp2(torch.where(size > torch.exp2(e), e + 1, e).clamp(-127, 127))
     grid = torch.tensor(sorted(set(abs(v) for v in LEVELS[case["grid"]] if abs(v) <= top)), dtype=torch.float64, device=y.device)
-    a = torch.where(m > 0, y.abs() / size, torch.zeros_like(y))
+    a = torch.where(m > 0, (y.abs() / size).float().double(), torch.zeros_like(y))  # and so is the quotient that is rounded
     up = torch.searchsorted(grid, a.contiguous()).clamp(1, 7)
     low, high = grid[up - 1], grid[up]
     mid = (low + high) / 2
