@@ -462,6 +462,132 @@ int ufp4_moe_tokens(const void* x, int64_t ldx, int64_t T, const float* logits, 
 /* Workspace bytes of ufp4_moe_tokens; 0 for sizes that it refuses and T = 0. */
 size_t ufp4_moe_tokens_workspace_bytes(int64_t T, int32_t E, int32_t top_k, int64_t H, int64_t F);
 
+/* ---------------------------------------------------------------------------
+ * Attention: causal, over packed sequences, with heads that share keys; and
+ * the same over a cache of keys and values held in 4 bits.  The conventions of
+ * the language-model operators hold.
+ *
+ * Packed rows.  The tokens of B sequences lie one after another in T rows;
+ * starts is a DEVICE int32 [B+1], ascending: sequence b is rows starts[b] ..
+ * starts[b+1] - 1 (none: an empty sequence).  Rows before starts[0] and from
+ * starts[B] on belong to no sequence: they are not read, and outputs keep what
+ * they hold there.  Values outside 0 .. T, or not ascending, never lead to an
+ * access outside the arrays, but which rows are computed is then unspecified.
+ * Row t of a tensor with heads holds head h at elements t ld + h D .. + D - 1
+ * (ld >= heads D), so a slice of a joint QKV product serves as it is; every
+ * such tensor is bf16, 16-byte aligned, with ld % 8 == 0 and D % 8 == 0.  heads
+ * is a multiple of kv_heads: head h reads key head h / (heads / kv_heads).
+ * ------------------------------------------------------------------------- */
+
+/* Attention of every sequence over itself, token i over tokens 0 .. i:
+ *   z[i][j] = scale q[i] . k[j]  (j <= i)     lse[i] = log sum over j of e^z[i][j]
+ *   o[i] = sum over j of e^(z[i][j] - lse[i]) v[j]
+ *   q, o : [T][heads][D], k, v : [T][kv_heads][D];  lse : fp32 [T][heads], or
+ *   NULL (no gradient wanted).
+ * Products of the inputs are exact and summed in fp32, as are the weights' sums;
+ * the weights e^(z - m) (m: a maximum of the row, up to 2^8 above 1) are rounded to bf16 for the second
+ * product, o once at the end.  An infinity or NaN in a token may turn up in
+ * earlier tokens of the same sequence, never in another one.
+ * Errors: UFP4_ERR_INVALID_ARG (negative sizes, null pointers, pitches,
+ * alignment, a scale that is not finite, heads not a multiple of kv_heads),
+ * UFP4_ERR_SHAPE (D % 8), UFP4_ERR_UNSUPPORTED (D > 128, T > 2^30, B > 2^20,
+ * heads > 1024, a pitch > 2^22).  T = 0 or B = 0 is a no-op. */
+int ufp4_attn_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                  int64_t ldv, const int32_t* starts, int32_t B, int64_t T, int32_t heads,
+                  int32_t kv_heads, int32_t D, float scale, void* o, int64_t ldo, float* lse,
+                  void* stream);
+
+/* Gradients of ufp4_attn_fwd: with p = e^(z - lse), do the gradient of o and
+ * delta[i] = do[i] . o[i],
+ *   dv[j] = sum over i of p[i][j] do[i]
+ *   ds[i][j] = scale p[i][j] (do[i] . v[j] - delta[i])
+ *   dq[i] = sum over j of ds[i][j] k[j]      dk[j] = sum over i of ds[i][j] q[i]
+ * dk and dv sum over the heads that share a key head.  p and ds / scale are
+ * rounded to bf16 for the products, whose sums are fp32; the outputs (bf16,
+ * laid out as q, k and v) are rounded once.  o and lse are the forward call's.
+ * Equal inputs give equal bits.  workspace: ufp4_attn_workspace_bytes(T,
+ * heads) bytes, 256-byte aligned, any contents; calls that share one must be
+ * ordered on one stream.  Errors as the forward call, and
+ * UFP4_ERR_INVALID_ARG for a workspace that is too small. */
+int ufp4_attn_bwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
+                  int64_t ldv, const int32_t* starts, int32_t B, int64_t T, int32_t heads,
+                  int32_t kv_heads, int32_t D, float scale, const void* o, int64_t ldo,
+                  const float* lse, const void* dout, int64_t lddo, void* dq, int64_t lddq,
+                  void* dk, int64_t lddk, void* dv, int64_t lddv, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of ufp4_attn_bwd; 0 for sizes that it refuses and T = 0. */
+size_t ufp4_attn_workspace_bytes(int64_t T, int32_t heads);
+
+/* A cache of keys and values in 4 bits, in pages of page_tokens tokens:
+ *   k_codes, v_codes   : uint8 [pages][kv_heads][page_tokens][D / 2]
+ *   k_scales, v_scales : fp32 or uint8 [pages][kv_heads][page_tokens][D / block_cols]
+ * A token's row of one head is quantized as ufp4_rht_quant (along = 0, K = D)
+ * quantizes a row: the whole of k_codes / k_scales is a ufp4_qtensor with P =
+ * pages kv_heads page_tokens, K = D, which ufp4_dequant reads.  cfg: a 4-bit
+ * codebook, 1 x 16 or 1 x 32 blocks, UFP4_RTNE, tensor_scale 0; D a multiple of
+ * 16, block_cols and rht_n, at most 128; page_tokens a power of two up to 2^16.
+ * Device pointers, codes 16-byte and scales 16-byte aligned. */
+typedef struct ufp4_kv_cache {
+  uint8_t* k_codes;
+  void* k_scales;
+  uint8_t* v_codes;
+  void* v_scales;
+  int64_t pages;
+  int32_t page_tokens;
+  int32_t kv_heads;
+  int32_t D;
+  ufp4_quant_cfg cfg;
+} ufp4_kv_cache;
+
+/* The cache's calls share what says where a token lies.  lens : DEVICE int32
+ * [B], the tokens of each sequence in the cache, the packed rows included: row
+ * i of sequence b's n = starts[b+1] - starts[b] rows is its token lens[b] - n +
+ * i, and token t lies in row t % page_tokens of page table[b][t /
+ * page_tokens] (table : DEVICE int32 [B][ldt], ldt >= width).  A token without
+ * a place -- before token 0, past the table's width, or whose page is not in 0
+ * .. pages - 1 -- is not written, reads as zeros, and is not attended to.
+ * Sequences may share pages that no call writes.
+ * Errors of all three: UFP4_ERR_INVALID_ARG (negative sizes, null pointers,
+ * pitches, alignment, page_tokens, heads), UFP4_ERR_SHAPE (D),
+ * UFP4_ERR_UNSUPPORTED (what cfg does not allow here, T > 2^30, B > 2^20,
+ * width or a pitch > 2^22, kv_heads or heads > 1024), UFP4_ERR_INVALID_ARG or
+ * as ufp4_rht_quant for cfg.  T = 0 or B = 0 is a no-op. */
+
+/* Quantizes rows k, v (bf16 [T][kv_heads][D]) into the cache. */
+int ufp4_kv_write(const void* k, int64_t ldk, const void* v, int64_t ldv, const int32_t* starts,
+                  int32_t B, int64_t T, const int32_t* lens, const int32_t* table, int64_t ldt,
+                  int64_t width, const ufp4_kv_cache* cache, void* stream);
+
+/* Reads rows back: k, v (bf16 [T][kv_heads][D]) = what the codes stand for,
+ * out of the basis of the rotation, x = S RN(c_n FWHT(level s)), rounded once
+ * more to bf16.  Starts that begin at 0 with n = lens[b] read whole sequences. */
+int ufp4_kv_read(const ufp4_kv_cache* cache, const int32_t* starts, int32_t B, int64_t T,
+                 const int32_t* lens, const int32_t* table, int64_t ldt, int64_t width, void* k,
+                 int64_t ldk, void* v, int64_t ldv, void* stream);
+
+/* Attention of the packed rows over the cache (generation: one or a few new
+ * tokens per sequence, whose keys and values have been written): row i of
+ * sequence b, which is its token t = lens[b] - n + i, over tokens 0 .. t,
+ *   z[j] = scale q . k[j]      o = sum over j of e^(z[j] - lse) v[j]
+ * with k, v what the codes stand for.  q is rotated instead of the keys, and o
+ * instead of the values ([UFP4] Method: the rotation cancels in the product).
+ * A row with nothing to attend to has o = 0.  Any number of rows is right; the
+ * call is made for few.
+ *   q, o : bf16 [T][heads][D].
+ * q keeps 16 bits of mantissa, levels are exact, scales and sums fp32; weights
+ * times value scales are rounded to bf16, o once at the end.  Equal inputs give
+ * equal bits.  workspace: ufp4_kv_attn_workspace_bytes bytes, 256-byte aligned,
+ * any contents; calls that share one must be ordered on one stream. */
+int ufp4_kv_attn(const void* q, int64_t ldq, const int32_t* starts, int32_t B, int64_t T,
+                 int32_t heads, const int32_t* lens, const int32_t* table, int64_t ldt,
+                 int64_t width, const ufp4_kv_cache* cache, float scale, void* o, int64_t ldo,
+                 void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of ufp4_kv_attn; 0 for sizes that it refuses and T = 0. */
+size_t ufp4_kv_attn_workspace_bytes(int64_t T, int32_t B, int32_t heads, int32_t kv_heads,
+                                    int32_t D);
+
 /* Name of a status code (static string). */
 const char* ufp4_status_string(int status);
 

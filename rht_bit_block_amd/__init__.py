@@ -41,6 +41,8 @@ EXPORTED = [
     "ufp4_glu_fwd", "ufp4_glu_bwd",
     "ufp4_linear_xent_fwd", "ufp4_linear_xent_bwd", "ufp4_linear_xent_workspace_bytes",
     "ufp4_moe_tokens", "ufp4_moe_tokens_workspace_bytes",
+    "ufp4_attn_fwd", "ufp4_attn_bwd", "ufp4_attn_workspace_bytes",
+    "ufp4_kv_write", "ufp4_kv_read", "ufp4_kv_attn", "ufp4_kv_attn_workspace_bytes",
 ]
 
 
@@ -79,6 +81,13 @@ class QTensorC(ctypes.Structure):
                 ("P", ctypes.c_int64), ("K", ctypes.c_int64), ("cfg", QuantCfg)]
 
 
+class KVCacheC(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("page_tokens", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("D", ctypes.c_int32), ("cfg", QuantCfg)]
+
+
 @dataclass
 class QTensor:
     """A quantized logical operand: codes uint8 [P, K/2], scales (fp32 or
@@ -112,6 +121,7 @@ def _lib():
         vp, i64, i32, u64, u32 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
                                   ctypes.c_uint64, ctypes.c_uint32)
         cfgp, qtp = ctypes.POINTER(QuantCfg), ctypes.POINTER(QTensorC)
+        kvp, f32 = ctypes.POINTER(KVCacheC), ctypes.c_float
         i64p = ctypes.POINTER(ctypes.c_int64)
         sig = {
             "ufp4_rht_quant": [vp, i64, i64, i64, i32, cfgp, vp, vp, vp, vp],
@@ -139,6 +149,14 @@ def _lib():
                                      i64, vp, ctypes.c_size_t, vp],
             "ufp4_moe_tokens": [vp, i64, i64, vp, i64, i32, i32, i32, i32, qtp, qtp, qtp, vp, i64,
                                 vp, ctypes.c_size_t, vp],
+            "ufp4_attn_fwd": [vp, i64, vp, i64, vp, i64, vp, i32, i64, i32, i32, i32, f32, vp, i64,
+                              vp, vp],
+            "ufp4_attn_bwd": [vp, i64, vp, i64, vp, i64, vp, i32, i64, i32, i32, i32, f32, vp, i64,
+                              vp, vp, i64, vp, i64, vp, i64, vp, i64, vp, ctypes.c_size_t, vp],
+            "ufp4_kv_write": [vp, i64, vp, i64, vp, i32, i64, vp, vp, i64, i64, kvp, vp],
+            "ufp4_kv_read": [kvp, vp, i32, i64, vp, vp, i64, i64, vp, i64, vp, i64, vp],
+            "ufp4_kv_attn": [vp, i64, vp, i32, i64, i32, vp, vp, i64, i64, kvp, f32, vp, i64, vp,
+                             ctypes.c_size_t, vp],
         }
         for name, args in sig.items():
             f = getattr(lib, name)
@@ -150,6 +168,10 @@ def _lib():
         lib.ufp4_linear_xent_workspace_bytes.restype = ctypes.c_size_t
         lib.ufp4_moe_tokens_workspace_bytes.argtypes = [i64, i32, i32, i64, i64]
         lib.ufp4_moe_tokens_workspace_bytes.restype = ctypes.c_size_t
+        lib.ufp4_attn_workspace_bytes.argtypes = [i64, i32]
+        lib.ufp4_attn_workspace_bytes.restype = ctypes.c_size_t
+        lib.ufp4_kv_attn_workspace_bytes.argtypes = [i64, i32, i32, i32, i32]
+        lib.ufp4_kv_attn_workspace_bytes.restype = ctypes.c_size_t
         lib.ufp4_codes_bytes.argtypes = [i64, i64]
         lib.ufp4_codes_bytes.restype = ctypes.c_size_t
         lib.ufp4_scales_bytes.argtypes = [i64, i64, cfgp]
@@ -765,6 +787,242 @@ def ufp4_moe_tokens(x: torch.Tensor, logits: torch.Tensor, wg: QTensor, wu: QTen
                                 ctypes.byref(c), _ptr(out), ldy, _ptr(workspace),
                                 workspace.numel(), _stream(x))
     _check("ufp4_moe_tokens", st)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Attention over packed sequences, and over a cache held in 4 bits
+# ---------------------------------------------------------------------------
+def _check_heads(name, t, shape=None, device=None):
+    """A bfloat16 tensor [rows, heads, D] whose row holds its heads one after
+    another; returns its row pitch."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be a 3-D bfloat16 tensor [rows, heads, D]")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
+    rows, heads, D = t.shape
+    if heads < 1 or D < 1:
+        raise ValueError(f"{name} has no heads or no elements in a head")
+    if rows and ((D > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != D)):
+        raise ValueError(f"{name}: the heads of a row must lie one after another")
+    if rows > 1 and t.stride(0) < heads * D:
+        raise ValueError(f"{name} row pitch {t.stride(0)} is below its {heads * D} elements")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return t.stride(0) if rows > 1 else (heads * D + 7) // 8 * 8
+
+
+def _check_starts(starts, device):
+    if not isinstance(starts, torch.Tensor) or starts.dim() != 1 or starts.shape[0] < 1:
+        raise ValueError("starts must be a 1-D int32 tensor of one more elements than sequences")
+    _check_vector("starts", starts, starts.shape[0], torch.int32, device)
+    return starts.shape[0] - 1
+
+
+def _attn_inputs(q, k, v, starts, scale):
+    ldq = _check_heads("q", q)
+    T, heads, D = q.shape
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a 3-D bfloat16 tensor [rows, heads, D]")
+    kv_heads = k.shape[1]
+    ldk = _check_heads("k", k, (T, kv_heads, D), q.device)
+    ldv = _check_heads("v", v, (T, kv_heads, D), q.device)
+    if heads % kv_heads:
+        raise ValueError(f"{heads} heads do not share {kv_heads} key heads evenly")
+    B = _check_starts(starts, q.device)
+    return T, B, heads, kv_heads, D, ldq, ldk, ldv, D ** -0.5 if scale is None else float(scale)
+
+
+def ufp4_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor,
+                  scale=None, out=None, lse=True):
+    """Causal attention of packed sequences (q [T, heads, D], k, v [T, kv_heads, D]
+    bfloat16, D % 8 == 0, D <= 128; starts int32 [B + 1] on the GPU: sequence b is rows
+    starts[b] .. starts[b+1] - 1).  scale: D ** -0.5 when not given.  Returns (o
+    [T, heads, D] bfloat16, lse [T, heads] float32); lse=False skips the latter, a
+    tensor is written into.  Rows of no sequence keep what out and lse hold."""
+    T, B, heads, kv_heads, D, ldq, ldk, ldv, scale = _attn_inputs(q, k, v, starts, scale)
+    dev = q.device
+    if out is None:
+        out = torch.empty((T, heads, D), dtype=torch.bfloat16, device=dev)
+    ldo = _check_heads("out", out, q.shape, dev)
+    if lse is True:
+        lse = torch.empty((T, heads), dtype=torch.float32, device=dev)
+    elif lse is False:
+        lse = None
+    if lse is not None:
+        _check_buffer("lse", lse, torch.float32, T * heads, dev)
+    _on_gpu(q, "q")
+    st = _lib().ufp4_attn_fwd(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(starts), B, T, heads,
+                              kv_heads, D, scale, _ptr(out), ldo, _ptr(lse), _stream(q))
+    _check("ufp4_attn_fwd", st)
+    return out, lse
+
+
+def ufp4_attn_workspace_bytes(T, heads):
+    return int(_lib().ufp4_attn_workspace_bytes(int(T), int(heads)))
+
+
+def ufp4_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor,
+                  o: torch.Tensor, lse: torch.Tensor, dout: torch.Tensor, scale=None, out=None,
+                  workspace=None):
+    """Gradients (dq, dk, dv, bfloat16) of ufp4_attn_fwd for the gradient dout of o; o and
+    lse are the forward call's.  out: optional (dq, dk, dv) to write into; workspace: uint8
+    device buffer of ufp4_attn_workspace_bytes(T, heads) (allocated when not given)."""
+    T, B, heads, kv_heads, D, ldq, ldk, ldv, scale = _attn_inputs(q, k, v, starts, scale)
+    dev = q.device
+    ldo = _check_heads("o", o, q.shape, dev)
+    lddo = _check_heads("dout", dout, q.shape, dev)
+    _check_buffer("lse", lse, torch.float32, T * heads, dev)
+    if out is None:
+        out = tuple(torch.empty(x.shape, dtype=torch.bfloat16, device=dev) for x in (q, k, v))
+    dq, dk, dv = out
+    lddq = _check_heads("dq", dq, q.shape, dev)
+    lddk = _check_heads("dk", dk, k.shape, dev)
+    lddv = _check_heads("dv", dv, v.shape, dev)
+    _on_gpu(q, "q")
+    need = ufp4_attn_workspace_bytes(T, heads)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _check_buffer("workspace", workspace, torch.uint8, need, dev)
+    st = _lib().ufp4_attn_bwd(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(starts), B, T, heads,
+                              kv_heads, D, scale, _ptr(o), ldo, _ptr(lse), _ptr(dout), lddo,
+                              _ptr(dq), lddq, _ptr(dk), lddk, _ptr(dv), lddv, _ptr(workspace),
+                              workspace.numel(), _stream(q))
+    _check("ufp4_attn_bwd", st)
+    return dq, dk, dv
+
+
+@dataclass
+class KVCache:
+    """Keys and values in 4 bits, in pages: codes uint8 [pages, kv_heads, page_tokens, D / 2]
+    and scales (float32, or E8M0 uint8) [pages, kv_heads, page_tokens, D / block_cols]."""
+    k_codes: torch.Tensor
+    k_scales: torch.Tensor
+    v_codes: torch.Tensor
+    v_scales: torch.Tensor
+    cfg: QuantCfg
+
+    @staticmethod
+    def empty(pages, kv_heads, page_tokens, D, cfg, device="cuda"):
+        """A cache whose pages hold nothing yet (not cleared)."""
+        code = lambda: torch.empty((pages, kv_heads, page_tokens, D // 2), dtype=torch.uint8,  # noqa: E731
+                                   device=device)
+        scale = lambda: torch.empty((pages, kv_heads, page_tokens, D // cfg.block_cols),  # noqa: E731
+                                    dtype=scales_dtype(cfg), device=device)
+        return KVCache(code(), scale(), code(), scale(), cfg)
+
+    def check(self):
+        """(pages, kv_heads, page_tokens, D), after checking the buffers against each other."""
+        if not isinstance(self.k_codes, torch.Tensor) or self.k_codes.dim() != 4:
+            raise ValueError("k_codes must be a 4-D uint8 tensor [pages, kv_heads, page_tokens, D / 2]")
+        pages, heads, page, half = self.k_codes.shape
+        dev, block = self.k_codes.device, max(1, self.cfg.block_cols)
+        if half < 1 or (2 * half) % block:
+            raise ValueError(f"a head of {2 * half} elements does not hold whole blocks of {block}")
+        for name, t, dt, n in (("k_codes", self.k_codes, torch.uint8, half),
+                               ("v_codes", self.v_codes, torch.uint8, half),
+                               ("k_scales", self.k_scales, scales_dtype(self.cfg), 2 * half // block),
+                               ("v_scales", self.v_scales, scales_dtype(self.cfg), 2 * half // block)):
+            if not isinstance(t, torch.Tensor) or t.dtype != dt or t.shape != (pages, heads, page, n):
+                raise ValueError(f"{name} must be a {dt} tensor of shape ({pages}, {heads}, {page}, {n})")
+            if not t.is_contiguous():
+                raise ValueError(f"{name} must be contiguous")
+            if t.device != dev:
+                raise ValueError(f"{name} must be on {dev}")
+        return pages, heads, page, 2 * half
+
+    def c(self):
+        pages, heads, page, D = self.check()
+        return KVCacheC(self.k_codes.data_ptr(), self.k_scales.data_ptr(), self.v_codes.data_ptr(),
+                        self.v_scales.data_ptr(), pages, page, heads, D, self.cfg)
+
+    def qtensors(self):
+        """Keys and values of all pages as QTensors, e.g. for ufp4_dequant (in the basis of the
+        rotation)."""
+        pages, heads, page, D = self.check()
+        rows = pages * heads * page
+        return (QTensor(self.k_codes, self.k_scales, rows, D, self.cfg),
+                QTensor(self.v_codes, self.v_scales, rows, D, self.cfg))
+
+
+def _cache_places(cache, starts, lens, table):
+    dev = cache.k_codes.device if isinstance(cache.k_codes, torch.Tensor) else None
+    c = cache.c()
+    B = _check_starts(starts, dev)
+    _check_vector("lens", lens, B, torch.int32, dev)
+    ldt = _check_input("table", table, None, torch.int32, dev)
+    if table.shape[0] != B:
+        raise ValueError(f"table has {table.shape[0]} rows, there are {B} sequences")
+    return c, dev, B, ldt, table.shape[1]
+
+
+def ufp4_kv_write(k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor, lens: torch.Tensor,
+                  table: torch.Tensor, cache: KVCache):
+    """Quantizes packed rows k, v ([T, kv_heads, D] bfloat16) into the cache: row i of sequence
+    b's n = starts[b+1] - starts[b] rows becomes its token lens[b] - n + i, which lies in page
+    table[b, token // page_tokens] (starts int32 [B + 1], lens int32 [B], table int32 [B, pages
+    of the longest sequence], all on the GPU).  A token without a place is not written."""
+    c, dev, B, ldt, width = _cache_places(cache, starts, lens, table)
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a 3-D bfloat16 tensor [rows, heads, D]")
+    T = k.shape[0]
+    ldk = _check_heads("k", k, (T, c.kv_heads, c.D), dev)
+    ldv = _check_heads("v", v, (T, c.kv_heads, c.D), dev)
+    _on_gpu(k, "k")
+    st = _lib().ufp4_kv_write(_ptr(k), ldk, _ptr(v), ldv, _ptr(starts), B, T, _ptr(lens),
+                              _ptr(table), ldt, width, ctypes.byref(c), _stream(k))
+    _check("ufp4_kv_write", st)
+
+
+def ufp4_kv_read(cache: KVCache, starts: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
+                 T: int, out=None):
+    """The rows that a write of the same starts, lens and table wrote, as the cache holds them:
+    (k, v) bfloat16 [T, kv_heads, D], not rotated; T rows in all (starts[B]).  With lens[b] rows
+    of each sequence: the whole sequences.  A token without a place reads as zeros; rows of no
+    sequence keep what out = (k, v) holds."""
+    c, dev, B, ldt, width = _cache_places(cache, starts, lens, table)
+    shape = (int(T), c.kv_heads, c.D)
+    if out is None:
+        out = tuple(torch.empty(shape, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    k, v = out
+    ldk, ldv = _check_heads("k", k, shape, dev), _check_heads("v", v, shape, dev)
+    _on_gpu(k, "k")
+    st = _lib().ufp4_kv_read(ctypes.byref(c), _ptr(starts), B, shape[0], _ptr(lens), _ptr(table),
+                             ldt, width, _ptr(k), ldk, _ptr(v), ldv, _stream(k))
+    _check("ufp4_kv_read", st)
+    return k, v
+
+
+def ufp4_kv_attn_workspace_bytes(T, B, heads, kv_heads, D):
+    return int(_lib().ufp4_kv_attn_workspace_bytes(int(T), int(B), int(heads), int(kv_heads), int(D)))
+
+
+def ufp4_kv_attn(q: torch.Tensor, starts: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
+                 cache: KVCache, scale=None, out=None, workspace=None):
+    """Attention of packed rows q ([T, heads, D] bfloat16, not rotated) over the cache; starts,
+    lens and table as in the write that put these rows' keys and values there, each row sees its
+    own token and those before.  Returns o [T, heads, D] bfloat16 (a row with nothing to attend
+    to: 0).  scale: D ** -0.5 when not given; workspace: uint8 device buffer of
+    ufp4_kv_attn_workspace_bytes (allocated when not given)."""
+    c, dev, B, ldt, width = _cache_places(cache, starts, lens, table)
+    ldq = _check_heads("q", q, None, dev)
+    T, heads, D = q.shape
+    if D != c.D or heads % c.kv_heads:
+        raise ValueError(f"q has {heads} heads of {D}, the cache {c.kv_heads} of {c.D}")
+    if out is None:
+        out = torch.empty((T, heads, D), dtype=torch.bfloat16, device=dev)
+    ldo = _check_heads("out", out, q.shape, dev)
+    _on_gpu(q, "q")
+    need = ufp4_kv_attn_workspace_bytes(T, B, heads, c.kv_heads, D)
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _check_buffer("workspace", workspace, torch.uint8, need, dev)
+    st = _lib().ufp4_kv_attn(_ptr(q), ldq, _ptr(starts), B, T, heads, _ptr(lens), _ptr(table), ldt,
+                             width, ctypes.byref(c), D ** -0.5 if scale is None else float(scale),
+                             _ptr(out), ldo, _ptr(workspace), workspace.numel(), _stream(q))
+    _check("ufp4_kv_attn", st)
     return out
 
 
