@@ -470,7 +470,7 @@ size_t ufp4_moe_tokens_workspace_bytes(int64_t T, int32_t E, int32_t top_k, int6
  * Packed rows.  The tokens of B sequences lie one after another in T rows;
  * starts is a DEVICE int32 [B+1], ascending: sequence b is rows starts[b] ..
  * starts[b+1] - 1 (none: an empty sequence).  Rows before starts[0] and from
- * starts[B] on belong to no sequence: they are not read, and outputs keep what
+ * starts[B] on belong to no sequence: what they hold does not matter, and outputs keep what
  * they hold there.  Values outside 0 .. T, or not ascending, never lead to an
  * access outside the arrays, but which rows are computed is then unspecified.
  * Row t of a tensor with heads holds head h at elements t ld + h D .. + D - 1

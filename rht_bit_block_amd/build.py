@@ -28,7 +28,9 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.cpp", "quant.hip", "quant_e1m2.hip", "quant_int4.hip", "quant_e2m1.hip", "quant_e4m3.hip",
            "gemm.hip", "gemm_rd.hip", "gemm_mx.hip", "misc.hip", "noalloc.hip",
-           "api_lm.cpp", "glu.hip", "xent.hip", "moe_tokens.hip"]
+           "api_lm.cpp", "glu.hip", "xent.hip", "moe_tokens.hip",
+           "api_attn.cpp", "attn.hip", "attn_grad.hip", "kv_rows.hip", "kv_e1m2.hip", "kv_int4.hip",
+           "kv_e2m1.hip", "kv_attn.hip"]
 
 # -ffp-contract=off: every fp32 operation that decides an output bit is an
 # explicit round-to-nearest op; no silent fma contraction.

@@ -1,0 +1,192 @@
+// Pieces that the attention kernels share: how a workgroup finds its sequence,
+// copies of K or V tiles into LDS, and the fragments that the matrix
+// instructions read from them.
+//
+// Everything is built on v_mfma_f32_32x32x16_bf16, C[m][n] = sum_k A[m][k]
+// B[n][k]: lane l holds A's row (B's row) l % 32 with k = 8 (l / 32) .. + 7, and
+// of C the column n = l % 32 with rows m = 8 (r / 4) + 4 (l / 32) + r % 4 in
+// registers r = 0 .. 15.  A product's registers 8 t .. 8 t + 7 therefore are a
+// fragment of the next product, which contracts over m, as long as the other
+// operand's lane holds the same sixteen m in the same order: rows 16 t + 4 (l /
+// 32) + {0 .. 3} and those + 8.  The transposing LDS read gives just that from
+// row-major tiles (16 lanes read 4 rows of 16 elements and each gets a column), so
+// neither the weights nor V, nor the gradients' operands, are ever exchanged
+// between lanes or stored turned.
+#pragma once
+
+#include "attn_internal.h"
+#include "lds_copy.h"
+
+namespace ufp4 {
+namespace attn {
+
+typedef float floatx16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr uint32_t kOutside = 0x7FFFFF00u;   // an offset past every buffer: reads as zeros
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const f32x2 v = {a, b};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+}
+
+__device__ __forceinline__ uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)p;
+}
+
+// The larger of x in lanes l and l ^ 32; their sum.
+__device__ __forceinline__ float both_max(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float both_sum(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// Rows of sequence b, clipped to the arrays whatever starts holds.
+__device__ __forceinline__ void rows_of(const int32_t* starts, int b, int64_t T, int64_t& row0,
+                                        int& n) {
+  const int64_t a = max(starts[b], 0), e = min((int64_t)starts[b + 1], T);
+  row0 = a;
+  n = e > a ? (int)(e - a) : 0;
+}
+
+// Tile number `tile` of the sequences' tiles of kAttnTile rows, one sequence after
+// another: its sequence's first row and length, and the tile's number in it;
+// false past the last one.  The whole wave works on it, 64 sequences a step.
+__device__ __forceinline__ bool find_tile(const int32_t* starts, int B, int64_t T, int tile,
+                                          int64_t& row0, int& n, int& t) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int b0 = 0; b0 < B; b0 += 64) {
+    int64_t r0 = 0;
+    int rows = 0;
+    if (b0 + lane < B) rows_of(starts, b0 + lane, T, r0, rows);
+    const int own = (rows + kAttnTile - 1) / kAttnTile;
+    int upto = own;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int x = __shfl_up(upto, d);
+      if (lane >= d) upto += x;
+    }
+    const uint64_t past = __ballot(before + upto > tile);
+    if (past) {
+      const int l = __builtin_ctzll(past);
+      t = __builtin_amdgcn_readfirstlane(tile - before - __shfl(upto - own, l));
+      n = __builtin_amdgcn_readfirstlane(__shfl(rows, l));
+      const int r = __shfl((int)r0, l);
+      row0 = __builtin_amdgcn_readfirstlane(r);
+      return true;
+    }
+    before += __shfl(upto, 63);
+  }
+  return false;
+}
+
+// A tile of `R` rows of up to DP elements in LDS, rows of DP elements whose 16-byte
+// chunks are exchanged by the row's number, so that neighbouring rows reading
+// one chunk fall on different banks.
+template <int DP>
+__device__ __forceinline__ uint32_t swz(int row) {
+  return DP == 128 ? row & 15 : (row >> 1) & 7;
+}
+template <int DP>
+__device__ __forceinline__ uint32_t chunk_at(int row, int c) {
+  return (uint32_t)(row * (DP * 2)) + 16u * ((uint32_t)c ^ swz<DP>(row));
+}
+
+// Copies of a tile of 64 rows: instruction i of wave w carries rows (w PER + i) ROWS
+// .. + ROWS - 1, ROWS = 512 / DP.
+template <int DP, int WAVES>
+struct TileCopy {
+  static constexpr int CH = DP / 8, ROWS = 64 / CH, PER = 64 / ROWS / WAVES;
+  static constexpr uint32_t BYTES = 64 * DP * 2;
+  uint32_t row, col;   // this lane's row within an instruction's, byte in its row
+
+  __device__ __forceinline__ void init(int lane) { row = lane / CH; }
+
+  // Rows j0 .. of a sequence of n rows at `base` (row 0), pitch ld elements.
+  __device__ __forceinline__ void issue(uint32_t lds, const uint16_t* base, int64_t ld, int j0,
+                                        int n, int D, int wave, int lane) const {
+    const int rows = min(n - j0, 64);
+    const sgpr4 r = rsrc4(base + (int64_t)j0 * ld,
+                          rows > 0 ? (uint32_t)(((int64_t)(rows - 1) * ld + D) * 2) : 0u);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int first = (wave * PER + i) * ROWS;
+      const int at = first + (int)row;
+      const uint32_t c = (uint32_t)(lane % CH) ^ swz<DP>(at);
+      uint32_t v = (uint32_t)at * (uint32_t)(ld * 2) + 16u * c;
+      if (8 * (int)c >= D) v = kOutside;
+      lds_load16(lds + (uint32_t)first * (DP * 2), r, v, 0u);
+    }
+  }
+};
+
+// Fragment s (16 elements of D) of 32 rows from `row0` on, rows as A's or B's rows.
+template <int DP>
+__device__ __forceinline__ bf16x8 frag_rows(const uint8_t* tile, int row0, int s, int lane) {
+  return *reinterpret_cast<const bf16x8*>(
+      tile + chunk_at<DP>(row0 + (lane & 31), 2 * s + (lane >> 5)));
+}
+
+// The turned fragment: lane l holds column d0 + l % 32 of the sixteen rows row0 + 4
+// (l / 32) + {0 .. 3, 8 .. 11}.
+template <int DP>
+__device__ __forceinline__ bf16x8 frag_turned(const uint8_t* tile, int row0, int d0, int lane) {
+  const int i = lane & 15;
+  const int row = row0 + 4 * (lane >> 5) + (i >> 2);
+  const int d = d0 + (lane & 16) + 4 * (i & 3);
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (lds_s16x4*)(tile + chunk_at<DP>(row, d >> 3) + 2 * (d & 7)));
+  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+      (lds_s16x4*)(tile + chunk_at<DP>(row + 8, d >> 3) + 2 * (d & 7)));
+  typedef short s16x8 __attribute__((ext_vector_type(8)));
+  const s16x8 v = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+// Fragments of 32 rows straight from memory (rows past n and elements past D: 0).
+template <int DP>
+__device__ __forceinline__ void load_rows(bf16x8 (&f)[DP / 16], const uint16_t* base, int64_t ld,
+                                          int row0, int n, int D, int lane) {
+  const int row = row0 + (lane & 31);
+#pragma unroll
+  for (int s = 0; s < DP / 16; ++s) {
+    const int d = 16 * s + 8 * (lane >> 5);
+    u32x4 x = {0u, 0u, 0u, 0u};
+    if (row < n && d < D) x = *reinterpret_cast<const u32x4*>(base + (int64_t)row * ld + d);
+    f[s] = __builtin_bit_cast(bf16x8, x);
+  }
+}
+
+// Registers 8 t .. 8 t + 7 of a product as a fragment, rounded to bf16.
+__device__ __forceinline__ bf16x8 frag_of(const floatx16& x, int t) {
+  const u32x4 v = {pack_bf16(x[8 * t], x[8 * t + 1]), pack_bf16(x[8 * t + 2], x[8 * t + 3]),
+                   pack_bf16(x[8 * t + 4], x[8 * t + 5]), pack_bf16(x[8 * t + 6], x[8 * t + 7])};
+  return __builtin_bit_cast(bf16x8, v);
+}
+
+__device__ __forceinline__ floatx16 mfma(const bf16x8& a, const bf16x8& b, const floatx16& c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ floatx16 zero16() {
+  floatx16 z;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) z[r] = 0.0f;
+  return z;
+}
+
+}  // namespace attn
+}  // namespace ufp4
