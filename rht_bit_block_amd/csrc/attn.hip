@@ -40,7 +40,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p) {
   const int keys = min(n, q0 + kAttnTile);
   const int tiles = (keys + 63) / 64;
 
-  TileCopy<DP, 4> copy;
+  TileCopy<DP, 64, 4> copy;
   copy.init(lane);
   const uint32_t lds0 = lds_address(lds);
   copy.issue(lds0, kb, p.ldk, 0, n, p.D, wave, lane);

@@ -92,24 +92,27 @@ __device__ __forceinline__ bool find_tile(const int32_t* starts, int B, int64_t 
   return false;
 }
 
-// A tile of `R` rows of up to DP elements in LDS, rows of DP elements whose 16-byte
-// chunks are exchanged by the row's number, so that neighbouring rows reading
-// one chunk fall on different banks.
+// A tile in LDS has rows of DP elements whose 16-byte chunks are exchanged by the
+// row's number so that both kinds of reads fill all 64 banks: sixteen rows
+// reading one chunk each (sixteen different places of a 256-byte line), and the turned reads'
+// four rows reading four neighbouring chunks each (four different quarters of
+// the line; with the row's own low bits instead, the four rows meet in one quarter:
+// 60 % of the LDS cycles of the forward pass were conflicts).
 template <int DP>
 __device__ __forceinline__ uint32_t swz(int row) {
-  return DP == 128 ? row & 15 : (row >> 1) & 7;
+  return DP == 128 ? ((row & 3) << 2) | ((row >> 2) & 3) : (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
 }
 template <int DP>
 __device__ __forceinline__ uint32_t chunk_at(int row, int c) {
   return (uint32_t)(row * (DP * 2)) + 16u * ((uint32_t)c ^ swz<DP>(row));
 }
 
-// Copies of a tile of 64 rows: instruction i of wave w carries rows (w PER + i) ROWS
+// Copies of a tile of R rows: instruction i of wave w carries rows (w PER + i) ROWS
 // .. + ROWS - 1, ROWS = 512 / DP.
-template <int DP, int WAVES>
+template <int DP, int R, int WAVES>
 struct TileCopy {
-  static constexpr int CH = DP / 8, ROWS = 64 / CH, PER = 64 / ROWS / WAVES;
-  static constexpr uint32_t BYTES = 64 * DP * 2;
+  static constexpr int CH = DP / 8, ROWS = 64 / CH, PER = R / ROWS / WAVES;
+  static_assert(PER * ROWS * WAVES == R, "the waves share the rows evenly");
   uint32_t row, col;   // this lane's row within an instruction's, byte in its row
 
   __device__ __forceinline__ void init(int lane) { row = lane / CH; }
@@ -117,7 +120,7 @@ struct TileCopy {
   // Rows j0 .. of a sequence of n rows at `base` (row 0), pitch ld elements.
   __device__ __forceinline__ void issue(uint32_t lds, const uint16_t* base, int64_t ld, int j0,
                                         int n, int D, int wave, int lane) const {
-    const int rows = min(n - j0, 64);
+    const int rows = min(n - j0, R);
     const sgpr4 r = rsrc4(base + (int64_t)j0 * ld,
                           rows > 0 ? (uint32_t)(((int64_t)(rows - 1) * ld + D) * 2) : 0u);
 #pragma unroll

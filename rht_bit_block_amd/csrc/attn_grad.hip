@@ -22,39 +22,44 @@ namespace {
 
 using namespace attn;
 
-// delta and lse log2(e), [heads][T]: sixteen lanes a row of a head.
+// delta and lse log2(e), [heads][T], 32 rows of a head to a wave.  delta is the
+// diagonal of do o^T, by the instructions that do v^T comes from: where a query
+// has one key, o is that v and do . v - delta exactly 0.
+template <int DP>
 __global__ __launch_bounds__(256) void k_attn_delta(AttnLaunch p) {
-  const int part = threadIdx.x & 15, h = blockIdx.y;
-  for (int64_t t = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4); t < p.T;
-       t += (int64_t)gridDim.x * 16) {
-    float s = 0.0f;
-    if (8 * part < p.D) {
-      const u32x4 a = *reinterpret_cast<const u32x4*>(p.o + t * p.ldo + (int64_t)h * p.D + 8 * part);
-      const u32x4 b =
-          *reinterpret_cast<const u32x4*>(p.dout + t * p.lddo + (int64_t)h * p.D + 8 * part);
+  const int lane = threadIdx.x & 63, h = blockIdx.y;
+  for (int64_t t0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 32; t0 < p.T;
+       t0 += (int64_t)gridDim.x * 128) {
+    bf16x8 a[DP / 16], b[DP / 16];
+    const int rows = (int)min(p.T - t0, (int64_t)32);
+    load_rows<DP>(a, p.dout + t0 * p.lddo + (int64_t)h * p.D, p.lddo, 0, rows, p.D, lane);
+    load_rows<DP>(b, p.o + t0 * p.ldo + (int64_t)h * p.D, p.ldo, 0, rows, p.D, lane);
+    floatx16 x = zero16();
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s = __builtin_fmaf(__uint_as_float(a[i] << 16), __uint_as_float(b[i] << 16), s);
-        s = __builtin_fmaf(__uint_as_float(a[i] & 0xFFFF0000u), __uint_as_float(b[i] & 0xFFFF0000u), s);
-      }
-    }
+    for (int s = 0; s < DP / 16; ++s) x = mfma(a[s], b[s], x);
+    // element (i, i) is register i % 4 + 4 (i / 8) of lane i or i + 32
+    const int i = lane & 31;
+    float d = 0.0f;
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1) s += __shfl_xor(s, d);
-    if (part == 0) {
-      p.delta[h * p.T + t] = s;
+    for (int r = 0; r < 16; ++r)
+      if (i == 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) d = x[r];
+    const int64_t t = t0 + i;
+    if (((i >> 2) & 1) == (lane >> 5) && i < rows) {
+      p.delta[h * p.T + t] = d;
       p.lw[h * p.T + t] = p.lse[t * p.heads + h] * kLog2e;
     }
   }
 }
 
-// dk and dv of 128 keys of one key head, 32 to a wave.
+// dk and dv of 128 keys of one key head, 32 to a wave: two waves to a SIMD, whose
+// registers hold the sums and K; V's rows stay in LDS.
 template <int DP>
-__global__ __launch_bounds__(256, 1) void k_attn_dkv(AttnLaunch p) {
+__global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p) {
   constexpr int S = DP / 16, NB = DP / 32;
-  constexpr int TILE = 64 * DP * 2;
+  constexpr int TILE = 32 * DP * 2;
   constexpr int STAGE = 2 * TILE;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * STAGE];
-  __shared__ __attribute__((aligned(16))) float stat[2][2][64];   // stage; lse log2(e), delta
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * TILE + 2 * STAGE];
+  __shared__ __attribute__((aligned(16))) float stat[2][64];   // stage; lse log2(e) and delta of 32 queries
   int64_t row0;
   int n, t;
   if (!find_tile(p.starts, p.B, p.T, (int)blockIdx.x, row0, n, t)) return;
@@ -64,71 +69,75 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(AttnLaunch p) {
   const int key = kw + (lane & 31);
   const float c = p.scale * kLog2e;
 
-  bf16x8 k[S], v[S];
+  bf16x8 k[S];
   load_rows<DP>(k, p.k + row0 * p.ldk + (int64_t)hk * p.D, p.ldk, kw, n, p.D, lane);
-  load_rows<DP>(v, p.v + row0 * p.ldv + (int64_t)hk * p.D, p.ldv, kw, n, p.D, lane);
   floatx16 dk[NB], dv[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) dk[b] = dv[b] = zero16();
 
-  // the queries from the first key on, 64 a step, head after head of the group
-  const int per_head = (n - k0 + 63) / 64, steps = per_head * p.group;
-  TileCopy<DP, 4> copy;
+  // the queries from the first key on, 32 a step, head after head of the group
+  const int per_head = (n - k0 + 31) / 32;
+  const uint32_t lds0 = lds_address(lds), steps0 = lds0 + 4 * TILE;
+  {
+    TileCopy<DP, 128, 4> copy;
+    copy.init(lane);
+    copy.issue(lds0, p.v + row0 * p.ldv + (int64_t)hk * p.D, p.ldv, k0, n, p.D, wave, lane);
+  }
+  TileCopy<DP, 32, 4> copy;
   copy.init(lane);
-  const uint32_t lds0 = lds_address(lds);
-  auto issue = [&](int i, int st) {
-    const int h = hk * p.group + i / per_head, i0 = k0 + 64 * (i % per_head);
-    copy.issue(lds0 + st * STAGE, p.q + row0 * p.ldq + (int64_t)h * p.D, p.ldq, i0, n, p.D, wave, lane);
-    copy.issue(lds0 + st * STAGE + TILE, p.dout + row0 * p.lddo + (int64_t)h * p.D, p.lddo, i0, n, p.D,
+  // queries past the sequence: q, do, lse and delta are 0, and so is what they add
+  auto issue = [&](int h, int i0, int st) {
+    copy.issue(steps0 + st * STAGE, p.q + row0 * p.ldq + (int64_t)h * p.D, p.ldq, i0, n, p.D, wave, lane);
+    copy.issue(steps0 + st * STAGE + TILE, p.dout + row0 * p.lddo + (int64_t)h * p.D, p.lddo, i0, n, p.D,
                wave, lane);
-    // queries past the sequence: q, do, lse and delta are 0, and so is what they add
-    if (wave < 2)
-      lds_load4(lds_address(&stat[st][wave][0]),
-                rsrc4((wave ? p.delta : p.lw) + h * p.T + row0 + i0, 4u * (uint32_t)min(n - i0, 64)),
+    if (wave < 2 && lane < 32)
+      lds_load4(lds_address(&stat[st][32 * wave]),
+                rsrc4((wave ? p.delta : p.lw) + h * p.T + row0 + i0, 4u * (uint32_t)min(n - i0, 32)),
                 4u * lane, 0u);
   };
-  issue(0, 0);
-  for (int i = 0; i < steps; ++i) {
-    const int st = i & 1;
-    const uint8_t* qt = lds + st * STAGE;
+  const int h_end = (hk + 1) * p.group;
+  int h = hk * p.group, step = 0;   // of the step in work
+  issue(h, k0, 0);
+  for (int st = 0; h < h_end; st ^= 1) {
+    const uint8_t* qt = lds + 4 * TILE + st * STAGE;
     const uint8_t* ot = qt + TILE;
+    const int i0 = k0 + 32 * step;
     wait_vmcnt<0>();
-    __syncthreads();   // step i is there, and step i - 1 has been read
-    if (i + 1 < steps) issue(i + 1, st ^ 1);
-    const int i0 = k0 + 64 * (i % per_head);
-    if (i0 + 63 < kw || kw >= n) continue;   // every query lies before the wave's keys
+    __syncthreads();   // the step is there, and the one before has been read
+    if (++step == per_head) {
+      step = 0;
+      ++h;
+    }
+    if (h < h_end) issue(h, k0 + 32 * step, st ^ 1);
+    if (i0 + 31 < kw || kw >= n) continue;   // every query lies before the wave's keys
+    floatx16 s = zero16(), dp = zero16();
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if (i0 + 32 * u + 31 < kw) continue;
-      floatx16 s = zero16(), dp = zero16();
+    for (int x = 0; x < S; ++x) {
+      s = mfma(frag_rows<DP>(qt, 0, x, lane), k[x], s);
+      dp = mfma(frag_rows<DP>(ot, 0, x, lane), frag_rows<DP>(lds, 32 * wave, x, lane), dp);
+    }
+    const bool edge = i0 < kw + 31;
 #pragma unroll
-      for (int x = 0; x < S; ++x) {
-        s = mfma(frag_rows<DP>(qt, 32 * u, x, lane), k[x], s);
-        dp = mfma(frag_rows<DP>(ot, 32 * u, x, lane), v[x], dp);
+    for (int g = 0; g < 4; ++g) {
+      const int at = 8 * g + 4 * (lane >> 5);
+      const f32x4 lw = *reinterpret_cast<const f32x4*>(&stat[st][at]);
+      const f32x4 de = *reinterpret_cast<const f32x4*>(&stat[st][32 + at]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int r = 4 * g + e;
+        float w = __builtin_amdgcn_exp2f(s[r] * c - lw[e]);
+        if (edge && (key > i0 + at + e)) w = 0.0f;
+        s[r] = w;
+        dp[r] = w == 0.0f ? 0.0f : w * (dp[r] - de[e]);
       }
-      const bool edge = i0 + 32 * u < kw + 31;
+    }
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int at = 32 * u + 8 * g + 4 * (lane >> 5);
-        const f32x4 lw = *reinterpret_cast<const f32x4*>(&stat[st][0][at]);
-        const f32x4 de = *reinterpret_cast<const f32x4*>(&stat[st][1][at]);
+    for (int x = 0; x < 2; ++x) {
+      const bf16x8 w = frag_of(s, x), ds = frag_of(dp, x);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = 4 * g + e;
-          float w = __builtin_amdgcn_exp2f(s[r] * c - lw[e]);
-          if (edge && key > i0 + at + e) w = 0.0f;
-          s[r] = w;
-          dp[r] = w == 0.0f ? 0.0f : w * (dp[r] - de[e]);
-        }
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const bf16x8 w = frag_of(s, x), ds = frag_of(dp, x);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          dv[b] = mfma(w, frag_turned<DP>(ot, 32 * u + 16 * x, 32 * b, lane), dv[b]);
-          dk[b] = mfma(ds, frag_turned<DP>(qt, 32 * u + 16 * x, 32 * b, lane), dk[b]);
-        }
+      for (int b = 0; b < NB; ++b) {
+        dv[b] = mfma(w, frag_turned<DP>(ot, 16 * x, 32 * b, lane), dv[b]);
+        dk[b] = mfma(ds, frag_turned<DP>(qt, 16 * x, 32 * b, lane), dk[b]);
       }
     }
   }
@@ -152,7 +161,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_dkv(AttnLaunch p) {
 
 // dq of 128 queries of one head, 32 to a wave.
 template <int DP>
-__global__ __launch_bounds__(256, 1) void k_attn_dq(AttnLaunch p) {
+__global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p) {
   constexpr int S = DP / 16, NB = DP / 32;
   constexpr int TILE = 64 * DP * 2;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * TILE];
@@ -166,7 +175,7 @@ __global__ __launch_bounds__(256, 1) void k_attn_dq(AttnLaunch p) {
   const uint16_t* kb = p.k + row0 * p.ldk + (int64_t)hk * p.D;
   const uint16_t* vb = p.v + row0 * p.ldv + (int64_t)hk * p.D;
   const int tiles = (min(n, q0 + kAttnTile) + 63) / 64;
-  TileCopy<DP, 4> copy;
+  TileCopy<DP, 64, 4> copy;
   copy.init(lane);
   const uint32_t lds0 = lds_address(lds);
   copy.issue(lds0, kb, p.ldk, 0, n, p.D, wave, lane);
@@ -238,6 +247,8 @@ __global__ __launch_bounds__(256, 1) void k_attn_dq(AttnLaunch p) {
 template <int DP>
 void launch(const AttnLaunch& p, hipStream_t s) {
   const unsigned tiles = (unsigned)(p.T / kAttnTile + p.B);
+  const int64_t rows = (p.T + 127) / 128;
+  k_attn_delta<DP><<<dim3((unsigned)(rows < (1 << 20) ? rows : 1 << 20), (unsigned)p.heads), 256, 0, s>>>(p);
   k_attn_dkv<DP><<<dim3(tiles, (unsigned)p.kv_heads), 256, 0, s>>>(p);
   k_attn_dq<DP><<<dim3(tiles, (unsigned)p.heads), 256, 0, s>>>(p);
 }
@@ -247,8 +258,6 @@ void launch(const AttnLaunch& p, hipStream_t s) {
 int64_t attn_workspace(int64_t T, int32_t heads) { return 2 * (int64_t)heads * T * 4; }
 
 hipError_t launch_attn_bwd(const AttnLaunch& p, hipStream_t s) {
-  const int64_t blocks = (p.T + 15) / 16;
-  k_attn_delta<<<dim3((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20), (unsigned)p.heads), 256, 0, s>>>(p);
   if (p.D <= 64) launch<64>(p, s);
   else launch<128>(p, s);
   return hipGetLastError();

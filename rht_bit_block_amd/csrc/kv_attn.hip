@@ -27,8 +27,8 @@
 // two bf16 pieces, 16 bits of mantissa.
 //
 // The work is cut evenly, not by sequence: with u = 64-token steps of every (sequence,
-// tile of queries, key head) laid end to end, workgroup w takes steps w / W .. (w
-// + 1) / W of all.  Whole items are finished where they are computed; parts of one
+// tile of queries, key head) laid end to end, and a few for each as such, workgroup w
+// takes steps w / W .. (w + 1) / W of all.  Whole items are finished where they are computed; parts of one
 // leave (o', m, l) in the workspace and a second launch joins them in order.
 #include "attn_internal.h"
 
@@ -143,11 +143,18 @@ __device__ __forceinline__ float signed_by(const uint32_t (&sign)[4], int e, flo
   return __uint_as_float(__float_as_uint(x) ^ ((w >> (e & 31)) << 31));
 }
 
+// What an item (a tile of queries of one key head) costs besides its steps, in steps:
+// rotating its queries, filling and joining its waves.  Without it a workgroup that
+// drew the short sequences of a batch took 88 of them one after another, 590 us where
+// the others were done after 100.
+constexpr int kItem = 4;
+
 // Sequence b's share of the work.
 struct Seq {
   int row0, rows;     // packed rows
   int len;            // tokens in the cache
   int64_t tiles, units;
+  __device__ int64_t cost(int heads) const { return tiles * heads * (units + kItem); }
 };
 __device__ __forceinline__ Seq sequence(const KvAttn& p, int b) {
   Seq q;
@@ -211,7 +218,7 @@ __device__ __forceinline__ int64_t plan(const KvAttn& p, int groups, int w, Plan
     own = 0;
     if (b < B) {
       const Seq q = sequence(p, b);
-      own = q.tiles * p.at.kv_heads * q.units;
+      own = q.cost(p.at.kv_heads);
     }
     int64_t part;
     upto = scan(own, s.scan, part);
@@ -227,7 +234,7 @@ __device__ __forceinline__ int64_t plan(const KvAttn& p, int groups, int w, Plan
       own = 0;
       if (b < B) {
         const Seq q = sequence(p, b);
-        own = q.tiles * p.at.kv_heads * q.units;
+        own = q.cost(p.at.kv_heads);
       }
       int64_t part;
       upto = scan(own, s.scan, part);
@@ -298,15 +305,19 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
 
   while (f.b < p.at.B && u < u_end) {
     const Seq q = sequence(p, f.b);
-    const int64_t cost = q.tiles * p.at.kv_heads * q.units;
+    const int64_t cost = q.cost(p.at.kv_heads);
     if (u >= f.before + cost) {   // this sequence is done
       f.before += cost;
       ++f.b;
       continue;
     }
-    const int64_t item = (u - f.before) / q.units;
-    const int64_t first = (u - f.before) - item * q.units;
-    const int64_t count = min(q.units - first, u_end - u);
+    const int64_t item = (u - f.before) / (q.units + kItem);
+    const int64_t from = (u - f.before) - item * (q.units + kItem);
+    const int64_t to = min(q.units + kItem, from + (u_end - u));
+    const bool leading = u == u_first;   // the workgroup's first item
+    u += to - from;
+    if (to <= kItem) continue;           // none of its steps
+    const int64_t first = max(from - kItem, (int64_t)0), count = to - kItem - first;
     const int hk = (int)(item % p.at.kv_heads);
     const int64_t r0 = item / p.at.kv_heads * (16 * MT);   // first (token, head of the group) row
     const int64_t nrows = (int64_t)q.rows * p.group;
@@ -385,10 +396,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
       return (((int64_t)page * p.at.kv_heads + hk) << p.at.page_shift) +
              (t & (((int64_t)1 << p.at.page_shift) - 1));
     };
-    // Codes and scales of the step whose rows are `row` into buffer `buf`; bytes: 1 x 32
-    // E8M0 scales that are not a whole word are left in `tail`.
+    // Codes and scales of the step whose rows are `row` into buffer `buf`.  E8M0 scales
+    // that are not a whole word a token come back as its word.
     auto issue = [&](int buf, int64_t row, uint64_t valid, const uint8_t* codes,
-                     const uint8_t* scales, uint32_t& tail) {
+                     const uint8_t* scales) -> uint32_t {
+      uint32_t tail = 0;
       const uint32_t to = mine0 + buf * L::UNIT;
       // a token without a place: any row that has one, and a mask
       const int some = __builtin_ctzll(valid);
@@ -421,8 +433,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
         if (D == 128) {
           copy4(ts, scales + at * 4);
         } else {
-          tail = 0;
-          for (int i = 0; i < D / 32; ++i) tail |= (uint32_t)scales[at * (D / 32) + i] << (8 * i);
+#pragma unroll
+          for (int i = 0; i < NB; ++i)
+            if (32 * i < D) tail |= (uint32_t)scales[at * (D / 32) + i] << (8 * i);
         }
       } else {
         const int ns = KIND == 1 ? D / 16 : D / 32;
@@ -430,6 +443,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
         for (int i = 0; i < L::NS; ++i)
           if (i < ns) copy4(ts + 256u * i, scales + (at * ns + i) * 4);
       }
+      return tail;
     };
 
     uint32_t tail_k = 0, tail_v = 0;
@@ -437,8 +451,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
     int64_t row = place(wave), next_row = place(wave + kWaves);
     uint64_t valid = __ballot(row >= 0);
     if (valid) {
-      issue(kb, row, valid, p.k_codes, p.k_scales, tail_k);
-      issue(vb, row, valid, p.v_codes, p.v_scales, tail_v);
+      tail_k = issue(kb, row, valid, p.k_codes, p.k_scales);
+      tail_v = issue(vb, row, valid, p.v_codes, p.v_scales);
     }
     for (int64_t step = wave; step < count; step += kWaves) {
       const int64_t after_row = place(step + 2 * kWaves);
@@ -456,7 +470,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
 #pragma unroll
         for (int i = 0; i < NB; ++i) vs[64 * i + lane] = __uint_as_float(((w >> (8 * i)) & 0xFFu) << 23);
       }
-      if (next_valid) issue(nb, next_row, next_valid, p.k_codes, p.k_scales, tail_k);
+      if (next_valid) tail_k = issue(nb, next_row, next_valid, p.k_codes, p.k_scales);
       f32x4 s[MT][4];
       if (valid) {
         const uint8_t* kt = mine + kb * L::UNIT;
@@ -521,7 +535,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
       }
       // the keys have been read: the next step's values take their place
       wait_lds();
-      if (next_valid) issue(kb, next_row, next_valid, p.v_codes, p.v_scales, tail_v);
+      if (next_valid) tail_v = issue(kb, next_row, next_valid, p.v_codes, p.v_scales);
       if (valid) {
         const int64_t t0 = (first + step) * kStep;
         const bool masked = valid != ~(uint64_t)0 || t0 + kStep - 1 > sure;
@@ -651,7 +665,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
       __syncthreads();
     }
     const bool whole = first == 0 && count == q.units;
-    float* part = p.partial + (int64_t)(2 * blockIdx.x + (u == u_first ? 0 : 1)) * (16 * MT) * (D + 2);
+    float* part = p.partial + (int64_t)(2 * blockIdx.x + (leading ? 0 : 1)) * (16 * MT) * (D + 2);
     for (int r = wave; r < 16 * MT; r += kWaves) {
       const int64_t at = r0 + r;
       if (at >= nrows) break;
@@ -678,7 +692,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
         if (lane == 0) *reinterpret_cast<f32x2*>(to + D) = f32x2{top, sum};
       }
     }
-    u += count;
   }
 }
 
@@ -692,14 +705,15 @@ __global__ __launch_bounds__(kThreads) void k_kv_join(KvAttn p) {
   const int64_t quota = plan(p, kKvGroups, w, plan_lds, f);
   if (f.b >= p.at.B) return;
   const Seq q = sequence(p, f.b);
-  const int64_t u = (int64_t)w * quota, item = (u - f.before) / q.units;
-  const int64_t a0 = f.before + item * q.units;            // the item's units
-  if (a0 == u || a0 < u - quota) return;                   // not split here, or before
+  const int64_t u = (int64_t)w * quota, item = (u - f.before) / (q.units + kItem);
+  const int64_t a0 = f.before + item * (q.units + kItem);  // the item's place, and its steps'
+  const int64_t s0 = a0 + kItem;
+  if (s0 >= u || s0 < u - quota) return;                   // not split here, or before
   const int hk = (int)(item % p.at.kv_heads);
   const int r = 4 * blockIdx.y + wave;
   const int64_t at = item / p.at.kv_heads * (16 * p.rows16) + r, nrows = (int64_t)q.rows * p.group;
   if (at >= nrows) return;
-  const int w0 = w - 1, w1 = (int)((a0 + q.units - 1) / quota);
+  const int w0 = w - 1, w1 = (int)((s0 + q.units - 1) / quota);
   const int64_t size = (int64_t)16 * p.rows16 * (D + 2);
   auto part = [&](int x) {   // an item that begins inside a workgroup's units is its second part
     return p.partial + (2 * x + (x == w0 && a0 > (int64_t)w0 * quota ? 1 : 0)) * size + (int64_t)r * (D + 2);
