@@ -23,16 +23,17 @@ namespace {
 using namespace attn;
 
 template <int DP>
-__global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p) {
+__global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p, int last_tile) {
   constexpr int S = DP / 16, NB = DP / 32;
   constexpr int TILE = 64 * DP * 2;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * TILE];
   int64_t row0;
   int n, t;
   // the last tile of a sequence has the most keys: it goes first
-  if (!find_tile(p.starts, p.B, p.T, (int)(gridDim.x - 1 - blockIdx.x), row0, n, t)) return;
+  const Share me = share_of(blockIdx.x, p.kv_heads, p.group);
+  if (!find_tile(p.starts, p.B, p.T, last_tile - me.tile, row0, n, t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int h = blockIdx.y, hk = h / p.group;
+  const int h = me.head, hk = h / p.group;
   const int q0 = t * kAttnTile, qw = q0 + 32 * wave;   // the workgroup's and the wave's first query
   const int qi = qw + (lane & 31);
   const uint16_t* kb = p.k + row0 * p.ldk + (int64_t)hk * p.D;
@@ -141,9 +142,12 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p) {
 }  // namespace
 
 hipError_t launch_attn_fwd(const AttnLaunch& p, hipStream_t s) {
-  const dim3 grid((unsigned)(p.T / kAttnTile + p.B), (unsigned)p.heads);
-  if (p.D <= 64) k_attn_fwd<64><<<grid, 256, 0, s>>>(p);
-  else k_attn_fwd<128><<<grid, 256, 0, s>>>(p);
+  const int64_t tiles = p.T / kAttnTile + p.B;
+  over_tiles(tiles, p.heads, [&](int t0, unsigned blocks) {
+    const int last = (int)(tiles - 1) - t0;
+    if (p.D <= 64) k_attn_fwd<64><<<blocks, 256, 0, s>>>(p, last);
+    else k_attn_fwd<128><<<blocks, 256, 0, s>>>(p, last);
+  });
   return hipGetLastError();
 }
 

@@ -92,6 +92,31 @@ __device__ __forceinline__ bool find_tile(const int32_t* starts, int B, int64_t 
   return false;
 }
 
+// Which tile and head a workgroup takes.  All heads of a tile follow one another: the
+// sequences' tiles run from the one with the most work to the one with the least,
+// and workgroups that start late have little of it (one head after another, a head's
+// longest tiles started last: 32768 tokens 2.76 ms instead of HEADS_FIRST).  Key heads
+// alternate first, then the heads of a group: workgroups go to the XCDs in turn, so
+// with eight key heads each XCD keeps one of them in its cache.
+struct Share {
+  int tile, head;
+};
+__device__ __forceinline__ Share share_of(uint32_t id, int kv_heads, int group) {
+  const uint32_t heads = (uint32_t)(kv_heads * group);
+  const uint32_t tile = id / heads, r = id - tile * heads;
+  const uint32_t in_group = r / (uint32_t)kv_heads;
+  return Share{(int)tile, (int)((r - in_group * kv_heads) * group + in_group)};
+}
+
+// Launches over `tiles` tiles of `heads` heads, fewer than 2^24 workgroups at a time; f(first
+// tile, workgroups).
+template <class F>
+void over_tiles(int64_t tiles, int heads, F&& f) {
+  const int64_t slice = ((int64_t)1 << 23) / heads;
+  for (int64_t t0 = 0; t0 < tiles; t0 += slice)
+    f((int)t0, (unsigned)((tiles - t0 < slice ? tiles - t0 : slice) * heads));
+}
+
 // A tile in LDS has rows of DP elements whose 16-byte chunks are exchanged by the
 // row's number so that both kinds of reads fill all 64 banks: sixteen rows
 // reading one chunk each (sixteen different places of a 256-byte line), and the turned reads'

@@ -54,7 +54,7 @@ __global__ __launch_bounds__(256) void k_attn_delta(AttnLaunch p) {
 // dk and dv of 128 keys of one key head, 32 to a wave: two waves to a SIMD, whose
 // registers hold the sums and K; V's rows stay in LDS.
 template <int DP>
-__global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p) {
+__global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first_tile) {
   constexpr int S = DP / 16, NB = DP / 32;
   constexpr int TILE = 32 * DP * 2;
   constexpr int STAGE = 2 * TILE;
@@ -62,9 +62,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p) {
   __shared__ __attribute__((aligned(16))) float stat[2][64];   // stage; lse log2(e) and delta of 32 queries
   int64_t row0;
   int n, t;
-  if (!find_tile(p.starts, p.B, p.T, (int)blockIdx.x, row0, n, t)) return;
+  const Share me = share_of(blockIdx.x, p.kv_heads, 1);
+  if (!find_tile(p.starts, p.B, p.T, first_tile + me.tile, row0, n, t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int hk = blockIdx.y;
+  const int hk = me.head;
   const int k0 = t * kAttnTile, kw = k0 + 32 * wave;
   const int key = kw + (lane & 31);
   const float c = p.scale * kLog2e;
@@ -161,15 +162,16 @@ __global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p) {
 
 // dq of 128 queries of one head, 32 to a wave.
 template <int DP>
-__global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p) {
+__global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int last_tile) {
   constexpr int S = DP / 16, NB = DP / 32;
   constexpr int TILE = 64 * DP * 2;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * TILE];
   int64_t row0;
   int n, t;
-  if (!find_tile(p.starts, p.B, p.T, (int)(gridDim.x - 1 - blockIdx.x), row0, n, t)) return;
+  const Share me = share_of(blockIdx.x, p.kv_heads, p.group);
+  if (!find_tile(p.starts, p.B, p.T, last_tile - me.tile, row0, n, t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int h = blockIdx.y, hk = h / p.group;
+  const int h = me.head, hk = h / p.group;
   const int q0 = t * kAttnTile, qw = q0 + 32 * wave;
   const int qi = qw + (lane & 31);
   const uint16_t* kb = p.k + row0 * p.ldk + (int64_t)hk * p.D;
@@ -246,11 +248,14 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p) {
 
 template <int DP>
 void launch(const AttnLaunch& p, hipStream_t s) {
-  const unsigned tiles = (unsigned)(p.T / kAttnTile + p.B);
-  const int64_t rows = (p.T + 127) / 128;
+  const int64_t tiles = p.T / kAttnTile + p.B, rows = (p.T + 127) / 128;
   k_attn_delta<DP><<<dim3((unsigned)(rows < (1 << 20) ? rows : 1 << 20), (unsigned)p.heads), 256, 0, s>>>(p);
-  k_attn_dkv<DP><<<dim3(tiles, (unsigned)p.kv_heads), 256, 0, s>>>(p);
-  k_attn_dq<DP><<<dim3(tiles, (unsigned)p.heads), 256, 0, s>>>(p);
+  over_tiles(tiles, p.kv_heads, [&](int t0, unsigned blocks) {
+    k_attn_dkv<DP><<<blocks, 256, 0, s>>>(p, t0);
+  });
+  over_tiles(tiles, p.heads, [&](int t0, unsigned blocks) {
+    k_attn_dq<DP><<<blocks, 256, 0, s>>>(p, (int)(tiles - 1) - t0);
+  });
 }
 
 }  // namespace
