@@ -72,6 +72,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p, int last_tile
     for (int x = 0; x < S; ++x)
 #pragma unroll
       for (int u = 0; u < 2; ++u) s[u] = mfma(frag_rows<DP>(kt, 32 * u, x, lane), q[x], s[u]);
+    reads_ahead<2 * S, 2 * S, 4>();
     // c is the sign of the factor too: the maximum is of c s
     if (j0 + 63 > qw) {
 #pragma unroll
@@ -118,6 +119,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p, int last_tile
           o[b] = mfma(frag_turned<DP>(vt, 32 * u + 16 * x, 32 * b, lane), w, o[b]);
       }
     }
+    reads_ahead<4 * NB, 8 * NB, 4>();
   }
   wait_vmcnt<0>();
   if (qi >= n) return;

@@ -209,6 +209,21 @@ __device__ __forceinline__ floatx16 mfma(const bf16x8& a, const bf16x8& b, const
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
+// Orders what the compiler schedules of the code before it, back to the last such call or
+// branch: AHEAD LDS reads, then each MFMA with PER more, so that a fragment is on its way
+// while the ones before it are multiplied (left alone, each read is waited for right
+// before its MFMA).
+template <int MFMAS, int READS, int AHEAD>
+__device__ __forceinline__ void reads_ahead() {
+  constexpr int PER = (READS + MFMAS - 1) / MFMAS;
+  __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+  for (int i = 0; i < MFMAS; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    if (AHEAD + i * PER < READS) __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);
+  }
+}
+
 __device__ __forceinline__ floatx16 zero16() {
   floatx16 z;
 #pragma unroll

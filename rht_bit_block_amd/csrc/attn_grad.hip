@@ -117,6 +117,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first_til
       s = mfma(frag_rows<DP>(qt, 0, x, lane), k[x], s);
       dp = mfma(frag_rows<DP>(ot, 0, x, lane), frag_rows<DP>(lds, 32 * wave, x, lane), dp);
     }
+    reads_ahead<2 * S, 3 * S, 3>();
     const bool edge = i0 < kw + 31;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
@@ -141,6 +142,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first_til
         dk[b] = mfma(ds, frag_turned<DP>(qt, 16 * x, 32 * b, lane), dk[b]);
       }
     }
+    reads_ahead<4 * NB, 8 * NB, 4>();
   }
   wait_vmcnt<0>();
   // a lane holds element 32 b + l % 32 of keys kw + 8 (r / 4) + 4 (l / 32) + r % 4
@@ -213,6 +215,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int last_tile)
         s = mfma(frag_rows<DP>(kt, 32 * u, x, lane), q[x], s);
         dp = mfma(frag_rows<DP>(vt, 32 * u, x, lane), g[x], dp);
       }
+      reads_ahead<2 * S, 2 * S, 4>();
       const bool edge = j0 + 32 * u + 31 > qw;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
@@ -228,6 +231,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int last_tile)
         for (int b = 0; b < NB; ++b)
           dq[b] = mfma(frag_turned<DP>(kt, 32 * u + 16 * x, 32 * b, lane), ds, dq[b]);
       }
+      reads_ahead<2 * NB, 4 * NB, 4>();
     }
   }
   wait_vmcnt<0>();
