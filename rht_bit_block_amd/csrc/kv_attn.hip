@@ -57,6 +57,10 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)p;
 }
 
+// a b, and 0 where either is 0, whatever the other (v_mul_legacy_f32).
+extern "C" __device__ float ufp4_llvm_fmul_legacy(float, float) __asm("llvm.amdgcn.fmul.legacy");
+__device__ __forceinline__ float mul_legacy(float a, float b) { return ufp4_llvm_fmul_legacy(a, b); }
+
 // HBM -> LDS without registers, lane i's bytes at lds + 16 i (4 i); waited for with
 // wait_copies.  Lanes that are switched off leave their place as it is.
 __device__ __forceinline__ void copy16(uint32_t lds, const void* src) {
@@ -66,6 +70,15 @@ __device__ __forceinline__ void copy16(uint32_t lds, const void* src) {
 __device__ __forceinline__ void copy4(uint32_t lds, const void* src) {
   asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, off"
                : : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(src) : "memory");
+}
+// The same from a wave-uniform address and a lane's offset.
+__device__ __forceinline__ void copy16(uint32_t lds, uint64_t base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2"
+               : : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t lds, uint64_t base, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dword %1, %2"
+               : : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base) : "memory");
 }
 __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" : : : "memory"); }
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
@@ -84,8 +97,13 @@ __device__ __forceinline__ float query_sum(float x) {
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
-// Eight codes as bf16 levels times 2^e of `scale`, in the order of kOrder.
-template <int GRID>
+// Eight codes as bf16 values, in the order of `order`: levels times 2^e of `scale`, or with
+// OFF (INT4) 136 + n, where `scale` is not used: n ^ 8 in the low mantissa bits of 128
+// is two instructions for two codes where tables and a conversion take four, and the
+// products' excess, 136 times the sum of the other operand, is taken off in the
+// accumulator.  SPLIT: the codes of two 1 x 16 blocks, nibbles 0 .. 3 of the first in
+// registers 0, 1, nibbles 4 .. 7 of the second in 2, 3.
+template <int GRID, bool OFF, bool SPLIT>
 __device__ __forceinline__ u32x4 decode8(uint32_t x, float scale) {
   u32x4 v;
   if constexpr (GRID == 2) {
@@ -93,6 +111,19 @@ __device__ __forceinline__ u32x4 decode8(uint32_t x, float scale) {
     v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 1));
     v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 2));
     v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 3));
+  } else if constexpr (OFF) {
+    const uint32_t y = x ^ 0x88888888u;
+    if constexpr (SPLIT) {
+      const uint32_t a = __builtin_amdgcn_perm(0u, y, 0x04010400u);   // bytes 0 and 1 apart
+      const uint32_t b = __builtin_amdgcn_perm(0u, y, 0x04030402u);
+      v[0] = (a & 0x000F000Fu) | 0x43004300u;
+      v[1] = ((a >> 4) & 0x000F000Fu) | 0x43004300u;
+      v[2] = (b & 0x000F000Fu) | 0x43004300u;
+      v[3] = ((b >> 4) & 0x000F000Fu) | 0x43004300u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = ((y >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+    }
   } else {
     // E4M3 bytes of the even and of the odd nibbles
     const uint32_t y = x >> 4;
@@ -110,16 +141,19 @@ __device__ __forceinline__ u32x4 decode8(uint32_t x, float scale) {
       b = __builtin_amdgcn_perm(nb, pb, ((y >> 1) & 0x04040404u) | 0x03020100u);
     }
     v[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, false));
-    v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, true));
-    v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, false));
+    v[SPLIT ? 2 : 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, scale, true));
+    v[SPLIT ? 1 : 2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, false));
     v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, true));
   }
   return v;
 }
 // Which nibble is the i-th value.
-template <int GRID>
+template <int GRID, bool OFF, bool SPLIT>
 __device__ constexpr int order(int i) {
-  return GRID == 2 ? i : i < 4 ? 2 * i : 2 * i - 7;
+  if (GRID == 2) return i;
+  if (SPLIT) return (i & 4) | ((i & 1) << 1) | ((i >> 1) & 1);
+  if (OFF) return (i >> 1) + 4 * (i & 1);
+  return i < 4 ? 2 * i : 2 * i - 7;
 }
 
 // Butterflies over a row of D elements, two neighbours to a lane.
@@ -268,40 +302,72 @@ __device__ __forceinline__ void store_row(const KvAttn& p, float a, float b, flo
 
 // LDS of one wave: three buffers that K and V take in turn, each the codes of 64
 // tokens (rows of ROW bytes, 16-byte chunks exchanged by the token) and their
-// scales, [block][token] (KIND 2: four bytes a token); KIND 2 also the current
-// values' scales in fp32.
+// scales as memory has them, SC bytes a token; KIND 2 also the current values' scales in fp32.
 template <int KIND, int NB>
 struct Lay {
   static constexpr int ROW = 16 * NB, CODES = kStep * ROW;
-  static constexpr int NS = KIND == 2 ? 1 : KIND == 1 ? 2 * NB : NB;
-  static constexpr int UNIT = CODES + NS * 256;
-  static constexpr int WAVE = 3 * UNIT + (KIND == 2 ? NB * 256 : 0);
+  static constexpr int SC = KIND == 2 ? NB : KIND == 1 ? 8 * NB : 4 * NB;
+  static constexpr int NS = SC / 4;   // words of a token (KIND 2, NB = 2: half a word)
+  static constexpr int UNIT = CODES + kStep * SC;
+  static constexpr int WIDE = KIND == 2 ? kStep * 4 * NB : 0;   // a step's value scales in fp32
+  static constexpr int PAIR = 2 * UNIT + WIDE;                  // a wave's part but the third buffer
   __device__ static uint32_t flip(int tok) {
     return NB == 4 ? ((tok >> 2) ^ (tok >> 4)) & 3 : ((tok >> 3) ^ (tok >> 4)) & 1;
   }
 };
 
-// NB: 32-element blocks of a row in LDS (2 or 4), MT: tiles of 16 queries.
-template <int GRID, int KIND, int NB, int MT>
-__global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
+// (Elements past D: any codes, which stand for something finite, against q' = 0, and scales of 0.)
+
+// N floats of an LDS row that starts at a multiple of 8 bytes.
+template <int N>
+__device__ __forceinline__ void read_scales(float (&x)[N], const float* at) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const f32x4 v = *reinterpret_cast<const f32x4*>(at + i);
+      x[i] = v[0]; x[i + 1] = v[1]; x[i + 2] = v[2]; x[i + 3] = v[3];
+    }
+  } else {
+    const f32x2 v = *reinterpret_cast<const f32x2*>(at);
+    x[0] = v[0]; x[1] = v[1];
+  }
+}
+
+// NB: 32-element blocks of a row in LDS (2 or 4), MT: tiles of 16 queries.  FAST: D = 32 NB
+// and pages of 64 tokens or more, so that a step's codes and scales are one run of memory
+// each and its page one scalar: its copies need no address arithmetic (otherwise a
+// step's addresses cost as many instructions as half of its arithmetic).
+template <int GRID, int KIND, int NB, int MT, bool FAST>
+__global__ __launch_bounds__(kThreads, MT == 2 && NB == 4 ? 1 : 2) void k_kv_attn(KvAttn p) {
   using L = Lay<KIND, NB>;
   constexpr int DP = 32 * NB, QP = DP + 4;
-  constexpr int kArea = kWaves * L::WAVE > 16 * MT * QP * 4 ? kWaves * L::WAVE : 16 * MT * QP * 4;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kArea];
+  constexpr bool SPLIT = KIND == 1;
+  // with two tiles of queries the excess costs more than the tables, and sums of values
+  // would carry the rounding of 136 weights where a value is 0
+  constexpr bool OFF = GRID == 1 && MT == 1 && KIND != 2;
+  constexpr int NBLK = SPLIT ? 2 * NB : NB;   // blocks of a row
+  constexpr int kRows = kWaves * L::PAIR;   // where the waves' third buffers lie, and `rows`
+  constexpr int kThird = kWaves * L::UNIT > 16 * MT * QP * 4 ? kWaves * L::UNIT : 16 * MT * QP * 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kRows + kThird];
   __shared__ PlanLds plan_lds;
   __shared__ float stat[2][kWaves][16 * MT];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, li = lane & 15;
-  const int D = p.at.D;
+  const int D = FAST ? DP : p.at.D;
   Found f;
   const int64_t quota = plan(p, gridDim.x, blockIdx.x, plan_lds, f);
   int64_t u = (int64_t)blockIdx.x * quota;
   const int64_t u_end = u + quota;
   const int64_t u_first = u;
   const float c = p.scale * kLog2e;
-  float* rows = reinterpret_cast<float*>(lds);   // [16 MT][QP], before and after the steps
-  uint8_t* mine = lds + wave * L::WAVE;
-  const uint32_t mine0 = lds_address(mine);
+  float* rows = reinterpret_cast<float*>(lds + kRows);   // [16 MT][QP], before and after the steps
+  uint8_t* const wide = lds + wave * L::PAIR + 2 * L::UNIT;
+  auto buffer = [&](int b) -> uint8_t* {
+    return b < 2 ? lds + wave * L::PAIR + b * L::UNIT : lds + kRows + wave * L::UNIT;
+  };
+  // a lane's 16 bytes within the 1024 of a copy; NB = 4: and 16 bytes times the copy's number
+  const uint32_t run = NB == 4 ? 64u * (lane >> 2) + 16u * ((lane & 3) ^ ((lane >> 4) & 3))
+                               : 32u * (lane >> 1) + 16u * ((lane & 1) ^ (((lane >> 4) ^ (lane >> 5)) & 1));
 
   while (f.b < p.at.B && u < u_end) {
     const Seq q = sequence(p, f.b);
@@ -317,48 +383,166 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
     const bool leading = u == u_first;   // the workgroup's first item
     u += to - from;
     if (to <= kItem) continue;           // none of its steps
-    const int64_t first = max(from - kItem, (int64_t)0), count = to - kItem - first;
+    const int64_t first = max(from - kItem, (int64_t)0);
+    const int count = (int)(to - kItem - first);
     const int hk = (int)(item % p.at.kv_heads);
     const int64_t r0 = item / p.at.kv_heads * (16 * MT);   // first (token, head of the group) row
     const int64_t nrows = (int64_t)q.rows * p.group;
 
-    // q' of the tile's rows in fp32
-    __syncthreads();   // `rows` is free
-    for (int r = wave; r < 16 * MT; r += kWaves) {
-      const int64_t at = r0 + r;
-      float a = 0.0f, b = 0.0f;
-      if (at < nrows) {   // uniform
-        const int64_t i = at / p.group;
-        const int h = hk * p.group + (int)(at - i * p.group);
-        if (2 * lane < D) {
-          const uint32_t x = *reinterpret_cast<const uint32_t*>(
-              p.q + (q.row0 + i) * p.ldq + (int64_t)h * D + 2 * lane);
-          a = signed_by(p.sign, 2 * lane, __uint_as_float(x << 16));
-          b = signed_by(p.sign, 2 * lane + 1, __uint_as_float(x & 0xFFFF0000u));
+    __syncthreads();   // the item before is done with the buffers
+    const int t_first = (int)first * kStep;
+    const int32_t* pages = p.at.table + f.b * p.at.ldt;
+
+    // Where the tokens of a step lie.  FAST: the page of all of them; else the row of token
+    // 64 step + lane among all rows, or -1.
+    auto place = [&](int step) -> int64_t {
+      if constexpr (FAST) {
+        const int t = t_first + step * kStep;
+        const int slot = t >> p.at.page_shift;
+        if (step >= count || t >= q.len || slot >= (int)p.at.width) return -1;
+        // the table does not change while the kernel runs: a scalar load
+        const int page = reinterpret_cast<const __attribute__((address_space(4))) int32_t*>(
+            (uint64_t)pages)[slot];
+        return page >= 0 && page < p.at.pages ? page : -1;
+      } else {
+        const int t = t_first + step * kStep + lane;
+        const int slot = t >> p.at.page_shift;
+        if (step >= count || t >= q.len || slot >= (int)p.at.width) return -1;
+        const int page = pages[slot];
+        if (page < 0 || page >= p.at.pages) return -1;
+        return (((int64_t)page * p.at.kv_heads + hk) << p.at.page_shift) +
+               (t & ((1 << p.at.page_shift) - 1));
+      }
+    };
+    // Which of a step's tokens have a place.
+    auto places = [&](int64_t at) -> uint64_t {
+      return FAST ? (at >= 0 ? ~(uint64_t)0 : 0) : __ballot(at >= 0);
+    };
+    // Codes and scales of a step into buffer `buf`.  Not FAST: the scales of token lane come
+    // back in registers, and are stored when the step begins.
+    float held[2][L::NS > 0 ? L::NS : 1];   // of keys and values (KIND 2: a word)
+    auto issue = [&](int buf, int step, int64_t at, uint64_t valid, int is_v) {
+      const uint8_t* codes = is_v ? p.v_codes : p.k_codes;
+      const uint8_t* scales = is_v ? p.v_scales : p.k_scales;
+      const uint32_t dst = lds_address(buffer(buf)), ds = dst + L::CODES;
+      if constexpr (FAST) {
+        const uint64_t row = (((uint64_t)at * p.at.kv_heads + hk) << p.at.page_shift) +
+                             (uint64_t)((t_first + step * kStep) & ((1 << p.at.page_shift) - 1));
+        const uint64_t cb = (uint64_t)codes + row * L::ROW, sb = (uint64_t)scales + row * L::SC;
+#pragma unroll
+        for (int i = 0; i < L::CODES / 1024; ++i)
+          copy16(dst + 1024u * i, cb + 1024u * i, NB == 4 ? run ^ (16u * i) : run);
+        constexpr int SB = kStep * L::SC;   // 128 .. 2048 bytes
+        if constexpr (SB >= 1024) {
+#pragma unroll
+          for (int i = 0; i < SB / 1024; ++i) copy16(ds + 1024u * i, sb + 1024u * i, 16u * lane);
+        } else if constexpr (SB >= 256) {
+          if (16 * lane < SB) copy16(ds, sb, 16u * lane);
+        } else {
+          if (4 * lane < SB) copy4(ds, sb, 4u * lane);
         }
-        rotate_row(a, b, p.n, lane);
-        if (p.n > 1) {
-          a *= p.cn;
-          b *= p.cn;
+      } else {
+        // a token without a place: any row that has one, and a mask
+        const int some = __builtin_ctzll(valid);
+        const uint32_t lo = at >= 0 ? (uint32_t)at : (uint32_t)__shfl((int)at, some);
+        const uint32_t hi = at >= 0 ? (uint32_t)(at >> 32) : (uint32_t)__shfl((int)(at >> 32), some);
+        const int64_t row = ((int64_t)hi << 32) | lo;
+        const int row_bytes = D / 2;
+        if ((D & 31) == 0) {
+          constexpr int PER = 64 / NB;   // tokens of an instruction
+#pragma unroll
+          for (int i = 0; i < kStep / PER; ++i) {
+            const int tok = PER * i + lane / NB;
+            const int64_t r = ((int64_t)(uint32_t)__shfl((int)hi, tok) << 32) | (uint32_t)__shfl((int)lo, tok);
+            const int ch = (lane % NB) ^ (int)L::flip(tok);
+            if (32 * ch < D) copy16(dst + 1024u * i, codes + r * row_bytes + 16 * ch);
+          }
+        } else {   // rows that end inside a chunk, by words
+          constexpr int PER = 16 / NB;
+          for (int i = 0; i < kStep / PER; ++i) {
+            const int tok = PER * i + lane / (4 * NB);
+            const int64_t r = ((int64_t)(uint32_t)__shfl((int)hi, tok) << 32) | (uint32_t)__shfl((int)lo, tok);
+            const int word = lane % (4 * NB);
+            const int ch = (word >> 2) ^ (int)L::flip(tok);
+            if (32 * ch + 8 * (word & 3) < D)
+              copy4(dst + 256u * i, codes + r * row_bytes + 16 * ch + 4 * (word & 3));
+          }
+        }
+        if constexpr (KIND == 2) {
+          uint32_t w = 0;
+#pragma unroll
+          for (int i = 0; i < NB; ++i)
+            if (32 * i < D) w |= (uint32_t)scales[row * (D / 32) + i] << (8 * i);
+          held[is_v][0] = __uint_as_float(w);
+        } else {
+          const int ns = SPLIT ? D / 16 : D / 32;
+#pragma unroll
+          for (int i = 0; i < L::NS; ++i)
+            held[is_v][i] = i < ns ? reinterpret_cast<const float*>(scales)[row * ns + i] : 0.0f;
         }
       }
-      if (2 * lane < DP) *reinterpret_cast<f32x2*>(rows + r * QP + 2 * lane) = f32x2{a, b};
+    };
+    auto settle = [&](int buf, int is_v) {   // the held scales of a step into its buffer
+      if constexpr (!FAST) {
+        uint8_t* to = buffer(buf) + L::CODES + lane * L::SC;
+        if constexpr (KIND == 2) {
+          if constexpr (NB == 4) *reinterpret_cast<uint32_t*>(to) = __float_as_uint(held[is_v][0]);
+          else *reinterpret_cast<uint16_t*>(to) = (uint16_t)__float_as_uint(held[is_v][0]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < L::NS; ++i) reinterpret_cast<float*>(to)[i] = held[is_v][i];
+        }
+      }
+    };
+    auto scale_word = [&](const uint8_t* ss, int tok) -> uint32_t {
+      if constexpr (NB == 4) return reinterpret_cast<const uint32_t*>(ss)[tok];
+      else return reinterpret_cast<const uint16_t*>(ss)[tok];
+    };
+
+    int kb = 0, vb = 1, nb = 2;   // buffers of the step's keys, its values, and the free one
+    int64_t at = place(wave), next_at = place(wave + kWaves);
+    uint64_t valid = places(at);
+    if (valid) {
+      issue(kb, wave, at, valid, 0);
+      issue(vb, wave, at, valid, 1);
+    }
+    // q' of the tile's rows in fp32, times the factor of the scores
+    uint32_t raw[16 * MT / kWaves];
+#pragma unroll
+    for (int k = 0; k < 16 * MT / kWaves; ++k) {
+      const int64_t row = r0 + wave + k * kWaves;
+      raw[k] = 0;
+      if (row < nrows && 2 * lane < D) {
+        const int64_t i = row / p.group;
+        const int h = hk * p.group + (int)(row - i * p.group);
+        raw[k] = *reinterpret_cast<const uint32_t*>(p.q + (q.row0 + i) * p.ldq + (int64_t)h * D + 2 * lane);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 16 * MT / kWaves; ++k) {
+      float a = signed_by(p.sign, 2 * lane, __uint_as_float(raw[k] << 16));
+      float b = signed_by(p.sign, 2 * lane + 1, __uint_as_float(raw[k] & 0xFFFF0000u));
+      rotate_row(a, b, p.n, lane);
+      const float f = p.n > 1 ? p.cn : 1.0f;
+      a = a * f * c;
+      b = b * f * c;
+      if (2 * lane < DP) *reinterpret_cast<f32x2*>(rows + (wave + k * kWaves) * QP + 2 * lane) = f32x2{a, b};
     }
     __syncthreads();
     // its fragments, in two bf16 pieces; value i of a lane is element `order`
     u32x4 qh[MT][NB], ql[MT][NB];
+    f32x4 excess[OFF ? NBLK : 1];   // -136 times the sum over a block of q', every row alike
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int s = 0; s < NB; ++s)
+      for (int s = 0; s < NB; ++s) {
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           float x[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int nib = order<GRID>(i + e);
-            // 1 x 16 blocks: nibbles 0 .. 3 are of the first block of the step, 4 .. 7 of the second
-            const int d = KIND == 1 ? 32 * s + 16 * (nib >> 2) + 4 * g + (nib & 3) : 32 * s + 8 * g + nib;
+            const int nib = order<GRID, OFF, SPLIT>(i + e);
+            const int d = SPLIT ? 32 * s + 16 * (nib >> 2) + 4 * g + (nib & 3) : 32 * s + 8 * g + nib;
             x[e] = rows[(16 * mt + li) * QP + d];
           }
           const uint32_t hi = pack_bf16(x[0], x[1]);
@@ -367,6 +551,23 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
           const float l0 = x[0] - __uint_as_float(hi << 16), l1 = x[1] - __uint_as_float(hi & 0xFFFF0000u);
           ql[mt][s][i / 2] = pack_bf16(fabsf(x[0]) < INFINITY ? l0 : 0.0f, fabsf(x[1]) < INFINITY ? l1 : 0.0f);
         }
+        if constexpr (OFF) {
+          const uint32_t m136 = 0xC308C308u;   // -136 in bf16
+          const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+          if constexpr (SPLIT) {
+            const s16x4 k = __builtin_bit_cast(s16x4, (u32x2{m136, m136}));
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              f32x4 y = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(k, __builtin_bit_cast(s16x4, (u32x2{qh[mt][s][2 * e], qh[mt][s][2 * e + 1]})), z, 0, 0, 0);
+              excess[2 * s + e] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(k, __builtin_bit_cast(s16x4, (u32x2{ql[mt][s][2 * e], ql[mt][s][2 * e + 1]})), y, 0, 0, 0);
+            }
+          } else {
+            const bf16x8 k = __builtin_bit_cast(bf16x8, (u32x4{m136, m136, m136, m136}));
+            f32x4 y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, __builtin_bit_cast(bf16x8, qh[mt][s]), z, 0, 0, 0);
+            excess[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, __builtin_bit_cast(bf16x8, ql[mt][s]), y, 0, 0, 0);
+          }
+        }
+      }
     wait_lds();
     __syncthreads();   // `rows` has been read: the steps may overwrite it
 
@@ -384,149 +585,71 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
     }
     // the earliest last token of any row: steps up to there need no mask
     const int sure = q.len - q.rows + (int)(r0 / p.group);
-
-    // Where token 64 step + lane lies: its row among all, or -1.
-    auto place = [&](int64_t step) -> int64_t {
-      const int64_t t = (first + step) * kStep + lane;
-      if (step >= count || t >= q.len) return -1;
-      const int64_t slot = t >> p.at.page_shift;
-      if (slot >= p.at.width) return -1;
-      const int page = p.at.table[f.b * p.at.ldt + slot];
-      if (page < 0 || page >= p.at.pages) return -1;
-      return (((int64_t)page * p.at.kv_heads + hk) << p.at.page_shift) +
-             (t & (((int64_t)1 << p.at.page_shift) - 1));
-    };
-    // Codes and scales of the step whose rows are `row` into buffer `buf`.  E8M0 scales
-    // that are not a whole word a token come back as its word.
-    auto issue = [&](int buf, int64_t row, uint64_t valid, const uint8_t* codes,
-                     const uint8_t* scales) -> uint32_t {
-      uint32_t tail = 0;
-      const uint32_t to = mine0 + buf * L::UNIT;
-      // a token without a place: any row that has one, and a mask
-      const int some = __builtin_ctzll(valid);
-      const uint32_t lo = row >= 0 ? (uint32_t)row : (uint32_t)__shfl((int)row, some);
-      const uint32_t hi = row >= 0 ? (uint32_t)(row >> 32) : (uint32_t)__shfl((int)(row >> 32), some);
-      const int64_t at = ((int64_t)hi << 32) | lo;
-      const int row_bytes = D / 2;
-      if ((D & 31) == 0) {
-        constexpr int PER = 64 / NB;   // tokens of an instruction
-#pragma unroll
-        for (int i = 0; i < kStep / PER; ++i) {
-          const int tok = PER * i + lane / NB;
-          const int64_t r = ((int64_t)(uint32_t)__shfl((int)hi, tok) << 32) | (uint32_t)__shfl((int)lo, tok);
-          const int ch = (lane % NB) ^ (int)L::flip(tok);
-          if (32 * ch < D) copy16(to + 1024u * i, codes + r * row_bytes + 16 * ch);
-        }
-      } else {   // rows that end inside a chunk, by words
-        constexpr int PER = 16 / NB;
-        for (int i = 0; i < kStep / PER; ++i) {
-          const int tok = PER * i + lane / (4 * NB);
-          const int64_t r = ((int64_t)(uint32_t)__shfl((int)hi, tok) << 32) | (uint32_t)__shfl((int)lo, tok);
-          const int word = lane % (4 * NB);
-          const int ch = (word >> 2) ^ (int)L::flip(tok);
-          if (32 * ch + 8 * (word & 3) < D)
-            copy4(to + 256u * i, codes + r * row_bytes + 16 * ch + 4 * (word & 3));
-        }
-      }
-      const uint32_t ts = to + L::CODES;
-      if constexpr (KIND == 2) {
-        if (D == 128) {
-          copy4(ts, scales + at * 4);
-        } else {
-#pragma unroll
-          for (int i = 0; i < NB; ++i)
-            if (32 * i < D) tail |= (uint32_t)scales[at * (D / 32) + i] << (8 * i);
-        }
-      } else {
-        const int ns = KIND == 1 ? D / 16 : D / 32;
-#pragma unroll
-        for (int i = 0; i < L::NS; ++i)
-          if (i < ns) copy4(ts + 256u * i, scales + (at * ns + i) * 4);
-      }
-      return tail;
-    };
-
-    uint32_t tail_k = 0, tail_v = 0;
-    int kb = 0, vb = 1, nb = 2;   // buffers of the step's keys, its values, and the free one
-    int64_t row = place(wave), next_row = place(wave + kWaves);
-    uint64_t valid = __ballot(row >= 0);
-    if (valid) {
-      tail_k = issue(kb, row, valid, p.k_codes, p.k_scales);
-      tail_v = issue(vb, row, valid, p.v_codes, p.v_scales);
-    }
-    for (int64_t step = wave; step < count; step += kWaves) {
-      const int64_t after_row = place(step + 2 * kWaves);
-      const uint64_t next_valid = __ballot(next_row >= 0);
+    for (int step = wave; step < count; step += kWaves) {
+      const int64_t after_at = place(step + 2 * kWaves);
+      const uint64_t next_valid = places(next_at);
       wait_copies();
-      if constexpr (KIND == 2) {
-        // the scales of values in fp32, and words where they came by bytes
-        uint32_t* ks = reinterpret_cast<uint32_t*>(mine + kb * L::UNIT + L::CODES);
-        uint32_t w = reinterpret_cast<uint32_t*>(mine + vb * L::UNIT + L::CODES)[lane];
-        if (D != 128) {
-          ks[lane] = tail_k;
-          w = tail_v;
-        }
-        float* vs = reinterpret_cast<float*>(mine + 3 * L::UNIT);
+      settle(kb, 0);
+      settle(vb, 1);
+      if constexpr (KIND == 2) {   // the scales of values in fp32
+        const uint32_t w = scale_word(buffer(vb) + L::CODES, lane);
+        float* vs = reinterpret_cast<float*>(wide) + lane * NB;
 #pragma unroll
-        for (int i = 0; i < NB; ++i) vs[64 * i + lane] = __uint_as_float(((w >> (8 * i)) & 0xFFu) << 23);
+        for (int i = 0; i < NB; ++i) vs[i] = __uint_as_float(((w >> (8 * i)) & 0xFFu) << 23);
       }
-      if (next_valid) tail_k = issue(nb, next_row, next_valid, p.k_codes, p.k_scales);
+      if (next_valid) issue(nb, step + kWaves, next_at, next_valid, 0);
       f32x4 s[MT][4];
       if (valid) {
-        const uint8_t* kt = mine + kb * L::UNIT;
-        const float* ks = reinterpret_cast<const float*>(kt + L::CODES);
+        const uint8_t* kt = buffer(kb);
+        const uint8_t* ss = kt + L::CODES;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int tok = 16 * j + li;
+          uint32_t sw = 0;
+          float sc[4][KIND == 2 ? 2 : NBLK];   // scales of the lane's four tokens
+          if constexpr (KIND == 2) {
+            sw = scale_word(ss, tok);
+          } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              read_scales<NBLK>(sc[r], reinterpret_cast<const float*>(ss + (16 * j + 4 * g + r) * L::SC));
+          }
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) s[mt][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-          uint32_t sw = 0;
-          if constexpr (KIND == 2) sw = reinterpret_cast<const uint32_t*>(ks)[tok];
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            const uint8_t* at = kt + tok * L::ROW + 16 * (b ^ (int)L::flip(tok));
-            if constexpr (KIND == 1) {
-              const uint32_t x = (uint32_t)*reinterpret_cast<const uint16_t*>(at + 2 * g) |
-                                 (uint32_t)*reinterpret_cast<const uint16_t*>(at + 8 + 2 * g) << 16;
-              const u32x4 v = decode8<GRID>(x, 1.0f);
-              // values 0 .. 3 of the order above lie in registers 0, 1 (E2M1) or 0, 2
-              constexpr int A1 = GRID == 2 ? 1 : 2, B0 = GRID == 2 ? 2 : 1;
-              const s16x4 ka = __builtin_bit_cast(s16x4, (u32x2{v[0], v[A1]}));
-              const s16x4 kc = __builtin_bit_cast(s16x4, (u32x2{v[B0], v[3]}));
-              const f32x4 s0 = *reinterpret_cast<const f32x4*>(ks + 64 * (2 * b) + 16 * j + 4 * g);
-              const f32x4 s1 = *reinterpret_cast<const f32x4*>(ks + 64 * (2 * b + 1) + 16 * j + 4 * g);
+            const uint8_t* at_k = kt + tok * L::ROW + 16 * (b ^ (int)L::flip(tok));
+            if constexpr (SPLIT) {
+              const uint32_t x = (uint32_t)*reinterpret_cast<const uint16_t*>(at_k + 2 * g) |
+                                 (uint32_t)*reinterpret_cast<const uint16_t*>(at_k + 8 + 2 * g) << 16;
+              const u32x4 v = decode8<GRID, OFF, true>(x, 1.0f);
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                const u32x4 h = qh[mt][b], w = ql[mt][b];
-                f32x4 x0 = {0.0f, 0.0f, 0.0f, 0.0f}, x1 = x0;
-                x0 = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(ka, __builtin_bit_cast(s16x4, (u32x2{h[0], h[A1]})), x0, 0, 0, 0);
-                x1 = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(kc, __builtin_bit_cast(s16x4, (u32x2{h[B0], h[3]})), x1, 0, 0, 0);
-                x0 = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(ka, __builtin_bit_cast(s16x4, (u32x2{w[0], w[A1]})), x0, 0, 0, 0);
-                x1 = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(kc, __builtin_bit_cast(s16x4, (u32x2{w[B0], w[3]})), x1, 0, 0, 0);
-                const bool second = 32 * b + 16 < D;
+              for (int e = 0; e < 2; ++e) {
+                const s16x4 k = __builtin_bit_cast(s16x4, (u32x2{v[2 * e], v[2 * e + 1]}));
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                  if (32 * b < D) s[mt][j][r] = __builtin_fmaf(x0[r], s0[r], s[mt][j][r]);
-                  if (second) s[mt][j][r] = __builtin_fmaf(x1[r], s1[r], s[mt][j][r]);
+                for (int mt = 0; mt < MT; ++mt) {
+                  f32x4 y = OFF ? excess[OFF ? 2 * b + e : 0] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                  y = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(k, __builtin_bit_cast(s16x4, (u32x2{qh[mt][b][2 * e], qh[mt][b][2 * e + 1]})), y, 0, 0, 0);
+                  y = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(k, __builtin_bit_cast(s16x4, (u32x2{ql[mt][b][2 * e], ql[mt][b][2 * e + 1]})), y, 0, 0, 0);
+#pragma unroll
+                  for (int r = 0; r < 4; ++r) s[mt][j][r] = __builtin_fmaf(y[r], sc[r][KIND == 2 ? 0 : 2 * b + e], s[mt][j][r]);
                 }
               }
             } else {
-              const uint32_t x = *reinterpret_cast<const uint32_t*>(at + 4 * g);
+              const uint32_t x = *reinterpret_cast<const uint32_t*>(at_k + 4 * g);
               float scale = 1.0f;
               if constexpr (KIND == 2) scale = __uint_as_float(((sw >> (8 * b)) & 0xFFu) << 23);
-              const bf16x8 k8 = __builtin_bit_cast(bf16x8, decode8<GRID>(x, scale));
-              f32x4 sc = {1.0f, 1.0f, 1.0f, 1.0f};
-              if constexpr (KIND == 0) sc = *reinterpret_cast<const f32x4*>(ks + 64 * b + 16 * j + 4 * g);
+              const bf16x8 k8 = __builtin_bit_cast(bf16x8, decode8<GRID, OFF, false>(x, scale));
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
-                f32x4 y = KIND == 2 ? s[mt][j] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                f32x4 y = KIND == 2 ? s[mt][j] : OFF ? excess[OFF ? b : 0] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                 y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8, __builtin_bit_cast(bf16x8, qh[mt][b]), y, 0, 0, 0);
                 y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8, __builtin_bit_cast(bf16x8, ql[mt][b]), y, 0, 0, 0);
-                if constexpr (KIND == 2) {
-                  if (32 * b < D) s[mt][j] = y;
-                } else if (32 * b < D) {
+                if constexpr (KIND == 2) {   // the conversion has applied the scale
+                  s[mt][j] = y;
+                } else {
 #pragma unroll
-                  for (int r = 0; r < 4; ++r) s[mt][j][r] = __builtin_fmaf(y[r], sc[r], s[mt][j][r]);
+                  for (int r = 0; r < 4; ++r) s[mt][j][r] = __builtin_fmaf(y[r], sc[r][b], s[mt][j][r]);
                 }
               }
             }
@@ -535,25 +658,36 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
       }
       // the keys have been read: the next step's values take their place
       wait_lds();
-      if (next_valid) tail_v = issue(kb, next_row, next_valid, p.v_codes, p.v_scales);
+      if (next_valid) issue(kb, step + kWaves, next_at, next_valid, 1);
       if (valid) {
-        const int64_t t0 = (first + step) * kStep;
-        const bool masked = valid != ~(uint64_t)0 || t0 + kStep - 1 > sure;
+        const uint8_t* vt = buffer(vb);
+        const int vtok = 16 * (li >> 2) + 4 * g + (li & 3);
+        i32x2 vc[2 * NB];   // a column of 16 values: eight codes of each half of the step
+#pragma unroll
+        for (int d = 0; d < 2 * NB; ++d) {
+          const uint8_t* at_v = vt + vtok * L::ROW + 16 * ((d >> 1) ^ (int)L::flip(vtok)) + 8 * (d & 1);
+          typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+          vc[d] = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i32x2*)at_v);
+        }
+        const int t0 = t_first + step * kStep;
+        if (valid != ~(uint64_t)0 || t0 + kStep - 1 > sure) {
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+              for (int r = 0; r < 4; ++r) {
+                const int tok = 16 * j + 4 * g + r;
+                if (t0 + tok > last[mt] || !((valid >> tok) & 1)) s[mt][j][r] = -INFINITY;
+              }
+        }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           float top = -INFINITY;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              float z = s[mt][j][r] * c;
-              if (masked) {
-                const int tok = 16 * j + 4 * g + r;
-                if (t0 + tok > last[mt] || !((valid >> tok) & 1)) z = -INFINITY;
-              }
-              s[mt][j][r] = z;
-              top = fmaxf(top, z);
-            }
+            for (int r = 0; r < 4; ++r) top = fmaxf(top, s[mt][j][r]);
           top = query_max(top);
           if (__any(top > m[mt] + 8.0f)) {
             const float next = top > m[mt] + 8.0f ? top : m[mt];
@@ -574,48 +708,34 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
               l[mt] += s[mt][j][r];
             }
         }
-        const uint8_t* vt = mine + vb * L::UNIT;
-        const float* vs = reinterpret_cast<const float*>(KIND == 2 ? mine + 3 * L::UNIT : vt + L::CODES);
-        constexpr int BD = KIND == 1 ? 1 : 2;   // 16-element columns of a block
-        const int vtok = 16 * (li >> 2) + 4 * g + (li & 3);
+        const uint8_t* vs = KIND == 2 ? wide : vt + L::CODES;
+        constexpr int VSC = KIND == 2 ? 4 * NB : L::SC;   // bytes of a token's fp32 scales
+        constexpr int BD = SPLIT ? 1 : 2;                 // 16-element columns of a block
 #pragma unroll
-        for (int b = 0; b < 2 * NB / BD; ++b) {
-          if (16 * BD * b >= D) continue;
-          bf16x8 w[MT][2];
+        for (int x = 0; x < 2; ++x) {                     // half of the step
+          // weights times scales, for every block of the values
+          u32x4 w[MT][NBLK];
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const f32x4 a = *reinterpret_cast<const f32x4*>(vs + 64 * b + 32 * x + 4 * g);
-            const f32x4 e = *reinterpret_cast<const f32x4*>(vs + 64 * b + 32 * x + 16 + 4 * g);
+          for (int i = 0; i < 4; ++i) {
+            const int e0 = order<GRID, false, false>(2 * i), e1 = order<GRID, false, false>(2 * i + 1);
+            float a[NBLK], b[NBLK];
+            read_scales<NBLK>(a, reinterpret_cast<const float*>(vs + (32 * x + 16 * (e0 >> 2) + 4 * g + (e0 & 3)) * VSC));
+            read_scales<NBLK>(b, reinterpret_cast<const float*>(vs + (32 * x + 16 * (e1 >> 2) + 4 * g + (e1 & 3)) * VSC));
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              float y[8];
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-              for (int r = 0; r < 4; ++r) {
-                y[r] = s[mt][2 * x][r] * a[r];
-                y[4 + r] = s[mt][2 * x + 1][r] * e[r];
-                if (masked) {   // whatever the scale of a token that is not seen
-                  y[r] = s[mt][2 * x][r] == 0.0f ? 0.0f : y[r];
-                  y[4 + r] = s[mt][2 * x + 1][r] == 0.0f ? 0.0f : y[4 + r];
-                }
-              }
-              u32x4 v;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) v[i] = pack_bf16(y[order<GRID>(2 * i)], y[order<GRID>(2 * i + 1)]);
-              w[mt][x] = __builtin_bit_cast(bf16x8, v);
-            }
+              for (int k = 0; k < NBLK; ++k)
+                // 0 times whatever the scale of a token that is not seen holds is 0
+                w[mt][k][i] = pack_bf16(mul_legacy(s[mt][2 * x + (e0 >> 2)][e0 & 3], a[k]),
+                                        mul_legacy(s[mt][2 * x + (e1 >> 2)][e1 & 3], b[k]));
           }
 #pragma unroll
-          for (int e = 0; e < BD; ++e) {
-            const int d = BD * b + e;
-            const uint8_t* at = vt + vtok * L::ROW + 16 * ((d >> 1) ^ (int)L::flip(vtok)) + 8 * (d & 1);
-            typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
-            const i32x2 x = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i32x2*)at);
-            const bf16x8 v0 = __builtin_bit_cast(bf16x8, decode8<GRID>((uint32_t)x[0], 1.0f));
-            const bf16x8 v1 = __builtin_bit_cast(bf16x8, decode8<GRID>((uint32_t)x[1], 1.0f));
+          for (int d = 0; d < 2 * NB; ++d) {
+            const bf16x8 v = __builtin_bit_cast(bf16x8, decode8<GRID, false, false>((uint32_t)vc[d][x], 1.0f));
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
-              o[mt][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, w[mt][0], o[mt][d], 0, 0, 0);
-              o[mt][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, w[mt][1], o[mt][d], 0, 0, 0);
+              const bf16x8 y = __builtin_bit_cast(bf16x8, w[mt][d / BD]);
+              o[mt][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, y, o[mt][d], 0, 0, 0);
             }
           }
         }
@@ -625,8 +745,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
       vb = kb;
       kb = nb;
       nb = free_now;
-      row = next_row;
-      next_row = after_row;
+      at = next_at;
+      next_at = after_at;
       valid = next_valid;
     }
     wait_copies();
@@ -664,7 +784,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
       }
       __syncthreads();
     }
-    const bool whole = first == 0 && count == q.units;
+    const bool whole = first == 0 && count == (int)q.units;
     float* part = p.partial + (int64_t)(2 * blockIdx.x + (leading ? 0 : 1)) * (16 * MT) * (D + 2);
     for (int r = wave; r < 16 * MT; r += kWaves) {
       const int64_t at = r0 + r;
@@ -702,7 +822,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_join(KvAttn p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int w = blockIdx.x + 1, D = p.at.D;
   Found f;
-  const int64_t quota = plan(p, kKvGroups, w, plan_lds, f);
+  const int64_t quota = plan(p, p.groups, w, plan_lds, f);
   if (f.b >= p.at.B) return;
   const Seq q = sequence(p, f.b);
   const int64_t u = (int64_t)w * quota, item = (u - f.before) / (q.units + kItem);
@@ -723,30 +843,55 @@ __global__ __launch_bounds__(kThreads) void k_kv_join(KvAttn p) {
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
   float a = 0.0f, b = 0.0f, l = 0.0f;
-  for (int x = w0; x <= w1; ++x) {
-    const float* from = part(x);
-    const f32x2 s = *reinterpret_cast<const f32x2*>(from + D);
-    f32x2 y = {0.0f, 0.0f};
-    if (2 * lane < D) y = *reinterpret_cast<const f32x2*>(from + 2 * lane);
-    if (s[1] == 0.0f) continue;   // saw nothing
-    const float fac = __builtin_amdgcn_exp2f(s[0] - top);
-    a += y[0] * fac;
-    b += y[1] * fac;
-    l += s[1] * fac;
+  for (int x0 = w0; x0 <= w1; x0 += 64) {
+    // lane i: the factor of part x0 + i, and what it adds to l; a part that saw nothing adds nothing
+    float fac = 0.0f;
+    if (x0 + lane <= w1) {
+      const f32x2 s = *reinterpret_cast<const f32x2*>(part(x0 + lane) + D);
+      fac = s[1] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(s[0] - top);
+      l += s[1] * fac;
+    }
+    const int n = min(w1 - x0 + 1, 64);
+    for (int i = 0; i < n; i += 8) {   // eight parts' loads at once
+      f32x2 y[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        y[k] = f32x2{0.0f, 0.0f};
+        if (i + k < n && 2 * lane < D) y[k] = *reinterpret_cast<const f32x2*>(part(x0 + i + k) + 2 * lane);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float e = __shfl(fac, i + k);
+        if (e != 0.0f) {
+          a += y[k][0] * e;
+          b += y[k][1] * e;
+        }
+      }
+    }
   }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) l += __shfl_xor(l, d);
   const int64_t i = at / p.group;
   store_row(p, a, b, l, q.row0 + i, hk * p.group + (int)(at - i * p.group), lane);
+}
+
+template <int GRID, int KIND, int NB, int MT>
+void launch_nb(const KvAttn& p, hipStream_t s) {
+  if (p.at.D == 32 * NB && p.at.page_shift >= 6)
+    k_kv_attn<GRID, KIND, NB, MT, true><<<(unsigned)p.groups, kThreads, 0, s>>>(p);
+  else
+    k_kv_attn<GRID, KIND, NB, MT, false><<<(unsigned)p.groups, kThreads, 0, s>>>(p);
 }
 
 template <int GRID, int KIND>
 void launch(const KvAttn& p, hipStream_t s) {
   const bool narrow = p.at.D <= 64;
   if (p.rows16 == 1) {
-    if (narrow) k_kv_attn<GRID, KIND, 2, 1><<<kKvGroups, kThreads, 0, s>>>(p);
-    else k_kv_attn<GRID, KIND, 4, 1><<<kKvGroups, kThreads, 0, s>>>(p);
+    if (narrow) launch_nb<GRID, KIND, 2, 1>(p, s);
+    else launch_nb<GRID, KIND, 4, 1>(p, s);
   } else {
-    if (narrow) k_kv_attn<GRID, KIND, 2, 2><<<kKvGroups, kThreads, 0, s>>>(p);
-    else k_kv_attn<GRID, KIND, 4, 2><<<kKvGroups, kThreads, 0, s>>>(p);
+    if (narrow) launch_nb<GRID, KIND, 2, 2>(p, s);
+    else launch_nb<GRID, KIND, 4, 2>(p, s);
   }
 }
 
@@ -771,13 +916,15 @@ int64_t kv_attn_workspace(int64_t T, int32_t B, int32_t heads, int32_t kv_heads,
   return (int64_t)2 * kKvGroups * 16 * kv_attn_rows16(T, B, heads / kv_heads) * (D + 2) * 4;
 }
 
-hipError_t launch_kv_attn(const KvAttn& p, hipStream_t s) {
+hipError_t launch_kv_attn(const KvAttn& args, hipStream_t s) {
+  KvAttn p = args;
+  p.groups = p.rows16 == 2 && p.at.D > 64 ? kKvGroups / 2 : kKvGroups;   // one workgroup fits a compute unit, or two
   switch (p.grid) {
     case 0: launch_grid<0>(p, s); break;
     case 1: launch_grid<1>(p, s); break;
     default: launch_grid<2>(p, s); break;
   }
-  k_kv_join<<<dim3(kKvGroups - 1, 4 * (unsigned)p.rows16), kThreads, 0, s>>>(p);
+  k_kv_join<<<dim3((unsigned)p.groups - 1, 4 * (unsigned)p.rows16), kThreads, 0, s>>>(p);
   return hipGetLastError();
 }
 
