@@ -64,7 +64,7 @@ struct KvRows {            // write and read
 hipError_t launch_kv_write(const KvRows& p, hipStream_t s);
 hipError_t launch_kv_read(const KvRows& p, hipStream_t s);
 
-constexpr int kKvGroups = 512;   // workgroups of the attention over a cache at most: two per compute unit
+constexpr int kKvGroups = 512;   // workgroups of the attention over a cache: two per compute unit
 struct KvAttn {
   KvPlace at;
   const uint16_t* q;
@@ -78,7 +78,6 @@ struct KvAttn {
   float cn, scale;
   int32_t n, grid, kind;   // kind: 0 fp32 / 32, 1 fp32 / 16, 2 E8M0 / 32
   int32_t heads, group, rows16;   // rows16: 16-row tiles that a workgroup takes at once
-  int32_t groups;          // workgroups (set by the launcher)
   float* partial;          // [2 kKvGroups][16 rows16][D + 2]
 };
 int32_t kv_attn_rows16(int64_t T, int32_t B, int32_t group);

@@ -57,6 +57,11 @@ __device__ __forceinline__ uint32_t lds_address(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) uint8_t*)p;
 }
 
+__device__ __forceinline__ int64_t uniform64(int64_t x) {
+  return ((int64_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32) |
+         (uint32_t)__builtin_amdgcn_readfirstlane((int)x);
+}
+
 // a b, and 0 where either is 0, whatever the other (v_mul_legacy_f32).
 extern "C" __device__ float ufp4_llvm_fmul_legacy(float, float) __asm("llvm.amdgcn.fmul.legacy");
 __device__ __forceinline__ float mul_legacy(float a, float b) { return ufp4_llvm_fmul_legacy(a, b); }
@@ -81,6 +86,8 @@ __device__ __forceinline__ void copy4(uint32_t lds, uint64_t base, uint32_t off)
                : : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(off), "s"(base) : "memory");
 }
 __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" : : : "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_all_but() { asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory"); }
 __device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory"); }
 
 // Maximum and sum over the lanes that hold one query (l % 16).
@@ -156,18 +163,26 @@ __device__ constexpr int order(int i) {
   return i < 4 ? 2 * i : 2 * i - 7;
 }
 
-// Butterflies over a row of D elements, two neighbours to a lane.
-__device__ __forceinline__ void rotate_row(float& a, float& b, int n, int lane) {
+// Butterflies over N rows of D elements, two neighbours to a lane.
+template <int N>
+__device__ __forceinline__ void rotate_rows(float (&a)[N], float (&b)[N], int n, int lane) {
   if (n > 1) {
-    const float s = a + b, d = a - b;
-    a = s;
-    b = d;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const float s = a[k] + b[k], d = a[k] - b[k];
+      a[k] = s;
+      b[k] = d;
+    }
   }
   for (int h = 2; h < n; h <<= 1) {
     const int m = h >> 1;
-    const float pa = __shfl_xor(a, m), pb = __shfl_xor(b, m);
-    a = (lane & m) ? pa - a : a + pa;
-    b = (lane & m) ? pb - b : b + pb;
+    const uint32_t neg = (lane & m) ? 0x80000000u : 0u;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const float pa = __shfl_xor(a[k], m), pb = __shfl_xor(b[k], m);
+      a[k] = pa + __uint_as_float(__float_as_uint(a[k]) ^ neg);
+      b[k] = pb + __uint_as_float(__float_as_uint(b[k]) ^ neg);
+    }
   }
 }
 // Signs of elements 2 lane, 2 lane + 1 of a row.
@@ -180,8 +195,8 @@ __device__ __forceinline__ float signed_by(const uint32_t (&sign)[4], int e, flo
 // What an item (a tile of queries of one key head) costs besides its steps, in steps:
 // rotating its queries, filling and joining its waves.  Without it a workgroup that
 // drew the short sequences of a batch took 88 of them one after another, 590 us where
-// the others were done after 100.
-constexpr int kItem = 4;
+// the others were done after 100; 4 steps: 160 us, 8: 105, 12: 83.
+constexpr int kItem = 12;
 
 // Sequence b's share of the work.
 struct Seq {
@@ -246,6 +261,23 @@ __device__ __forceinline__ int64_t quota_of(int64_t total, int groups) {
 // The quota, and the sequence that holds unit w quota.
 __device__ __forceinline__ int64_t plan(const KvAttn& p, int groups, int w, PlanLds& s, Found& f) {
   const int B = p.at.B;
+  if (B <= 64) {   // every wave by itself
+    const int lane = threadIdx.x & 63;
+    int64_t mine = 0;
+    if (lane < B) mine = sequence(p, lane).cost(p.at.kv_heads);
+    int64_t sum = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int64_t y = __shfl_up((long long)sum, d);
+      if (lane >= d) sum += y;
+    }
+    const int64_t quota = quota_of(__shfl((long long)sum, 63), groups), u = (int64_t)w * quota;
+    const uint64_t here = __ballot(u < sum && u >= sum - mine);
+    f.b = here ? __builtin_ctzll(here) : B;
+    f.before = uniform64(__shfl((long long)(sum - mine), f.b & 63));
+    f.b = __builtin_amdgcn_readfirstlane(f.b);
+    return uniform64(quota);
+  }
   int64_t total = 0, own = 0, upto = 0;
   for (int b0 = 0; b0 < B; b0 += kThreads) {
     const int b = b0 + (int)threadIdx.x;
@@ -281,23 +313,37 @@ __device__ __forceinline__ int64_t plan(const KvAttn& p, int groups, int w, Plan
   __syncthreads();
   f = s.found;
   f.b = __builtin_amdgcn_readfirstlane(f.b);
-  return quota;
+  f.before = uniform64(f.before);
+  return uniform64(quota);
 }
 
-// One row of o', divided by l and out of the basis of the rotation, to memory.
-__device__ __forceinline__ void store_row(const KvAttn& p, float a, float b, float l, int64_t row,
-                                          int h, int lane) {
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;   // nothing to attend to: 0
-  a *= inv;
-  b *= inv;
-  rotate_row(a, b, p.n, lane);
-  if (p.n > 1) {
-    a *= p.cn;
-    b *= p.cn;
+// Rows at, at + kWaves, .. (of `nrows`) of o', divided by l and out of the basis of the rotation,
+// to memory.
+template <int N>
+__device__ __forceinline__ void store_rows(const KvAttn& p, float (&a)[N], float (&b)[N],
+                                           const float (&l)[N], int row0, int64_t at,
+                                           int64_t nrows, int hk, int lane) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const float inv = l[k] == 0.0f ? 0.0f : 1.0f / l[k];   // nothing to attend to: 0
+    a[k] *= inv;
+    b[k] *= inv;
   }
-  if (2 * lane < p.at.D)
-    *reinterpret_cast<uint32_t*>(p.o + row * p.ldo + (int64_t)h * p.at.D + 2 * lane) =
-        pack_bf16(signed_by(p.sign, 2 * lane, a), signed_by(p.sign, 2 * lane + 1, b));
+  rotate_rows<N>(a, b, p.n, lane);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    if (p.n > 1) {
+      a[k] *= p.cn;
+      b[k] *= p.cn;
+    }
+    const int64_t r = at + k * kWaves;
+    if (r < nrows && 2 * lane < p.at.D) {
+      const int64_t i = r / p.group;
+      const int h = hk * p.group + (int)(r - i * p.group);
+      *reinterpret_cast<uint32_t*>(p.o + (row0 + i) * p.ldo + (int64_t)h * p.at.D + 2 * lane) =
+          pack_bf16(signed_by(p.sign, 2 * lane, a[k]), signed_by(p.sign, 2 * lane + 1, b[k]));
+    }
+  }
 }
 
 // LDS of one wave: three buffers that K and V take in turn, each the codes of 64
@@ -309,6 +355,8 @@ struct Lay {
   static constexpr int SC = KIND == 2 ? NB : KIND == 1 ? 8 * NB : 4 * NB;
   static constexpr int NS = SC / 4;   // words of a token (KIND 2, NB = 2: half a word)
   static constexpr int UNIT = CODES + kStep * SC;
+  // copies of a step's keys or values (whole pages)
+  static constexpr int COPIES = CODES / 1024 + (kStep * SC > 1024 ? 2 : 1);
   static constexpr int WIDE = KIND == 2 ? kStep * 4 * NB : 0;   // a step's value scales in fp32
   static constexpr int PAIR = 2 * UNIT + WIDE;                  // a wave's part but the third buffer
   __device__ static uint32_t flip(int tok) {
@@ -338,7 +386,7 @@ __device__ __forceinline__ void read_scales(float (&x)[N], const float* at) {
 // each and its page one scalar: its copies need no address arithmetic (otherwise a
 // step's addresses cost as many instructions as half of its arithmetic).
 template <int GRID, int KIND, int NB, int MT, bool FAST>
-__global__ __launch_bounds__(kThreads, MT == 2 && NB == 4 ? 1 : 2) void k_kv_attn(KvAttn p) {
+__global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
   using L = Lay<KIND, NB>;
   constexpr int DP = 32 * NB, QP = DP + 4;
   constexpr bool SPLIT = KIND == 1;
@@ -346,9 +394,11 @@ __global__ __launch_bounds__(kThreads, MT == 2 && NB == 4 ? 1 : 2) void k_kv_att
   // would carry the rounding of 136 weights where a value is 0
   constexpr bool OFF = GRID == 1 && MT == 1 && KIND != 2;
   constexpr int NBLK = SPLIT ? 2 * NB : NB;   // blocks of a row
+  constexpr int GB = NBLK < 4 ? NBLK : 4;     // blocks whose scales are read together
   constexpr int kRows = kWaves * L::PAIR;   // where the waves' third buffers lie, and `rows`
   constexpr int kThird = kWaves * L::UNIT > 16 * MT * QP * 4 ? kWaves * L::UNIT : 16 * MT * QP * 4;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kRows + kThird];
+  constexpr int kParts = kWaves * 16 * MT * QP * 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kRows + kThird > kParts ? kRows + kThird : kParts];
   __shared__ PlanLds plan_lds;
   __shared__ float stat[2][kWaves][16 * MT];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -360,7 +410,7 @@ __global__ __launch_bounds__(kThreads, MT == 2 && NB == 4 ? 1 : 2) void k_kv_att
   const int64_t u_end = u + quota;
   const int64_t u_first = u;
   const float c = p.scale * kLog2e;
-  float* rows = reinterpret_cast<float*>(lds + kRows);   // [16 MT][QP], before and after the steps
+  float* rows = reinterpret_cast<float*>(lds + kRows);   // [16 MT][QP], before the steps
   uint8_t* const wide = lds + wave * L::PAIR + 2 * L::UNIT;
   auto buffer = [&](int b) -> uint8_t* {
     return b < 2 ? lds + wave * L::PAIR + b * L::UNIT : lds + kRows + wave * L::UNIT;
@@ -518,15 +568,20 @@ __global__ __launch_bounds__(kThreads, MT == 2 && NB == 4 ? 1 : 2) void k_kv_att
         raw[k] = *reinterpret_cast<const uint32_t*>(p.q + (q.row0 + i) * p.ldq + (int64_t)h * D + 2 * lane);
       }
     }
+    {
+      constexpr int PER = 16 * MT / kWaves;
+      float a[PER], b[PER];
 #pragma unroll
-    for (int k = 0; k < 16 * MT / kWaves; ++k) {
-      float a = signed_by(p.sign, 2 * lane, __uint_as_float(raw[k] << 16));
-      float b = signed_by(p.sign, 2 * lane + 1, __uint_as_float(raw[k] & 0xFFFF0000u));
-      rotate_row(a, b, p.n, lane);
+      for (int k = 0; k < PER; ++k) {
+        a[k] = signed_by(p.sign, 2 * lane, __uint_as_float(raw[k] << 16));
+        b[k] = signed_by(p.sign, 2 * lane + 1, __uint_as_float(raw[k] & 0xFFFF0000u));
+      }
+      rotate_rows<PER>(a, b, p.n, lane);
       const float f = p.n > 1 ? p.cn : 1.0f;
-      a = a * f * c;
-      b = b * f * c;
-      if (2 * lane < DP) *reinterpret_cast<f32x2*>(rows + (wave + k * kWaves) * QP + 2 * lane) = f32x2{a, b};
+#pragma unroll
+      for (int k = 0; k < PER; ++k)
+        if (2 * lane < DP)
+          *reinterpret_cast<f32x2*>(rows + (wave + k * kWaves) * QP + 2 * lane) = f32x2{a[k] * f * c, b[k] * f * c};
     }
     __syncthreads();
     // its fragments, in two bf16 pieces; value i of a lane is element `order`
@@ -588,15 +643,10 @@ __global__ __launch_bounds__(kThreads, MT == 2 && NB == 4 ? 1 : 2) void k_kv_att
     for (int step = wave; step < count; step += kWaves) {
       const int64_t after_at = place(step + 2 * kWaves);
       const uint64_t next_valid = places(next_at);
-      wait_copies();
+      // the keys are there; the values, copied after them, may still be on their way
+      if constexpr (FAST) wait_all_but<L::COPIES>();
+      else wait_copies();
       settle(kb, 0);
-      settle(vb, 1);
-      if constexpr (KIND == 2) {   // the scales of values in fp32
-        const uint32_t w = scale_word(buffer(vb) + L::CODES, lane);
-        float* vs = reinterpret_cast<float*>(wide) + lane * NB;
-#pragma unroll
-        for (int i = 0; i < NB; ++i) vs[i] = __uint_as_float(((w >> (8 * i)) & 0xFFu) << 23);
-      }
       if (next_valid) issue(nb, step + kWaves, next_at, next_valid, 0);
       f32x4 s[MT][4];
       if (valid) {
@@ -606,18 +656,20 @@ __global__ __launch_bounds__(kThreads, MT == 2 && NB == 4 ? 1 : 2) void k_kv_att
         for (int j = 0; j < 4; ++j) {
           const int tok = 16 * j + li;
           uint32_t sw = 0;
-          float sc[4][KIND == 2 ? 2 : NBLK];   // scales of the lane's four tokens
-          if constexpr (KIND == 2) {
-            sw = scale_word(ss, tok);
-          } else {
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              read_scales<NBLK>(sc[r], reinterpret_cast<const float*>(ss + (16 * j + 4 * g + r) * L::SC));
-          }
+          float sc[4][GB];   // scales of the lane's four tokens, of the blocks in work
+          if constexpr (KIND == 2) sw = scale_word(ss, tok);
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) s[mt][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
+            constexpr int PER = SPLIT ? GB / 2 : GB;   // blocks or pairs of them in a group
+            if constexpr (KIND != 2) {
+              if (b % PER == 0) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                  read_scales<GB>(sc[r], reinterpret_cast<const float*>(ss + (16 * j + 4 * g + r) * L::SC) + b / PER * GB);
+              }
+            }
             const uint8_t* at_k = kt + tok * L::ROW + 16 * (b ^ (int)L::flip(tok));
             if constexpr (SPLIT) {
               const uint32_t x = (uint32_t)*reinterpret_cast<const uint16_t*>(at_k + 2 * g) |
@@ -632,7 +684,7 @@ __global__ __launch_bounds__(kThreads, MT == 2 && NB == 4 ? 1 : 2) void k_kv_att
                   y = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(k, __builtin_bit_cast(s16x4, (u32x2{qh[mt][b][2 * e], qh[mt][b][2 * e + 1]})), y, 0, 0, 0);
                   y = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(k, __builtin_bit_cast(s16x4, (u32x2{ql[mt][b][2 * e], ql[mt][b][2 * e + 1]})), y, 0, 0, 0);
 #pragma unroll
-                  for (int r = 0; r < 4; ++r) s[mt][j][r] = __builtin_fmaf(y[r], sc[r][KIND == 2 ? 0 : 2 * b + e], s[mt][j][r]);
+                  for (int r = 0; r < 4; ++r) s[mt][j][r] = __builtin_fmaf(y[r], sc[r][(2 * b + e) % GB], s[mt][j][r]);
                 }
               }
             } else {
@@ -649,7 +701,7 @@ __global__ __launch_bounds__(kThreads, MT == 2 && NB == 4 ? 1 : 2) void k_kv_att
                   s[mt][j] = y;
                 } else {
 #pragma unroll
-                  for (int r = 0; r < 4; ++r) s[mt][j][r] = __builtin_fmaf(y[r], sc[r][b], s[mt][j][r]);
+                  for (int r = 0; r < 4; ++r) s[mt][j][r] = __builtin_fmaf(y[r], sc[r][b % GB], s[mt][j][r]);
                 }
               }
             }
@@ -658,16 +710,16 @@ __global__ __launch_bounds__(kThreads, MT == 2 && NB == 4 ? 1 : 2) void k_kv_att
       }
       // the keys have been read: the next step's values take their place
       wait_lds();
+      if (FAST && next_valid) wait_all_but<L::COPIES>();   // this step's values are there
+      else wait_copies();
+      if (valid) settle(vb, 1);   // before the next ones are loaded
       if (next_valid) issue(kb, step + kWaves, next_at, next_valid, 1);
       if (valid) {
-        const uint8_t* vt = buffer(vb);
-        const int vtok = 16 * (li >> 2) + 4 * g + (li & 3);
-        i32x2 vc[2 * NB];   // a column of 16 values: eight codes of each half of the step
+        if constexpr (KIND == 2) {   // the scales of values in fp32
+          const uint32_t w = scale_word(buffer(vb) + L::CODES, lane);
+          float* vs = reinterpret_cast<float*>(wide) + lane * NB;
 #pragma unroll
-        for (int d = 0; d < 2 * NB; ++d) {
-          const uint8_t* at_v = vt + vtok * L::ROW + 16 * ((d >> 1) ^ (int)L::flip(vtok)) + 8 * (d & 1);
-          typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
-          vc[d] = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i32x2*)at_v);
+          for (int i = 0; i < NB; ++i) vs[i] = __uint_as_float(((w >> (8 * i)) & 0xFFu) << 23);
         }
         const int t0 = t_first + step * kStep;
         if (valid != ~(uint64_t)0 || t0 + kStep - 1 > sure) {
@@ -708,34 +760,46 @@ __global__ __launch_bounds__(kThreads, MT == 2 && NB == 4 ? 1 : 2) void k_kv_att
               l[mt] += s[mt][j][r];
             }
         }
+        const uint8_t* vt = buffer(vb);
         const uint8_t* vs = KIND == 2 ? wide : vt + L::CODES;
+        const int vtok = 16 * (li >> 2) + 4 * g + (li & 3);
         constexpr int VSC = KIND == 2 ? 4 * NB : L::SC;   // bytes of a token's fp32 scales
         constexpr int BD = SPLIT ? 1 : 2;                 // 16-element columns of a block
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {                     // half of the step
-          // weights times scales, for every block of the values
-          u32x4 w[MT][NBLK];
+        for (int k0 = 0; k0 < NBLK; k0 += GB) {           // blocks of the values
+          i32x2 vc[GB * BD];   // columns of 16 values: eight codes of each half of the step
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int e0 = order<GRID, false, false>(2 * i), e1 = order<GRID, false, false>(2 * i + 1);
-            float a[NBLK], b[NBLK];
-            read_scales<NBLK>(a, reinterpret_cast<const float*>(vs + (32 * x + 16 * (e0 >> 2) + 4 * g + (e0 & 3)) * VSC));
-            read_scales<NBLK>(b, reinterpret_cast<const float*>(vs + (32 * x + 16 * (e1 >> 2) + 4 * g + (e1 & 3)) * VSC));
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-              for (int k = 0; k < NBLK; ++k)
-                // 0 times whatever the scale of a token that is not seen holds is 0
-                w[mt][k][i] = pack_bf16(mul_legacy(s[mt][2 * x + (e0 >> 2)][e0 & 3], a[k]),
-                                        mul_legacy(s[mt][2 * x + (e1 >> 2)][e1 & 3], b[k]));
+          for (int e = 0; e < GB * BD; ++e) {
+            const int d = BD * k0 + e;
+            const uint8_t* at_v = vt + vtok * L::ROW + 16 * ((d >> 1) ^ (int)L::flip(vtok)) + 8 * (d & 1);
+            typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
+            vc[e] = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_i32x2*)at_v);
           }
 #pragma unroll
-          for (int d = 0; d < 2 * NB; ++d) {
-            const bf16x8 v = __builtin_bit_cast(bf16x8, decode8<GRID, false, false>((uint32_t)vc[d][x], 1.0f));
+          for (int x = 0; x < 2; ++x) {                   // half of the step
+            u32x4 w[MT][GB];                              // weights times scales
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              const bf16x8 y = __builtin_bit_cast(bf16x8, w[mt][d / BD]);
-              o[mt][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, y, o[mt][d], 0, 0, 0);
+            for (int i = 0; i < 4; ++i) {
+              constexpr bool NO = false;
+              const int e0 = order<GRID, NO, NO>(2 * i), e1 = order<GRID, NO, NO>(2 * i + 1);
+              float a[GB], b[GB];
+              read_scales<GB>(a, reinterpret_cast<const float*>(vs + (32 * x + 16 * (e0 >> 2) + 4 * g + (e0 & 3)) * VSC) + k0);
+              read_scales<GB>(b, reinterpret_cast<const float*>(vs + (32 * x + 16 * (e1 >> 2) + 4 * g + (e1 & 3)) * VSC) + k0);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int k = 0; k < GB; ++k)
+                  // 0 times whatever the scale of a token that is not seen holds is 0
+                  w[mt][k][i] = pack_bf16(mul_legacy(s[mt][2 * x + (e0 >> 2)][e0 & 3], a[k]),
+                                          mul_legacy(s[mt][2 * x + (e1 >> 2)][e1 & 3], b[k]));
+            }
+#pragma unroll
+            for (int e = 0; e < GB * BD; ++e) {
+              const bf16x8 v = __builtin_bit_cast(bf16x8, decode8<GRID, false, false>((uint32_t)vc[e][x], 1.0f));
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+                o[mt][BD * k0 + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    v, __builtin_bit_cast(bf16x8, w[mt][e / BD]), o[mt][BD * k0 + e], 0, 0, 0);
             }
           }
         }
@@ -751,7 +815,7 @@ __global__ __launch_bounds__(kThreads, MT == 2 && NB == 4 ? 1 : 2) void k_kv_att
     }
     wait_copies();
 
-    // the waves' parts, one after another into `rows`
+    // every wave's part, [16 MT][QP] each, and what a row's parts come to
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       l[mt] = query_sum(l[mt]);
@@ -760,56 +824,48 @@ __global__ __launch_bounds__(kThreads, MT == 2 && NB == 4 ? 1 : 2) void k_kv_att
         stat[1][wave][16 * mt + li] = l[mt];
       }
     }
-    __syncthreads();   // and all steps are done with the buffers
+    __syncthreads();   // all steps are done with the buffers
+    float* parts = reinterpret_cast<float*>(lds);
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stat[0][w][16 * mt + li]);
-      const float fac = l[mt] == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(m[mt] - top);
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int d = 0; d < 2 * NB; ++d)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[mt][d][r] = l[mt] == 0.0f ? 0.0f : o[mt][d][r] * fac;
-    }
-    for (int w = 0; w < kWaves; ++w) {
-      if (w == wave) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int d = 0; d < 2 * NB; ++d) {
-            f32x4* to = reinterpret_cast<f32x4*>(rows + (16 * mt + li) * QP + 16 * d + 4 * g);
-            *to = w ? *to + o[mt][d] : o[mt][d];
-          }
-      }
-      __syncthreads();
-    }
+        *reinterpret_cast<f32x4*>(parts + (wave * 16 * MT + 16 * mt + li) * QP + 16 * d + 4 * g) = o[mt][d];
+    __syncthreads();
     const bool whole = first == 0 && count == (int)q.units;
     float* part = p.partial + (int64_t)(2 * blockIdx.x + (leading ? 0 : 1)) * (16 * MT) * (D + 2);
-    for (int r = wave; r < 16 * MT; r += kWaves) {
-      const int64_t at = r0 + r;
-      if (at >= nrows) break;
-      float top = -INFINITY, sum = 0.0f;
+    constexpr int PER = 16 * MT / kWaves;   // rows of a wave
+    float ya[PER], yb[PER], top[PER], sum[PER];
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) top = fmaxf(top, stat[0][w][r]);
+    for (int k = 0; k < PER; ++k) {
+      const int r = wave + k * kWaves;
+      top[k] = -INFINITY;
+      ya[k] = yb[k] = sum[k] = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) top[k] = fmaxf(top[k], stat[0][w][r]);
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) {
         const float lw = stat[1][w][r];
-        if (lw != 0.0f) sum += lw * __builtin_amdgcn_exp2f(stat[0][w][r] - top);
+        if (lw == 0.0f) continue;   // saw nothing
+        const float fac = __builtin_amdgcn_exp2f(stat[0][w][r] - top[k]);
+        sum[k] += lw * fac;
+        if (2 * lane < DP) {
+          const f32x2 x = *reinterpret_cast<const f32x2*>(parts + (w * 16 * MT + r) * QP + 2 * lane);
+          ya[k] += x[0] * fac;
+          yb[k] += x[1] * fac;
+        }
       }
-      float a = 0.0f, b = 0.0f;
-      if (2 * lane < D) {
-        const f32x2 x = *reinterpret_cast<const f32x2*>(rows + r * QP + 2 * lane);
-        a = x[0];
-        b = x[1];
-      }
-      if (whole) {
-        const int64_t i = at / p.group;
-        store_row(p, a, b, sum, q.row0 + i, hk * p.group + (int)(at - i * p.group), lane);
-      } else {
+    }
+    if (whole) {
+      store_rows<PER>(p, ya, yb, sum, q.row0, r0 + wave, nrows, hk, lane);
+    } else {
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const int r = wave + k * kWaves;
+        if (r0 + r >= nrows) continue;
         float* to = part + (int64_t)r * (D + 2);
-        if (2 * lane < D) *reinterpret_cast<f32x2*>(to + 2 * lane) = f32x2{a, b};
-        if (lane == 0) *reinterpret_cast<f32x2*>(to + D) = f32x2{top, sum};
+        if (2 * lane < D) *reinterpret_cast<f32x2*>(to + 2 * lane) = f32x2{ya[k], yb[k]};
+        if (lane == 0) *reinterpret_cast<f32x2*>(to + D) = f32x2{top[k], sum[k]};
       }
     }
   }
@@ -822,7 +878,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_join(KvAttn p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int w = blockIdx.x + 1, D = p.at.D;
   Found f;
-  const int64_t quota = plan(p, p.groups, w, plan_lds, f);
+  const int64_t quota = plan(p, kKvGroups, w, plan_lds, f);
   if (f.b >= p.at.B) return;
   const Seq q = sequence(p, f.b);
   const int64_t u = (int64_t)w * quota, item = (u - f.before) / (q.units + kItem);
@@ -871,16 +927,16 @@ __global__ __launch_bounds__(kThreads) void k_kv_join(KvAttn p) {
   }
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) l += __shfl_xor(l, d);
-  const int64_t i = at / p.group;
-  store_row(p, a, b, l, q.row0 + i, hk * p.group + (int)(at - i * p.group), lane);
+  float ya[1] = {a}, yb[1] = {b}, yl[1] = {l};
+  store_rows<1>(p, ya, yb, yl, q.row0, at, nrows, hk, lane);
 }
 
 template <int GRID, int KIND, int NB, int MT>
 void launch_nb(const KvAttn& p, hipStream_t s) {
   if (p.at.D == 32 * NB && p.at.page_shift >= 6)
-    k_kv_attn<GRID, KIND, NB, MT, true><<<(unsigned)p.groups, kThreads, 0, s>>>(p);
+    k_kv_attn<GRID, KIND, NB, MT, true><<<kKvGroups, kThreads, 0, s>>>(p);
   else
-    k_kv_attn<GRID, KIND, NB, MT, false><<<(unsigned)p.groups, kThreads, 0, s>>>(p);
+    k_kv_attn<GRID, KIND, NB, MT, false><<<kKvGroups, kThreads, 0, s>>>(p);
 }
 
 template <int GRID, int KIND>
@@ -916,15 +972,13 @@ int64_t kv_attn_workspace(int64_t T, int32_t B, int32_t heads, int32_t kv_heads,
   return (int64_t)2 * kKvGroups * 16 * kv_attn_rows16(T, B, heads / kv_heads) * (D + 2) * 4;
 }
 
-hipError_t launch_kv_attn(const KvAttn& args, hipStream_t s) {
-  KvAttn p = args;
-  p.groups = p.rows16 == 2 && p.at.D > 64 ? kKvGroups / 2 : kKvGroups;   // one workgroup fits a compute unit, or two
+hipError_t launch_kv_attn(const KvAttn& p, hipStream_t s) {
   switch (p.grid) {
     case 0: launch_grid<0>(p, s); break;
     case 1: launch_grid<1>(p, s); break;
     default: launch_grid<2>(p, s); break;
   }
-  k_kv_join<<<dim3((unsigned)p.groups - 1, 4 * (unsigned)p.rows16), kThreads, 0, s>>>(p);
+  k_kv_join<<<dim3(kKvGroups - 1, 4 * (unsigned)p.rows16), kThreads, 0, s>>>(p);
   return hipGetLastError();
 }
 
