@@ -194,8 +194,22 @@ def _check(fn, st):
 
 def _stream(t: Optional[torch.Tensor] = None):
     if t is not None and t.is_cuda:
-        return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _call(name, t, *args):
+    """The library's function `name` with the current stream of t's device behind its
+    arguments, on that device."""
+    fn, dev = getattr(_lib(), name), t.get_device()
+    if dev < 0 or dev == torch._C._cuda_getDevice():   # an empty tensor may lie anywhere
+        dev = torch._C._cuda_getDevice()
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if st != UFP4_OK:
+        raise UFP4Error(name, st)
 
 
 def _ptr(t):
@@ -796,27 +810,30 @@ def ufp4_moe_tokens(x: torch.Tensor, logits: torch.Tensor, wg: QTensor, wu: QTen
 def _check_heads(name, t, shape=None, device=None):
     """A bfloat16 tensor [rows, heads, D] whose row holds its heads one after
     another; returns its row pitch."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.dtype != torch.bfloat16:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 3:
         raise ValueError(f"{name} must be a 3-D bfloat16 tensor [rows, heads, D]")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, needs {tuple(shape)}")
-    rows, heads, D = t.shape
+    size = t.shape
+    if shape is not None and size != shape:
+        raise ValueError(f"{name} has shape {tuple(size)}, needs {tuple(shape)}")
+    rows, heads, D = size
     if heads < 1 or D < 1:
         raise ValueError(f"{name} has no heads or no elements in a head")
-    if rows and ((D > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != D)):
+    pitch, by_head, by_elem = t.stride()
+    if rows and ((D > 1 and by_elem != 1) or (heads > 1 and by_head != D)):
         raise ValueError(f"{name}: the heads of a row must lie one after another")
-    if rows > 1 and t.stride(0) < heads * D:
-        raise ValueError(f"{name} row pitch {t.stride(0)} is below its {heads * D} elements")
+    if rows > 1 and pitch < heads * D:
+        raise ValueError(f"{name} row pitch {pitch} is below its {heads * D} elements")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    return t.stride(0) if rows > 1 else (heads * D + 7) // 8 * 8
+    return pitch if rows > 1 else (heads * D + 7) // 8 * 8
 
 
 def _check_starts(starts, device):
     if not isinstance(starts, torch.Tensor) or starts.dim() != 1 or starts.shape[0] < 1:
         raise ValueError("starts must be a 1-D int32 tensor of one more elements than sequences")
-    _check_vector("starts", starts, starts.shape[0], torch.int32, device)
-    return starts.shape[0] - 1
+    n = starts.shape[0]
+    _check_vector("starts", starts, n, torch.int32, device)
+    return n - 1
 
 
 def _attn_inputs(q, k, v, starts, scale):
@@ -844,17 +861,18 @@ def ufp4_attn_fwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: tor
     dev = q.device
     if out is None:
         out = torch.empty((T, heads, D), dtype=torch.bfloat16, device=dev)
-    ldo = _check_heads("out", out, q.shape, dev)
+        ldo = heads * D
+    else:
+        ldo = _check_heads("out", out, q.shape, dev)
     if lse is True:
         lse = torch.empty((T, heads), dtype=torch.float32, device=dev)
     elif lse is False:
         lse = None
-    if lse is not None:
+    else:
         _check_buffer("lse", lse, torch.float32, T * heads, dev)
     _on_gpu(q, "q")
-    st = _lib().ufp4_attn_fwd(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(starts), B, T, heads,
-                              kv_heads, D, scale, _ptr(out), ldo, _ptr(lse), _stream(q))
-    _check("ufp4_attn_fwd", st)
+    _call("ufp4_attn_fwd", q, q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
+          starts.data_ptr(), B, T, heads, kv_heads, D, scale, out.data_ptr(), ldo, _ptr(lse))
     return out, lse
 
 
@@ -885,11 +903,10 @@ def ufp4_attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: tor
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
         _check_buffer("workspace", workspace, torch.uint8, need, dev)
-    st = _lib().ufp4_attn_bwd(_ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(starts), B, T, heads,
-                              kv_heads, D, scale, _ptr(o), ldo, _ptr(lse), _ptr(dout), lddo,
-                              _ptr(dq), lddq, _ptr(dk), lddk, _ptr(dv), lddv, _ptr(workspace),
-                              workspace.numel(), _stream(q))
-    _check("ufp4_attn_bwd", st)
+    _call("ufp4_attn_bwd", q, q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv,
+          starts.data_ptr(), B, T, heads, kv_heads, D, scale, o.data_ptr(), ldo, _ptr(lse),
+          dout.data_ptr(), lddo, dq.data_ptr(), lddq, dk.data_ptr(), lddk, dv.data_ptr(), lddv,
+          workspace.data_ptr(), workspace.numel())
     return dq, dk, dv
 
 
@@ -916,16 +933,18 @@ class KVCache:
         """(pages, kv_heads, page_tokens, D), after checking the buffers against each other."""
         if not isinstance(self.k_codes, torch.Tensor) or self.k_codes.dim() != 4:
             raise ValueError("k_codes must be a 4-D uint8 tensor [pages, kv_heads, page_tokens, D / 2]")
-        pages, heads, page, half = self.k_codes.shape
+        size = self.k_codes.shape
+        pages, heads, page, half = size
         dev, block = self.k_codes.device, max(1, self.cfg.block_cols)
         if half < 1 or (2 * half) % block:
             raise ValueError(f"a head of {2 * half} elements does not hold whole blocks of {block}")
-        for name, t, dt, n in (("k_codes", self.k_codes, torch.uint8, half),
-                               ("v_codes", self.v_codes, torch.uint8, half),
-                               ("k_scales", self.k_scales, scales_dtype(self.cfg), 2 * half // block),
-                               ("v_scales", self.v_scales, scales_dtype(self.cfg), 2 * half // block)):
-            if not isinstance(t, torch.Tensor) or t.dtype != dt or t.shape != (pages, heads, page, n):
-                raise ValueError(f"{name} must be a {dt} tensor of shape ({pages}, {heads}, {page}, {n})")
+        scale, blocks = scales_dtype(self.cfg), (pages, heads, page, 2 * half // block)
+        for name, t, dt, n in (("k_codes", self.k_codes, torch.uint8, size),
+                               ("v_codes", self.v_codes, torch.uint8, size),
+                               ("k_scales", self.k_scales, scale, blocks),
+                               ("v_scales", self.v_scales, scale, blocks)):
+            if not isinstance(t, torch.Tensor) or t.dtype != dt or t.shape != n:
+                raise ValueError(f"{name} must be a {dt} tensor of shape {tuple(n)}")
             if not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
             if t.device != dev:
@@ -970,9 +989,8 @@ def ufp4_kv_write(k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor, lens: 
     ldk = _check_heads("k", k, (T, c.kv_heads, c.D), dev)
     ldv = _check_heads("v", v, (T, c.kv_heads, c.D), dev)
     _on_gpu(k, "k")
-    st = _lib().ufp4_kv_write(_ptr(k), ldk, _ptr(v), ldv, _ptr(starts), B, T, _ptr(lens),
-                              _ptr(table), ldt, width, ctypes.byref(c), _stream(k))
-    _check("ufp4_kv_write", st)
+    _call("ufp4_kv_write", k, k.data_ptr(), ldk, v.data_ptr(), ldv, starts.data_ptr(), B, T,
+          lens.data_ptr(), table.data_ptr(), ldt, width, ctypes.byref(c))
 
 
 def ufp4_kv_read(cache: KVCache, starts: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
@@ -984,13 +1002,15 @@ def ufp4_kv_read(cache: KVCache, starts: torch.Tensor, lens: torch.Tensor, table
     c, dev, B, ldt, width = _cache_places(cache, starts, lens, table)
     shape = (int(T), c.kv_heads, c.D)
     if out is None:
-        out = tuple(torch.empty(shape, dtype=torch.bfloat16, device=dev) for _ in range(2))
-    k, v = out
-    ldk, ldv = _check_heads("k", k, shape, dev), _check_heads("v", v, shape, dev)
+        k = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        v = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        ldk = ldv = c.kv_heads * c.D
+    else:
+        k, v = out
+        ldk, ldv = _check_heads("k", k, shape, dev), _check_heads("v", v, shape, dev)
     _on_gpu(k, "k")
-    st = _lib().ufp4_kv_read(ctypes.byref(c), _ptr(starts), B, shape[0], _ptr(lens), _ptr(table),
-                             ldt, width, _ptr(k), ldk, _ptr(v), ldv, _stream(k))
-    _check("ufp4_kv_read", st)
+    _call("ufp4_kv_read", k, ctypes.byref(c), starts.data_ptr(), B, shape[0], lens.data_ptr(),
+          table.data_ptr(), ldt, width, k.data_ptr(), ldk, v.data_ptr(), ldv)
     return k, v
 
 
@@ -1012,17 +1032,18 @@ def ufp4_kv_attn(q: torch.Tensor, starts: torch.Tensor, lens: torch.Tensor, tabl
         raise ValueError(f"q has {heads} heads of {D}, the cache {c.kv_heads} of {c.D}")
     if out is None:
         out = torch.empty((T, heads, D), dtype=torch.bfloat16, device=dev)
-    ldo = _check_heads("out", out, q.shape, dev)
+        ldo = heads * D
+    else:
+        ldo = _check_heads("out", out, q.shape, dev)
     _on_gpu(q, "q")
-    need = ufp4_kv_attn_workspace_bytes(T, B, heads, c.kv_heads, D)
+    need = _lib().ufp4_kv_attn_workspace_bytes(T, B, heads, c.kv_heads, D)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
         _check_buffer("workspace", workspace, torch.uint8, need, dev)
-    st = _lib().ufp4_kv_attn(_ptr(q), ldq, _ptr(starts), B, T, heads, _ptr(lens), _ptr(table), ldt,
-                             width, ctypes.byref(c), D ** -0.5 if scale is None else float(scale),
-                             _ptr(out), ldo, _ptr(workspace), workspace.numel(), _stream(q))
-    _check("ufp4_kv_attn", st)
+    _call("ufp4_kv_attn", q, q.data_ptr(), ldq, starts.data_ptr(), B, T, heads, lens.data_ptr(),
+          table.data_ptr(), ldt, width, ctypes.byref(c), D ** -0.5 if scale is None else
+          float(scale), out.data_ptr(), ldo, workspace.data_ptr(), workspace.numel())
     return out
 
 

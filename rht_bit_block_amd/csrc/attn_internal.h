@@ -55,6 +55,7 @@ struct KvRows {            // write and read
   uint32_t sign_pat[4];    // as QuantLaunch
   float cn;
   int32_t n, grid, scale_mode, bc;
+  int32_t items;           // heads of k and v that a lane takes one after another (set by the launcher)
   // what the quantizer's lane function asks of its launch
   float* rotated;          // null
   float tmul;              // 1

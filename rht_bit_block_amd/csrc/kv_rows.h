@@ -19,6 +19,7 @@ namespace ufp4 {
 namespace kv {
 
 constexpr int kThreads = 256;
+constexpr int kFull = 1024;     // workgroups that fill the chip
 constexpr int kSeqLds = 1024;   // starts kept in LDS while a workgroup looks for its rows' sequences
 
 // Where packed row t lies in the cache, as page and row of a page; page < 0: nowhere,
@@ -73,52 +74,85 @@ __device__ __forceinline__ uint64_t cache_row(const KvPlace& a, const Where& w, 
   return (((uint64_t)w.page * a.kv_heads + h) << a.page_shift) + w.row;
 }
 
-// blockIdx.y: head; blockIdx.z: k or v.  segs: W-element segments of a row.
-template <int W, int B, int N, int GRID, int RND>
-__global__ __launch_bounds__(kThreads) void k_kv_write(KvRows p, FastDiv segs) {
-  __shared__ int32_t starts[kSeqLds];
-  const bool in_lds = starts_to_lds(p.at, starts);
-  constexpr int lpc = N > W ? N / W : 1;
+// The lane's place in the launch: W elements from k0 on of packed row t, of the heads of k
+// and then of v from item blockIdx.y `items` on.
+struct Lane {
+  int64_t t;
+  uint32_t k0, qpos;
+  int item, end;
+};
+template <int W, int LPC>
+__device__ __forceinline__ Lane lane_of(const KvRows& p, FastDiv segs) {
   const uint32_t id = blockIdx.x * kThreads + threadIdx.x;
-  const uint32_t qpos = id & (uint32_t)(lpc - 1);
-  const uint32_t rel = qk::fdiv_u32(id, segs), k0 = (id - rel * segs.d) * W;
-  const int64_t t = p.t0 + rel;
-  const int h = blockIdx.y;
-  const bool is_v = blockIdx.z != 0;
-  if (t >= p.at.T) return;
-  const uint16_t* src = (is_v ? p.v + t * p.ldv : p.k + t * p.ldk) +
-                        (int64_t)h * p.at.D + k0;
-  uint32_t w[W / 2];
+  const uint32_t rel = qk::fdiv_u32(id, segs);
+  Lane l;
+  l.t = p.t0 + rel;
+  l.k0 = (id - rel * segs.d) * W;
+  l.qpos = id & (uint32_t)(LPC - 1);
+  l.item = (int)blockIdx.y * p.items;
+  l.end = min(l.item + p.items, 2 * p.at.kv_heads);
+  return l;
+}
+
+// W elements of an item of a packed row.
+template <int W>
+__device__ __forceinline__ void load_row(const KvRows& p, const Lane& l, int item, uint32_t (&w)[W / 2]) {
+  const bool is_v = item >= p.at.kv_heads;
+  const int h = is_v ? item - p.at.kv_heads : item;
+  const uint16_t* src = (is_v ? p.v + l.t * p.ldv : p.k + l.t * p.ldk) + (int64_t)h * p.at.D + l.k0;
 #pragma unroll
   for (int i = 0; i < W / 8; ++i) {
     const uint4 x = qk::ld16(reinterpret_cast<const uint4*>(src) + i);
     w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
   }
-  const Where at = locate(p.at, starts, in_lds, t);
-  if (at.page < 0) return;   // a whole row: the lanes of a rotation stay together
-  uint32_t pm[W / 2];
-  qk::sign_masks<W>(qk::select_pattern(p, qpos), pm);
-  float y[W];
-  qk::unpack<W>(w, pm, y);
-  const uint32_t sig = qk::fwht<W, N>(y, (qpos & 1u) ? 0x80000000u : 0u,
-                                      (qpos & 2u) ? 0x80000000u : 0u, false);
-  const uint64_t row = cache_row(p.at, at, h);
-  uint8_t* codes = is_v ? p.codes[1] : p.codes[0];
-  void* scales = is_v ? p.scales[1] : p.scales[0];
-  qk::finish_lane<W, B, N, GRID, RND, KvRows>(
-      y, sig, p, 0, codes + (row * p.at.D + k0) / 2,
-      qk::scale_at<RND>(scales, row * (uint32_t)(p.at.D / B) + k0 / B));
 }
 
-// Launches `kernel` over all rows, 2^30 lanes of a head at a time.
+template <int W, int B, int N, int GRID, int RND>
+__global__ __launch_bounds__(kThreads) void k_kv_write(KvRows p, FastDiv segs) {
+  __shared__ int32_t starts[kSeqLds];
+  constexpr int lpc = N > W ? N / W : 1;
+  const Lane l = lane_of<W, lpc>(p, segs);
+  // the first item is on its way while the row's place is looked up, the next one while
+  // an item is quantized
+  uint32_t w[W / 2];
+  if (l.t < p.at.T) load_row<W>(p, l, l.item, w);
+  const bool in_lds = starts_to_lds(p.at, starts);
+  const Where at = locate(p.at, starts, in_lds, l.t);
+  if (at.page < 0) return;   // a whole row: the lanes of a rotation stay together
+  uint32_t pm[W / 2];
+  qk::sign_masks<W>(qk::select_pattern(p, l.qpos), pm);
+  for (int item = l.item; item < l.end; ++item) {
+    float y[W];
+    qk::unpack<W>(w, pm, y);
+    if (item + 1 < l.end) load_row<W>(p, l, item + 1, w);
+    const uint32_t sig = qk::fwht<W, N>(y, (l.qpos & 1u) ? 0x80000000u : 0u,
+                                        (l.qpos & 2u) ? 0x80000000u : 0u, false);
+    const bool is_v = item >= p.at.kv_heads;
+    const uint64_t row = cache_row(p.at, at, is_v ? item - p.at.kv_heads : item);
+    uint8_t* codes = is_v ? p.codes[1] : p.codes[0];
+    void* scales = is_v ? p.scales[1] : p.scales[0];
+    qk::finish_lane<W, B, N, GRID, RND, KvRows>(
+        y, sig, p, 0, codes + (row * p.at.D + l.k0) / 2,
+        qk::scale_at<RND>(scales, row * (uint32_t)(p.at.D / B) + l.k0 / B));
+  }
+}
+
+// Launches `kernel` over all rows, 2^30 lanes at a time.  A lane takes several items (heads
+// of k and v) of its row where there are rows enough to fill the chip without: looking
+// up the row's place is four dependent loads.
 template <class K>
 hipError_t over_rows(K kernel, const KvRows& p, int W, hipStream_t s) {
   const int64_t per_row = p.at.D / W, slice = ((int64_t)1 << 30) / per_row;
   KvRows q = p;
+  const int all = 2 * p.at.kv_heads;
+  const int64_t blocks = (p.at.T * per_row + kThreads - 1) / kThreads;
+  const int64_t each = blocks * all / kFull;
+  q.items = each < 1 ? 1 : each > all ? all : (int)each;
+  const unsigned split = (unsigned)((all + q.items - 1) / q.items);
   for (q.t0 = 0; q.t0 < p.at.T; q.t0 += slice) {
     const int64_t rows = p.at.T - q.t0 < slice ? p.at.T - q.t0 : slice;
-    kernel<<<dim3((unsigned)((rows * per_row + kThreads - 1) / kThreads), (unsigned)p.at.kv_heads, 2),
-             kThreads, 0, s>>>(q, make_fastdiv((uint32_t)per_row));
+    kernel<<<dim3((unsigned)((rows * per_row + kThreads - 1) / kThreads), split), kThreads, 0, s>>>(
+        q, make_fastdiv((uint32_t)per_row));
   }
   return hipGetLastError();
 }

@@ -28,57 +28,72 @@ __device__ __forceinline__ void levels8(uint32_t c, float* y) {
   }
 }
 
+// Codes and scales of W elements of an item's row.
+template <int W, int B, bool E8>
+__device__ __forceinline__ void load_codes(const KvRows& p, const Lane& l, const Where& at, int item,
+                                           uint32_t (&c)[W / 8], float (&s)[W / B]) {
+  const bool is_v = item >= p.at.kv_heads;
+  const uint64_t row = cache_row(p.at, at, is_v ? item - p.at.kv_heads : item);
+  const uint32_t* codes =
+      reinterpret_cast<const uint32_t*>((is_v ? p.codes[1] : p.codes[0]) + (row * p.at.D + l.k0) / 2);
+  const uint64_t s0 = row * (uint32_t)(p.at.D / B) + l.k0 / B;
+  const void* scales = is_v ? p.scales[1] : p.scales[0];
+#pragma unroll
+  for (int i = 0; i < W / 8; ++i) c[i] = codes[i];
+#pragma unroll
+  for (int b = 0; b < W / B; ++b) {
+    if constexpr (E8) s[b] = __uint_as_float(reinterpret_cast<const uint8_t*>(scales)[s0 + b]);   // still the byte
+    else s[b] = reinterpret_cast<const float*>(scales)[s0 + b];
+  }
+}
+
 template <int W, int B, int N, int GRID, bool E8>
 __global__ __launch_bounds__(kThreads) void k_kv_read(KvRows p, FastDiv segs) {
   __shared__ int32_t starts[kSeqLds];
   const bool in_lds = starts_to_lds(p.at, starts);
   constexpr int lpc = N > W ? N / W : 1;
-  const uint32_t id = blockIdx.x * kThreads + threadIdx.x;
-  const uint32_t qpos = id & (uint32_t)(lpc - 1);
-  const uint32_t rel = qk::fdiv_u32(id, segs), k0 = (id - rel * segs.d) * W;
-  const int64_t t = p.t0 + rel;
-  const int h = blockIdx.y;
-  const bool is_v = blockIdx.z != 0;
-  const Where at = locate(p.at, starts, in_lds, t);
+  const Lane l = lane_of<W, lpc>(p, segs);
+  const Where at = locate(p.at, starts, in_lds, l.t);
   if (at.seq < 0) return;
-  uint16_t* dst = (is_v ? p.v + t * p.ldv : p.k + t * p.ldk) +
-                  (int64_t)h * p.at.D + k0;
-  if (at.page < 0) {
+  uint32_t c[W / 8];
+  float s[W / B];
+  if (at.page >= 0) load_codes<W, B, E8>(p, l, at, l.item, c, s);
+  for (int item = l.item; item < l.end; ++item) {
+    const bool is_v = item >= p.at.kv_heads;
+    const int h = is_v ? item - p.at.kv_heads : item;
+    uint16_t* dst = (is_v ? p.v + l.t * p.ldv : p.k + l.t * p.ldk) + (int64_t)h * p.at.D + l.k0;
+    if (at.page < 0) {
 #pragma unroll
-    for (int i = 0; i < W / 8; ++i) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
-    return;
-  }
-  const uint64_t row = cache_row(p.at, at, h);
-  const uint32_t* codes =
-      reinterpret_cast<const uint32_t*>((is_v ? p.codes[1] : p.codes[0]) + (row * p.at.D + k0) / 2);
-  const uint64_t s0 = row * (uint32_t)(p.at.D / B) + k0 / B;
-  const void* scales = is_v ? p.scales[1] : p.scales[0];
-  float y[W];
-#pragma unroll
-  for (int i = 0; i < W / 8; ++i) levels8<GRID>(codes[i], y + 8 * i);
-#pragma unroll
-  for (int b = 0; b < W / B; ++b) {
-    float s;
-    if constexpr (E8) s = ldexpf(1.0f, (int)reinterpret_cast<const uint8_t*>(scales)[s0 + b] - 127);
-    else s = reinterpret_cast<const float*>(scales)[s0 + b];
-#pragma unroll
-    for (int i = 0; i < B; ++i) y[b * B + i] = __fmul_rn(y[b * B + i], s);
-  }
-  const uint32_t sig = qk::fwht<W, N>(y, (qpos & 1u) ? 0x80000000u : 0u,
-                                      (qpos & 2u) ? 0x80000000u : 0u, false);
-  if constexpr (N > 1) qk::scale_by<W>(y, p.cn);
-  const uint32_t pat = qk::select_pattern(p, qpos) ^ (sig ? 0xFFFFFFFFu : 0u);
-#pragma unroll
-  for (int i = 0; i < W; i += 8) {
-    u32x4 o;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int e = i + 2 * j;
-      const f32x2 v = {y[e], y[e + 1]};
-      o[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2)) ^
-             (((pat >> e) & 1u) << 15) ^ (((pat >> (e + 1)) & 1u) << 31);
+      for (int i = 0; i < W / 8; ++i) reinterpret_cast<uint4*>(dst)[i] = make_uint4(0, 0, 0, 0);
+      continue;
     }
-    *reinterpret_cast<u32x4*>(dst + i) = o;
+    float y[W];
+#pragma unroll
+    for (int i = 0; i < W / 8; ++i) levels8<GRID>(c[i], y + 8 * i);
+#pragma unroll
+    for (int b = 0; b < W / B; ++b) {
+      float f = s[b];
+      if constexpr (E8) f = ldexpf(1.0f, (int)__float_as_uint(s[b]) - 127);
+#pragma unroll
+      for (int i = 0; i < B; ++i) y[b * B + i] = __fmul_rn(y[b * B + i], f);
+    }
+    if (item + 1 < l.end) load_codes<W, B, E8>(p, l, at, item + 1, c, s);
+    const uint32_t sig = qk::fwht<W, N>(y, (l.qpos & 1u) ? 0x80000000u : 0u,
+                                        (l.qpos & 2u) ? 0x80000000u : 0u, false);
+    if constexpr (N > 1) qk::scale_by<W>(y, p.cn);
+    const uint32_t pat = qk::select_pattern(p, l.qpos) ^ (sig ? 0xFFFFFFFFu : 0u);
+#pragma unroll
+    for (int i = 0; i < W; i += 8) {
+      u32x4 o;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int e = i + 2 * j;
+        const f32x2 v = {y[e], y[e + 1]};
+        o[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2)) ^
+               (((pat >> e) & 1u) << 15) ^ (((pat >> (e + 1)) & 1u) << 31);
+      }
+      *reinterpret_cast<u32x4*>(dst + i) = o;
+    }
   }
 }
 
