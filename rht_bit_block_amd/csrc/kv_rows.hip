@@ -11,19 +11,35 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-// Levels of the eight codes of a word.
+// The eight codes of a word as fp32 levels times 2^e of `scale`, two to a conversion: E2M1
+// directly, E1M2 and INT4 by way of E4M3 bytes from tables.
 template <int GRID>
-__device__ __forceinline__ void levels8(uint32_t c, float* y) {
+__device__ __forceinline__ void levels8(uint32_t c, float scale, float* y) {
+  if constexpr (GRID == 2) {
+    f32x2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 0);
+    y[0] = v[0]; y[1] = v[1];
+    v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 1);
+    y[2] = v[0]; y[3] = v[1];
+    v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 2);
+    y[4] = v[0]; y[5] = v[1];
+    v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, scale, 3);
+    y[6] = v[0]; y[7] = v[1];
+  } else {
+    uint32_t b[2];   // of the even and of the odd nibbles
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if constexpr (GRID == 1) {
-      y[i] = (float)((int)(c << (28 - 4 * i)) >> 28);
-    } else {
-      const uint32_t m = (c >> (4 * i)) & 7u, sign = (c << (28 - 4 * i)) & 0x80000000u;
-      float v;
-      if constexpr (GRID == 0) v = 0.25f * (float)m;
-      else v = m < 4 ? 0.5f * (float)m : (float)((2u + (m & 1u)) << ((m >> 1) - 2u));
-      y[i] = __uint_as_float(__float_as_uint(v) | sign);
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t x = c >> (4 * i), low = x & 0x07070707u;
+      if constexpr (GRID == 0) {
+        b[i] = __builtin_amdgcn_perm(0x3E3C3A38u, 0x34302800u, low) | ((x << 4) & 0x80808080u);
+      } else {
+        const uint32_t pos = __builtin_amdgcn_perm(0x4E4C4A48u, 0x44403800u, low);
+        const uint32_t neg = __builtin_amdgcn_perm(0xB8C0C4C8u, 0xCACCCED0u, low);
+        b[i] = __builtin_amdgcn_perm(neg, pos, ((x >> 1) & 0x04040404u) | 0x03020100u);
+      }
+      f32x2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(b[i], scale, false);
+      y[i] = v[0]; y[2 + i] = v[1];
+      v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(b[i], scale, true);
+      y[4 + i] = v[0]; y[6 + i] = v[1];
     }
   }
 }
@@ -55,6 +71,8 @@ __global__ __launch_bounds__(kThreads) void k_kv_read(KvRows p, FastDiv segs) {
   const Lane l = lane_of<W, lpc>(p, segs);
   const Where at = locate(p.at, starts, in_lds, l.t);
   if (at.seq < 0) return;
+  uint32_t pm[W / 2];
+  qk::sign_masks<W>(qk::select_pattern(p, l.qpos), pm);
   uint32_t c[W / 8];
   float s[W / B];
   if (at.page >= 0) load_codes<W, B, E8>(p, l, at, l.item, c, s);
@@ -69,19 +87,17 @@ __global__ __launch_bounds__(kThreads) void k_kv_read(KvRows p, FastDiv segs) {
     }
     float y[W];
 #pragma unroll
-    for (int i = 0; i < W / 8; ++i) levels8<GRID>(c[i], y + 8 * i);
+    for (int i = 0; i < W / 8; ++i)   // an E8M0 byte is the exponent of the conversion's factor
+      levels8<GRID>(c[i], E8 ? __uint_as_float(__float_as_uint(s[8 * i / B]) << 23) : 1.0f, y + 8 * i);
+    if constexpr (!E8) {
 #pragma unroll
-    for (int b = 0; b < W / B; ++b) {
-      float f = s[b];
-      if constexpr (E8) f = ldexpf(1.0f, (int)__float_as_uint(s[b]) - 127);
-#pragma unroll
-      for (int i = 0; i < B; ++i) y[b * B + i] = __fmul_rn(y[b * B + i], f);
+      for (int i = 0; i < W; ++i) y[i] = __fmul_rn(y[i], s[i / B]);
     }
     if (item + 1 < l.end) load_codes<W, B, E8>(p, l, at, item + 1, c, s);
     const uint32_t sig = qk::fwht<W, N>(y, (l.qpos & 1u) ? 0x80000000u : 0u,
                                         (l.qpos & 2u) ? 0x80000000u : 0u, false);
     if constexpr (N > 1) qk::scale_by<W>(y, p.cn);
-    const uint32_t pat = qk::select_pattern(p, l.qpos) ^ (sig ? 0xFFFFFFFFu : 0u);
+    const uint32_t both = sig | (sig >> 16);   // the signs of a pair that came out negated
 #pragma unroll
     for (int i = 0; i < W; i += 8) {
       u32x4 o;
@@ -89,8 +105,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_read(KvRows p, FastDiv segs) {
       for (int j = 0; j < 4; ++j) {
         const int e = i + 2 * j;
         const f32x2 v = {y[e], y[e + 1]};
-        o[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2)) ^
-               (((pat >> e) & 1u) << 15) ^ (((pat >> (e + 1)) & 1u) << 31);
+        o[j] = __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2)) ^ pm[e / 2] ^ both;
       }
       *reinterpret_cast<u32x4*>(dst + i) = o;
     }
