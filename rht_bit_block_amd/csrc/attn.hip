@@ -22,9 +22,9 @@ namespace {
 
 using namespace attn;
 
-template <int DP>
+// DP: elements of a row in LDS; S, NB: 16- and 32-element pieces of a head in use.
+template <int DP, int S, int NB>
 __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p, int last_tile) {
-  constexpr int S = DP / 16, NB = DP / 32;
   constexpr int TILE = 64 * DP * 2;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * TILE];
   int64_t row0;
@@ -38,8 +38,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p, int last_tile
   const int qi = qw + (lane & 31);
   const uint16_t* kb = p.k + row0 * p.ldk + (int64_t)hk * p.D;
   const uint16_t* vb = p.v + row0 * p.ldv + (int64_t)hk * p.D;
-  const int keys = min(n, q0 + kAttnTile);
-  const int tiles = (keys + 63) / 64;
+  const int tiles = (min(n, q0 + kAttnTile) + 63) / 64;
 
   TileCopy<DP, 64, 4> copy;
   copy.init(lane);
@@ -47,13 +46,22 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p, int last_tile
   copy.issue(lds0, kb, p.ldk, 0, n, p.D, wave, lane);
   copy.issue(lds0 + TILE, vb, p.ldv, 0, n, p.D, wave, lane);
   bf16x8 q[S];
-  load_rows<DP>(q, p.q + row0 * p.ldq + (int64_t)h * p.D, p.ldq, qw, n, p.D, lane);
+  load_rows<S>(q, p.q + row0 * p.ldq + (int64_t)h * p.D, p.ldq, qw, n, p.D, lane);
+  // the factor of the scores is c >= 0, its sign in q; not 0, because -inf marks a key that
+  // is not seen
+  const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);
+  if (p.scale < 0.0f) {
+#pragma unroll
+    for (int x = 0; x < S; ++x)
+      q[x] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, q[x]) ^ 0x80008000u);
+  }
+  const RowFrag<DP> rows(lane);
+  const TurnedFrag<DP> turned(lane);
 
   floatx16 o[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) o[b] = zero16();
-  float m = -INFINITY, l = 0.0f;
-  const float c = p.scale * kLog2e;
+  float m = -INFINITY, l = 0.0f;   // m: of c s
 
   for (int j = 0; j < tiles; ++j) {
     const uint8_t* kt = lds + (j & 1) * 2 * TILE;
@@ -68,32 +76,28 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p, int last_tile
     const int j0 = 64 * j;
     if (j0 > qw + 31 || qw >= n) continue;   // nothing for this wave in the tile
     floatx16 s[2] = {zero16(), zero16()};
-#pragma unroll
-    for (int x = 0; x < S; ++x)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) s[u] = mfma(frag_rows<DP>(kt, 32 * u, x, lane), q[x], s[u]);
-    reads_ahead<2 * S, 2 * S, 4>();
-    // c is the sign of the factor too: the maximum is of c s
+    {
+      auto read = [&](int i) { return rows.read(kt, 32 * (i & 1), i >> 1); };
+      Run<2 * S, 4, bf16x8> run;
+      run.begin(read);
+      run.go(read, [&](int i, const bf16x8& k) { s[i & 1] = mfma(k, q[i >> 1], s[i & 1]); });
+    }
+    auto read_v = [&](int i) { return turned.read(vt, 16 * (i / NB), 32 * (i % NB)); };
+    Run<4 * NB, 3, bf16x8> run;
+    run.begin(read_v);
     if (j0 + 63 > qw) {
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           const int key = j0 + 32 * u + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-          s[u][r] = key > qi ? -INFINITY : s[u][r] * c;
+          if (key > qi) s[u][r] = -INFINITY;
         }
-    } else {
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[u][r] *= c;
     }
-    float top = s[0][0];
+    float top = fmaxf(s[0][0], s[1][0]);
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) top = fmaxf(top, s[u][r]);
-    top = both_max(top);
+    for (int r = 1; r < 16; ++r) top = fmaxf(fmaxf(top, s[0][r]), s[1][r]);
+    top = both_max(top) * c;
     if (__any(top > m + 8.0f)) {   // also the first finite one
       const float next = top > m + 8.0f ? top : m;
       const float f = next == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - next);
@@ -104,22 +108,20 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p, int last_tile
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[b][r] *= f;
     }
+    bf16x8 w[4];
+    float sum = 0.0f;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        s[u][r] = __builtin_amdgcn_exp2f(s[u][r] - m);
-        l += s[u][r];
+        s[u][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][r], c, -m));
+        sum += s[u][r];
       }
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const bf16x8 w = frag_of(s[u], x);
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          o[b] = mfma(frag_turned<DP>(vt, 32 * u + 16 * x, 32 * b, lane), w, o[b]);
-      }
+      for (int x = 0; x < 2; ++x) w[2 * u + x] = frag_of(s[u], x);
     }
-    reads_ahead<4 * NB, 8 * NB, 4>();
+    l += sum;
+    run.go(read_v, [&](int i, const bf16x8& v) { o[i % NB] = mfma(v, w[i / NB], o[i % NB]); });
   }
   wait_vmcnt<0>();
   if (qi >= n) return;
@@ -147,8 +149,10 @@ hipError_t launch_attn_fwd(const AttnLaunch& p, hipStream_t s) {
   const int64_t tiles = p.T / kAttnTile + p.B;
   over_tiles(tiles, p.heads, [&](int t0, unsigned blocks) {
     const int last = (int)(tiles - 1) - t0;
-    if (p.D <= 64) k_attn_fwd<64><<<blocks, 256, 0, s>>>(p, last);
-    else k_attn_fwd<128><<<blocks, 256, 0, s>>>(p, last);
+    if (p.D <= 32) k_attn_fwd<64, 2, 1><<<blocks, 256, 0, s>>>(p, last);
+    else if (p.D <= 64) k_attn_fwd<64, 4, 2><<<blocks, 256, 0, s>>>(p, last);
+    else if (p.D <= 96) k_attn_fwd<128, 6, 3><<<blocks, 256, 0, s>>>(p, last);
+    else k_attn_fwd<128, 8, 4><<<blocks, 256, 0, s>>>(p, last);
   });
   return hipGetLastError();
 }

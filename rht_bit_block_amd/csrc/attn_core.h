@@ -95,7 +95,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* starts, int B, int64_t 
 // Which tile and head a workgroup takes.  All heads of a tile follow one another: the
 // sequences' tiles run from the one with the most work to the one with the least,
 // and workgroups that start late have little of it (one head after another, a head's
-// longest tiles started last: 32768 tokens 2.76 ms instead of HEADS_FIRST).  Key heads
+// longest tiles started last: 32768 tokens 2.76 ms instead of 2.33).  Key heads
 // alternate first, then the heads of a group: workgroups go to the XCDs in turn, so
 // with eight key heads each XCD keeps one of them in its cache.
 struct Share {
@@ -160,37 +160,48 @@ struct TileCopy {
   }
 };
 
-// Fragment s (16 elements of D) of 32 rows from `row0` on, rows as A's or B's rows.
+// Fragment s (16 elements of D) of 32 rows of a tile, as A's or B's rows: at(lane) is the
+// lane's part of the address, which the fragment's number changes by an exclusive or.
 template <int DP>
-__device__ __forceinline__ bf16x8 frag_rows(const uint8_t* tile, int row0, int s, int lane) {
-  return *reinterpret_cast<const bf16x8*>(
-      tile + chunk_at<DP>(row0 + (lane & 31), 2 * s + (lane >> 5)));
-}
+struct RowFrag {
+  uint32_t lane_at;
+  __device__ __forceinline__ explicit RowFrag(int lane) {
+    lane_at = chunk_at<DP>(lane & 31, lane >> 5);
+  }
+  __device__ __forceinline__ bf16x8 read(const uint8_t* tile, int row0, int s) const {
+    return *reinterpret_cast<const bf16x8*>(tile + row0 * (DP * 2) + (lane_at ^ (uint32_t)(32 * s)));
+  }
+};
 
 // The turned fragment: lane l holds column d0 + l % 32 of the sixteen rows row0 + 4
-// (l / 32) + {0 .. 3, 8 .. 11}.
+// (l / 32) + {0 .. 3, 8 .. 11} (row0 and d0 multiples of 16 and 32).
 template <int DP>
-__device__ __forceinline__ bf16x8 frag_turned(const uint8_t* tile, int row0, int d0, int lane) {
-  const int i = lane & 15;
-  const int row = row0 + 4 * (lane >> 5) + (i >> 2);
-  const int d = d0 + (lane & 16) + 4 * (i & 3);
-  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-      (lds_s16x4*)(tile + chunk_at<DP>(row, d >> 3) + 2 * (d & 7)));
-  const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-      (lds_s16x4*)(tile + chunk_at<DP>(row + 8, d >> 3) + 2 * (d & 7)));
-  typedef short s16x8 __attribute__((ext_vector_type(8)));
-  const s16x8 v = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-  return __builtin_bit_cast(bf16x8, v);
-}
+struct TurnedFrag {
+  uint32_t lane_at[2];   // of the first and of the second four rows
+  __device__ __forceinline__ explicit TurnedFrag(int lane) {
+    const int i = lane & 15, row = 4 * (lane >> 5) + (i >> 2), d = (lane & 16) + 4 * (i & 3);
+    lane_at[0] = chunk_at<DP>(row, d >> 3) + 2 * (d & 7);
+    lane_at[1] = chunk_at<DP>(row + 8, d >> 3) + 2 * (d & 7);
+  }
+  __device__ __forceinline__ bf16x8 read(const uint8_t* tile, int row0, int d0) const {
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_s16x4*)(tile + row0 * (DP * 2) + (lane_at[0] ^ (uint32_t)(2 * d0))));
+    const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_s16x4*)(tile + row0 * (DP * 2) + (lane_at[1] ^ (uint32_t)(2 * d0))));
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    const s16x8 v = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    return __builtin_bit_cast(bf16x8, v);
+  }
+};
 
 // Fragments of 32 rows straight from memory (rows past n and elements past D: 0).
-template <int DP>
-__device__ __forceinline__ void load_rows(bf16x8 (&f)[DP / 16], const uint16_t* base, int64_t ld,
+template <int S>
+__device__ __forceinline__ void load_rows(bf16x8 (&f)[S], const uint16_t* base, int64_t ld,
                                           int row0, int n, int D, int lane) {
   const int row = row0 + (lane & 31);
 #pragma unroll
-  for (int s = 0; s < DP / 16; ++s) {
+  for (int s = 0; s < S; ++s) {
     const int d = 16 * s + 8 * (lane >> 5);
     u32x4 x = {0u, 0u, 0u, 0u};
     if (row < n && d < D) x = *reinterpret_cast<const u32x4*>(base + (int64_t)row * ld + d);
@@ -209,20 +220,33 @@ __device__ __forceinline__ floatx16 mfma(const bf16x8& a, const bf16x8& b, const
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
 
-// Orders what the compiler schedules of the code before it, back to the last such call or
-// branch: AHEAD LDS reads, then each MFMA with PER more, so that a fragment is on its way
-// while the ones before it are multiplied (left alone, each read is waited for right
-// before its MFMA).
-template <int MFMAS, int READS, int AHEAD>
-__device__ __forceinline__ void reads_ahead() {
-  constexpr int PER = (READS + MFMAS - 1) / MFMAS;
-  __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+// Multiplies a run of COUNT fragments in order, each read from LDS LEAD places before its
+// MFMA: mul(i, fragment) after read(i), held in that order (left alone, the compiler
+// reads a fragment right before its MFMA and waits).  The first LEAD are read by
+// `begin`, before whatever code stands between.
+template <int COUNT, int LEAD, class F>
+struct Run {
+  F f[LEAD + 1];
+  template <class R>
+  __device__ __forceinline__ void begin(R&& read) {
 #pragma unroll
-  for (int i = 0; i < MFMAS; ++i) {
-    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-    if (AHEAD + i * PER < READS) __builtin_amdgcn_sched_group_barrier(0x100, PER, 0);
+    for (int i = 0; i < LEAD; ++i) f[i] = read(i);
   }
-}
+  template <class R, class M>
+  __device__ __forceinline__ void go(R&& read, M&& mul) {
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+      if (i + LEAD < COUNT) f[(i + LEAD) % (LEAD + 1)] = read(i + LEAD);
+      __builtin_amdgcn_sched_barrier(0);
+      mul(i, f[i % (LEAD + 1)]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+};
+
+// a b, and 0 where either is 0, whatever the other (v_mul_legacy_f32).
+extern "C" __device__ float ufp4_llvm_fmul_legacy(float, float) __asm("llvm.amdgcn.fmul.legacy");
+__device__ __forceinline__ float mul_legacy(float a, float b) { return ufp4_llvm_fmul_legacy(a, b); }
 
 __device__ __forceinline__ floatx16 zero16() {
   floatx16 z;

@@ -25,18 +25,18 @@ using namespace attn;
 // delta and lse log2(e), [heads][T], 32 rows of a head to a wave.  delta is the
 // diagonal of do o^T, by the instructions that do v^T comes from: where a query
 // has one key, o is that v and do . v - delta exactly 0.
-template <int DP>
+template <int S>
 __global__ __launch_bounds__(256) void k_attn_delta(AttnLaunch p) {
   const int lane = threadIdx.x & 63, h = blockIdx.y;
   for (int64_t t0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 32; t0 < p.T;
        t0 += (int64_t)gridDim.x * 128) {
-    bf16x8 a[DP / 16], b[DP / 16];
+    bf16x8 a[S], b[S];
     const int rows = (int)min(p.T - t0, (int64_t)32);
-    load_rows<DP>(a, p.dout + t0 * p.lddo + (int64_t)h * p.D, p.lddo, 0, rows, p.D, lane);
-    load_rows<DP>(b, p.o + t0 * p.ldo + (int64_t)h * p.D, p.ldo, 0, rows, p.D, lane);
+    load_rows<S>(a, p.dout + t0 * p.lddo + (int64_t)h * p.D, p.lddo, 0, rows, p.D, lane);
+    load_rows<S>(b, p.o + t0 * p.ldo + (int64_t)h * p.D, p.ldo, 0, rows, p.D, lane);
     floatx16 x = zero16();
 #pragma unroll
-    for (int s = 0; s < DP / 16; ++s) x = mfma(a[s], b[s], x);
+    for (int s = 0; s < S; ++s) x = mfma(a[s], b[s], x);
     // element (i, i) is register i % 4 + 4 (i / 8) of lane i or i + 32
     const int i = lane & 31;
     float d = 0.0f;
@@ -53,9 +53,8 @@ __global__ __launch_bounds__(256) void k_attn_delta(AttnLaunch p) {
 
 // dk and dv of 128 keys of one key head, 32 to a wave: two waves to a SIMD, whose
 // registers hold the sums and K; V's rows stay in LDS.
-template <int DP>
+template <int DP, int S, int NB>
 __global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first_tile) {
-  constexpr int S = DP / 16, NB = DP / 32;
   constexpr int TILE = 32 * DP * 2;
   constexpr int STAGE = 2 * TILE;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * TILE + 2 * STAGE];
@@ -68,10 +67,15 @@ __global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first_til
   const int hk = me.head;
   const int k0 = t * kAttnTile, kw = k0 + 32 * wave;
   const int key = kw + (lane & 31);
-  const float c = p.scale * kLog2e;
+  const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);   // as the forward pass
 
   bf16x8 k[S];
-  load_rows<DP>(k, p.k + row0 * p.ldk + (int64_t)hk * p.D, p.ldk, kw, n, p.D, lane);
+  load_rows<S>(k, p.k + row0 * p.ldk + (int64_t)hk * p.D, p.ldk, kw, n, p.D, lane);
+  if (p.scale < 0.0f) {
+#pragma unroll
+    for (int x = 0; x < S; ++x)
+      k[x] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, k[x]) ^ 0x80008000u);
+  }
   floatx16 dk[NB], dv[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) dk[b] = dv[b] = zero16();
@@ -96,6 +100,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first_til
                 rsrc4((wave ? p.delta : p.lw) + h * p.T + row0 + i0, 4u * (uint32_t)min(n - i0, 32)),
                 4u * lane, 0u);
   };
+  const RowFrag<DP> rows(lane);
+  const TurnedFrag<DP> turned(lane);
   const int h_end = (hk + 1) * p.group;
   int h = hk * p.group, step = 0;   // of the step in work
   issue(h, k0, 0);
@@ -112,13 +118,31 @@ __global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first_til
     if (h < h_end) issue(h, k0 + 32 * step, st ^ 1);
     if (i0 + 31 < kw || kw >= n) continue;   // every query lies before the wave's keys
     floatx16 s = zero16(), dp = zero16();
-#pragma unroll
-    for (int x = 0; x < S; ++x) {
-      s = mfma(frag_rows<DP>(qt, 0, x, lane), k[x], s);
-      dp = mfma(frag_rows<DP>(ot, 0, x, lane), frag_rows<DP>(lds, 32 * wave, x, lane), dp);
+    {
+      struct Three {
+        bf16x8 q, g, v;
+      };
+      auto read = [&](int x) {
+        return Three{rows.read(qt, 0, x), rows.read(ot, 0, x), rows.read(lds, 32 * wave, x)};
+      };
+      Run<S, 2, Three> run;
+      run.begin(read);
+      run.go(read, [&](int x, const Three& f) {
+        s = mfma(f.q, k[x], s);
+        dp = mfma(f.g, f.v, dp);
+      });
     }
-    reads_ahead<2 * S, 3 * S, 3>();
-    const bool edge = i0 < kw + 31;
+    // do for dv, q for dk, in turn
+    auto read_t = [&](int i) {
+      return turned.read((i & 1) ? qt : ot, 16 * (i / (2 * NB)), 32 * ((i >> 1) % NB));
+    };
+    Run<4 * NB, 3, bf16x8> run;
+    run.begin(read_t);
+    if (i0 < kw + 31) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (key > i0 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) s[r] = -INFINITY;
+    }
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const int at = 8 * g + 4 * (lane >> 5);
@@ -127,22 +151,16 @@ __global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first_til
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int r = 4 * g + e;
-        float w = __builtin_amdgcn_exp2f(s[r] * c - lw[e]);
-        if (edge && (key > i0 + at + e)) w = 0.0f;
-        s[r] = w;
-        dp[r] = w == 0.0f ? 0.0f : w * (dp[r] - de[e]);
+        s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c, -lw[e]));
+        dp[r] = mul_legacy(s[r], dp[r] - de[e]);   // 0 for a key that is not seen
       }
     }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const bf16x8 w = frag_of(s, x), ds = frag_of(dp, x);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        dv[b] = mfma(w, frag_turned<DP>(ot, 16 * x, 32 * b, lane), dv[b]);
-        dk[b] = mfma(ds, frag_turned<DP>(qt, 16 * x, 32 * b, lane), dk[b]);
-      }
-    }
-    reads_ahead<4 * NB, 8 * NB, 4>();
+    const bf16x8 w[2] = {frag_of(s, 0), frag_of(s, 1)}, ds[2] = {frag_of(dp, 0), frag_of(dp, 1)};
+    run.go(read_t, [&](int i, const bf16x8& f) {
+      const int x = i / (2 * NB), b = (i >> 1) % NB;
+      if (i & 1) dk[b] = mfma(ds[x], f, dk[b]);
+      else dv[b] = mfma(w[x], f, dv[b]);
+    });
   }
   wait_vmcnt<0>();
   // a lane holds element 32 b + l % 32 of keys kw + 8 (r / 4) + 4 (l / 32) + r % 4
@@ -163,9 +181,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first_til
 }
 
 // dq of 128 queries of one head, 32 to a wave.
-template <int DP>
+template <int DP, int S, int NB>
 __global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int last_tile) {
-  constexpr int S = DP / 16, NB = DP / 32;
   constexpr int TILE = 64 * DP * 2;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * TILE];
   int64_t row0;
@@ -185,11 +202,18 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int last_tile)
   copy.issue(lds0, kb, p.ldk, 0, n, p.D, wave, lane);
   copy.issue(lds0 + TILE, vb, p.ldv, 0, n, p.D, wave, lane);
   bf16x8 q[S], g[S];
-  load_rows<DP>(q, p.q + row0 * p.ldq + (int64_t)h * p.D, p.ldq, qw, n, p.D, lane);
-  load_rows<DP>(g, p.dout + row0 * p.lddo + (int64_t)h * p.D, p.lddo, qw, n, p.D, lane);
+  load_rows<S>(q, p.q + row0 * p.ldq + (int64_t)h * p.D, p.ldq, qw, n, p.D, lane);
+  load_rows<S>(g, p.dout + row0 * p.lddo + (int64_t)h * p.D, p.lddo, qw, n, p.D, lane);
   const float lw = qi < n ? p.lw[h * p.T + row0 + qi] : INFINITY;
   const float delta = qi < n ? p.delta[h * p.T + row0 + qi] : 0.0f;
-  const float c = p.scale * kLog2e;
+  const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);   // as the forward pass
+  if (p.scale < 0.0f) {
+#pragma unroll
+    for (int x = 0; x < S; ++x)
+      q[x] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, q[x]) ^ 0x80008000u);
+  }
+  const RowFrag<DP> rows(lane);
+  const TurnedFrag<DP> turned(lane);
   floatx16 dq[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) dq[b] = zero16();
@@ -210,28 +234,28 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int last_tile)
     for (int u = 0; u < 2; ++u) {
       if (j0 + 32 * u > qw + 31) continue;
       floatx16 s = zero16(), dp = zero16();
-#pragma unroll
-      for (int x = 0; x < S; ++x) {
-        s = mfma(frag_rows<DP>(kt, 32 * u, x, lane), q[x], s);
-        dp = mfma(frag_rows<DP>(vt, 32 * u, x, lane), g[x], dp);
+      {
+        auto read = [&](int i) { return rows.read((i & 1) ? vt : kt, 32 * u, i >> 1); };
+        Run<2 * S, 4, bf16x8> run;
+        run.begin(read);
+        run.go(read, [&](int i, const bf16x8& f) {
+          if (i & 1) dp = mfma(f, g[i >> 1], dp);
+          else s = mfma(f, q[i >> 1], s);
+        });
       }
-      reads_ahead<2 * S, 2 * S, 4>();
-      const bool edge = j0 + 32 * u + 31 > qw;
+      auto read_k = [&](int i) { return turned.read(kt, 32 * u + 16 * (i / NB), 32 * (i % NB)); };
+      Run<2 * NB, 3, bf16x8> run;
+      run.begin(read_k);
+      if (j0 + 32 * u + 31 > qw) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int key = j0 + 32 * u + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-        float w = __builtin_amdgcn_exp2f(s[r] * c - lw);
-        if (edge && key > qi) w = 0.0f;
-        s[r] = w == 0.0f ? 0.0f : w * (dp[r] - delta);
+        for (int r = 0; r < 16; ++r)
+          if (j0 + 32 * u + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3) > qi) s[r] = -INFINITY;
       }
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const bf16x8 ds = frag_of(s, x);
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          dq[b] = mfma(frag_turned<DP>(kt, 32 * u + 16 * x, 32 * b, lane), ds, dq[b]);
-      }
-      reads_ahead<2 * NB, 4 * NB, 4>();
+      for (int r = 0; r < 16; ++r)   // 0 for a key that is not seen
+        s[r] = mul_legacy(__builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c, -lw)), dp[r] - delta);
+      const bf16x8 ds[2] = {frag_of(s, 0), frag_of(s, 1)};
+      run.go(read_k, [&](int i, const bf16x8& f) { dq[i % NB] = mfma(f, ds[i / NB], dq[i % NB]); });
     }
   }
   wait_vmcnt<0>();
@@ -250,15 +274,15 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int last_tile)
     }
 }
 
-template <int DP>
+template <int DP, int S, int NB>
 void launch(const AttnLaunch& p, hipStream_t s) {
   const int64_t tiles = p.T / kAttnTile + p.B, rows = (p.T + 127) / 128;
-  k_attn_delta<DP><<<dim3((unsigned)(rows < (1 << 20) ? rows : 1 << 20), (unsigned)p.heads), 256, 0, s>>>(p);
+  k_attn_delta<S><<<dim3((unsigned)(rows < (1 << 20) ? rows : 1 << 20), (unsigned)p.heads), 256, 0, s>>>(p);
   over_tiles(tiles, p.kv_heads, [&](int t0, unsigned blocks) {
-    k_attn_dkv<DP><<<blocks, 256, 0, s>>>(p, t0);
+    k_attn_dkv<DP, S, NB><<<blocks, 256, 0, s>>>(p, t0);
   });
   over_tiles(tiles, p.heads, [&](int t0, unsigned blocks) {
-    k_attn_dq<DP><<<blocks, 256, 0, s>>>(p, (int)(tiles - 1) - t0);
+    k_attn_dq<DP, S, NB><<<blocks, 256, 0, s>>>(p, (int)(tiles - 1) - t0);
   });
 }
 
@@ -267,8 +291,10 @@ void launch(const AttnLaunch& p, hipStream_t s) {
 int64_t attn_workspace(int64_t T, int32_t heads) { return 2 * (int64_t)heads * T * 4; }
 
 hipError_t launch_attn_bwd(const AttnLaunch& p, hipStream_t s) {
-  if (p.D <= 64) launch<64>(p, s);
-  else launch<128>(p, s);
+  if (p.D <= 32) launch<64, 2, 1>(p, s);
+  else if (p.D <= 64) launch<64, 4, 2>(p, s);
+  else if (p.D <= 96) launch<128, 6, 3>(p, s);
+  else launch<128, 8, 4>(p, s);
   return hipGetLastError();
 }
 
