@@ -24,14 +24,13 @@ using namespace attn;
 
 // DP: elements of a row in LDS; S, NB: 16- and 32-element pieces of a head in use.
 template <int DP, int S, int NB>
-__global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p, int last_tile) {
+__global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p, int first, int tiles_in_all) {
   constexpr int TILE = 64 * DP * 2;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * TILE];
   int64_t row0;
   int n, t;
-  // the last tile of a sequence has the most keys: it goes first
   const Share me = share_of(blockIdx.x, p.kv_heads, p.group);
-  if (!find_tile(p.starts, p.B, p.T, last_tile - me.tile, row0, n, t)) return;
+  if (!find_tile<false>(p.starts, p.B, p.T, tiles_in_all, first + me.tile, row0, n, t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = me.head, hk = h / p.group;
   const int q0 = t * kAttnTile, qw = q0 + 32 * wave;   // the workgroup's and the wave's first query
@@ -148,11 +147,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p, int last_tile
 hipError_t launch_attn_fwd(const AttnLaunch& p, hipStream_t s) {
   const int64_t tiles = p.T / kAttnTile + p.B;
   over_tiles(tiles, p.heads, [&](int t0, unsigned blocks) {
-    const int last = (int)(tiles - 1) - t0;
-    if (p.D <= 32) k_attn_fwd<64, 2, 1><<<blocks, 256, 0, s>>>(p, last);
-    else if (p.D <= 64) k_attn_fwd<64, 4, 2><<<blocks, 256, 0, s>>>(p, last);
-    else if (p.D <= 96) k_attn_fwd<128, 6, 3><<<blocks, 256, 0, s>>>(p, last);
-    else k_attn_fwd<128, 8, 4><<<blocks, 256, 0, s>>>(p, last);
+    if (p.D <= 32) k_attn_fwd<64, 2, 1><<<blocks, 256, 0, s>>>(p, t0, (int)tiles);
+    else if (p.D <= 64) k_attn_fwd<64, 4, 2><<<blocks, 256, 0, s>>>(p, t0, (int)tiles);
+    else if (p.D <= 96) k_attn_fwd<128, 6, 3><<<blocks, 256, 0, s>>>(p, t0, (int)tiles);
+    else k_attn_fwd<128, 8, 4><<<blocks, 256, 0, s>>>(p, t0, (int)tiles);
   });
   return hipGetLastError();
 }

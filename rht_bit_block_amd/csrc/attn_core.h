@@ -60,12 +60,48 @@ __device__ __forceinline__ void rows_of(const int32_t* starts, int b, int64_t T,
   n = e > a ? (int)(e - a) : 0;
 }
 
-// Tile number `tile` of the sequences' tiles of kAttnTile rows, one sequence after
-// another: its sequence's first row and length, and the tile's number in it;
-// false past the last one.  The whole wave works on it, 64 sequences a step.
-__device__ __forceinline__ bool find_tile(const int32_t* starts, int B, int64_t T, int tile,
+// Tile number `x` of all sequences' tiles of kAttnTile rows, those with the most work first:
+// its sequence's first row and length, and the tile's number in it; false past the
+// last one.  A sequence of N tiles has one of each work 1 .. N (its tile t attends to t +
+// 1 tiles of keys, and is attended to from N - t of queries: FROM_END).  Up to 64
+// sequences, a lane each: of the tiles with more work than w there are sum of max(0, N -
+// w), and the work of number x is found by halving.  More sequences: one after
+// another, from the last one.
+template <bool FROM_END>
+__device__ __forceinline__ bool find_tile(const int32_t* starts, int B, int64_t T, int tiles, int x,
                                           int64_t& row0, int& n, int& t) {
   const int lane = threadIdx.x & 63;
+  if (B <= 64) {
+    int64_t r0 = 0;
+    int rows = 0;
+    if (lane < B) rows_of(starts, lane, T, r0, rows);
+    const int own = (rows + kAttnTile - 1) / kAttnTile;
+    int most = own;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) most = max(most, __shfl_xor(most, d));
+    auto beyond = [&](int w) {   // tiles with more work than w
+      int c = max(own - w, 0);
+#pragma unroll
+      for (int d = 32; d > 0; d >>= 1) c += __shfl_xor(c, d);
+      return __builtin_amdgcn_readfirstlane(c);
+    };
+    if (x >= beyond(0)) return false;
+    int lo = 0, hi = __builtin_amdgcn_readfirstlane(most);   // beyond(lo) > x >= beyond(hi)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (beyond(mid) > x) lo = mid;
+      else hi = mid;
+    }
+    // work hi: the (x - beyond(hi))-th sequence of that many tiles or more
+    uint64_t in = __ballot(own >= hi);
+    for (int skip = x - beyond(hi); skip > 0; --skip) in &= in - 1;
+    const int l = __builtin_ctzll(in);
+    t = FROM_END ? __builtin_amdgcn_readfirstlane(__shfl(own, l)) - hi : hi - 1;
+    n = __builtin_amdgcn_readfirstlane(__shfl(rows, l));
+    row0 = __builtin_amdgcn_readfirstlane(__shfl((int)r0, l));
+    return true;
+  }
+  const int tile = FROM_END ? x : tiles - 1 - x;
   int before = 0;
   for (int b0 = 0; b0 < B; b0 += 64) {
     int64_t r0 = 0;
@@ -75,8 +111,8 @@ __device__ __forceinline__ bool find_tile(const int32_t* starts, int B, int64_t 
     int upto = own;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const int x = __shfl_up(upto, d);
-      if (lane >= d) upto += x;
+      const int y = __shfl_up(upto, d);
+      if (lane >= d) upto += y;
     }
     const uint64_t past = __ballot(before + upto > tile);
     if (past) {
@@ -92,9 +128,8 @@ __device__ __forceinline__ bool find_tile(const int32_t* starts, int B, int64_t 
   return false;
 }
 
-// Which tile and head a workgroup takes.  All heads of a tile follow one another: the
-// sequences' tiles run from the one with the most work to the one with the least,
-// and workgroups that start late have little of it (one head after another, a head's
+// Which tile and head a workgroup takes.  All heads of a tile follow one another, so that
+// workgroups that start late have little work (one head after another, a head's
 // longest tiles started last: 32768 tokens 2.76 ms instead of 2.33).  Key heads
 // alternate first, then the heads of a group: workgroups go to the XCDs in turn, so
 // with eight key heads each XCD keeps one of them in its cache.

@@ -54,7 +54,7 @@ __global__ __launch_bounds__(256) void k_attn_delta(AttnLaunch p) {
 // dk and dv of 128 keys of one key head, 32 to a wave: two waves to a SIMD, whose
 // registers hold the sums and K; V's rows stay in LDS.
 template <int DP, int S, int NB>
-__global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first_tile) {
+__global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first, int tiles_in_all) {
   constexpr int TILE = 32 * DP * 2;
   constexpr int STAGE = 2 * TILE;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * TILE + 2 * STAGE];
@@ -62,7 +62,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first_til
   int64_t row0;
   int n, t;
   const Share me = share_of(blockIdx.x, p.kv_heads, 1);
-  if (!find_tile(p.starts, p.B, p.T, first_tile + me.tile, row0, n, t)) return;
+  if (!find_tile<true>(p.starts, p.B, p.T, tiles_in_all, first + me.tile, row0, n, t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int hk = me.head;
   const int k0 = t * kAttnTile, kw = k0 + 32 * wave;
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first_til
       auto read = [&](int x) {
         return Three{rows.read(qt, 0, x), rows.read(ot, 0, x), rows.read(lds, 32 * wave, x)};
       };
-      Run<S, 2, Three> run;
+      Run<S, 1, Three> run;
       run.begin(read);
       run.go(read, [&](int x, const Three& f) {
         s = mfma(f.q, k[x], s);
@@ -182,13 +182,13 @@ __global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first_til
 
 // dq of 128 queries of one head, 32 to a wave.
 template <int DP, int S, int NB>
-__global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int last_tile) {
+__global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int first, int tiles_in_all) {
   constexpr int TILE = 64 * DP * 2;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * TILE];
   int64_t row0;
   int n, t;
   const Share me = share_of(blockIdx.x, p.kv_heads, p.group);
-  if (!find_tile(p.starts, p.B, p.T, last_tile - me.tile, row0, n, t)) return;
+  if (!find_tile<false>(p.starts, p.B, p.T, tiles_in_all, first + me.tile, row0, n, t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = me.head, hk = h / p.group;
   const int q0 = t * kAttnTile, qw = q0 + 32 * wave;
@@ -279,10 +279,10 @@ void launch(const AttnLaunch& p, hipStream_t s) {
   const int64_t tiles = p.T / kAttnTile + p.B, rows = (p.T + 127) / 128;
   k_attn_delta<S><<<dim3((unsigned)(rows < (1 << 20) ? rows : 1 << 20), (unsigned)p.heads), 256, 0, s>>>(p);
   over_tiles(tiles, p.kv_heads, [&](int t0, unsigned blocks) {
-    k_attn_dkv<DP, S, NB><<<blocks, 256, 0, s>>>(p, t0);
+    k_attn_dkv<DP, S, NB><<<blocks, 256, 0, s>>>(p, t0, (int)tiles);
   });
   over_tiles(tiles, p.heads, [&](int t0, unsigned blocks) {
-    k_attn_dq<DP, S, NB><<<blocks, 256, 0, s>>>(p, (int)(tiles - 1) - t0);
+    k_attn_dq<DP, S, NB><<<blocks, 256, 0, s>>>(p, t0, (int)tiles);
   });
 }
 
