@@ -4,9 +4,10 @@
 //   dv_j = sum_i p_ij do_i         ds_ij = p_ij (do_i . v_j - delta_i)
 //   dk_j = scale sum_i ds_ij q_i   dq_i = scale sum_j ds_ij k_j
 //
-// The scores are computed again, twice: one kernel goes over the queries for
-// 128 keys and sums dk and dv, over all heads of the group, in registers; another
-// goes over the keys for 128 queries and sums dq.  Seven products instead of five,
+// The scores are computed again, twice: one kernel goes over the keys for 128 queries
+// and sums dq (and leaves their delta and lse log2(e) for the other); another goes
+// over the queries for 128 keys and sums dk and dv, over all heads of the group, in
+// registers.  Seven products instead of five,
 // but no sum is shared between workgroups: no atomics, no order that changes,
 // nothing in memory that is not an output.  p and ds are rounded to bf16 for the
 // products that they enter, half a step each in long sums.
@@ -21,35 +22,6 @@ namespace ufp4 {
 namespace {
 
 using namespace attn;
-
-// delta and lse log2(e), [heads][T], 32 rows of a head to a wave.  delta is the
-// diagonal of do o^T, by the instructions that do v^T comes from: where a query
-// has one key, o is that v and do . v - delta exactly 0.
-template <int S>
-__global__ __launch_bounds__(256) void k_attn_delta(AttnLaunch p) {
-  const int lane = threadIdx.x & 63, h = blockIdx.y;
-  for (int64_t t0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * 32; t0 < p.T;
-       t0 += (int64_t)gridDim.x * 128) {
-    bf16x8 a[S], b[S];
-    const int rows = (int)min(p.T - t0, (int64_t)32);
-    load_rows<S>(a, p.dout + t0 * p.lddo + (int64_t)h * p.D, p.lddo, 0, rows, p.D, lane);
-    load_rows<S>(b, p.o + t0 * p.ldo + (int64_t)h * p.D, p.ldo, 0, rows, p.D, lane);
-    floatx16 x = zero16();
-#pragma unroll
-    for (int s = 0; s < S; ++s) x = mfma(a[s], b[s], x);
-    // element (i, i) is register i % 4 + 4 (i / 8) of lane i or i + 32
-    const int i = lane & 31;
-    float d = 0.0f;
-#pragma unroll
-    for (int r = 0; r < 16; ++r)
-      if (i == 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) d = x[r];
-    const int64_t t = t0 + i;
-    if (((i >> 2) & 1) == (lane >> 5) && i < rows) {
-      p.delta[h * p.T + t] = d;
-      p.lw[h * p.T + t] = p.lse[t * p.heads + h] * kLog2e;
-    }
-  }
-}
 
 // dk and dv of 128 keys of one key head, 32 to a wave: two waves to a SIMD, whose
 // registers hold the sums and K; V's rows stay in LDS.
@@ -204,8 +176,28 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int first, int
   bf16x8 q[S], g[S];
   load_rows<S>(q, p.q + row0 * p.ldq + (int64_t)h * p.D, p.ldq, qw, n, p.D, lane);
   load_rows<S>(g, p.dout + row0 * p.lddo + (int64_t)h * p.D, p.lddo, qw, n, p.D, lane);
-  const float lw = qi < n ? p.lw[h * p.T + row0 + qi] : INFINITY;
-  const float delta = qi < n ? p.delta[h * p.T + row0 + qi] : 0.0f;
+  // delta is the diagonal of o do^T, by the instructions that v do^T comes from: where a
+  // query has one key, o is that v and do . v - delta exactly 0
+  float lw = INFINITY, delta = 0.0f;
+  {
+    bf16x8 o[S];
+    load_rows<S>(o, p.o + row0 * p.ldo + (int64_t)h * p.D, p.ldo, qw, n, p.D, lane);
+    floatx16 x = zero16();
+#pragma unroll
+    for (int s = 0; s < S; ++s) x = mfma(o[s], g[s], x);
+    // element (i, i) is register i % 4 + 4 (i / 8) of lane i or i + 32
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      if ((lane & 31) == 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) delta = x[r];
+    delta = both_sum(delta);
+    if (qi < n) {
+      lw = p.lse[(row0 + qi) * p.heads + h] * kLog2e;
+      if (lane < 32) {
+        p.delta[h * p.T + row0 + qi] = delta;
+        p.lw[h * p.T + row0 + qi] = lw;
+      }
+    }
+  }
   const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);   // as the forward pass
   if (p.scale < 0.0f) {
 #pragma unroll
@@ -276,13 +268,12 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int first, int
 
 template <int DP, int S, int NB>
 void launch(const AttnLaunch& p, hipStream_t s) {
-  const int64_t tiles = p.T / kAttnTile + p.B, rows = (p.T + 127) / 128;
-  k_attn_delta<S><<<dim3((unsigned)(rows < (1 << 20) ? rows : 1 << 20), (unsigned)p.heads), 256, 0, s>>>(p);
-  over_tiles(tiles, p.kv_heads, [&](int t0, unsigned blocks) {
-    k_attn_dkv<DP, S, NB><<<blocks, 256, 0, s>>>(p, t0, (int)tiles);
-  });
+  const int64_t tiles = p.T / kAttnTile + p.B;
   over_tiles(tiles, p.heads, [&](int t0, unsigned blocks) {
     k_attn_dq<DP, S, NB><<<blocks, 256, 0, s>>>(p, t0, (int)tiles);
+  });
+  over_tiles(tiles, p.kv_heads, [&](int t0, unsigned blocks) {   // reads what dq's left
+    k_attn_dkv<DP, S, NB><<<blocks, 256, 0, s>>>(p, t0, (int)tiles);
   });
 }
 

@@ -211,6 +211,19 @@ def test_later_tokens_never_matter():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("heads,kv,D", [(1, 1, 64), (6, 2, 128), (3, 3, 80), (2, 1, 24)])
+def test_a_single_key_has_no_gradient_of_scores(heads, kv, D):
+    """Sequences of one token: o = v and ds = 0, exactly."""
+    T = 37
+    starts = packed([1] * T).cuda()
+    Q, K, V, dO = (rand(T, h, D, s).cuda() for h, s in ((heads, 1), (kv, 2), (kv, 3), (heads, 4)))
+    o, lse = U.ufp4_attn_fwd(Q, K, V, starts)
+    assert torch.equal(o, V.repeat_interleave(heads // kv, 1))
+    dq, dk, dv = U.ufp4_attn_bwd(Q, K, V, starts, o, lse, dO)
+    assert not bool(dq.any()) and not bool(dk.any()) and bool(dv.any())
+
+
+@pytest.mark.gpu
 def test_many_sequences_and_one_long():
     """More sequences than a wave has lanes, and a sequence of several dozen tiles."""
     lens = [(7 * i) % 23 for i in range(150)]
