@@ -116,8 +116,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p, int first, in
         s[u][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][r], c, -m));
         sum += s[u][r];
       }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) w[2 * u + x] = frag_of(s[u], x);
+      uint32_t pairs[8];
+      round_pairs(s[u], pairs);
+      w[2 * u] = frag_of(pairs, 0);
+      w[2 * u + 1] = frag_of(pairs, 1);
     }
     l += sum;
     run.go(read_v, [&](int i, const bf16x8& v) { o[i % NB] = mfma(v, w[i / NB], o[i % NB]); });

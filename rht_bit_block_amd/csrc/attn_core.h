@@ -244,11 +244,13 @@ __device__ __forceinline__ void load_rows(bf16x8 (&f)[S], const uint16_t* base, 
   }
 }
 
-// Registers 8 t .. 8 t + 7 of a product as a fragment, rounded to bf16.
-__device__ __forceinline__ bf16x8 frag_of(const floatx16& x, int t) {
-  const u32x4 v = {pack_bf16(x[8 * t], x[8 * t + 1]), pack_bf16(x[8 * t + 2], x[8 * t + 3]),
-                   pack_bf16(x[8 * t + 4], x[8 * t + 5]), pack_bf16(x[8 * t + 6], x[8 * t + 7])};
-  return __builtin_bit_cast(bf16x8, v);
+// Registers 8 t .. 8 t + 7 of a product as a fragment, rounded to bf16: pairs w[4 t] .. w[4 t + 3].
+__device__ __forceinline__ bf16x8 frag_of(const uint32_t (&w)[8], int t) {
+  return __builtin_bit_cast(bf16x8, (u32x4{w[4 * t], w[4 * t + 1], w[4 * t + 2], w[4 * t + 3]}));
+}
+__device__ __forceinline__ void round_pairs(const floatx16& x, uint32_t (&w)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = pack_bf16(x[2 * i], x[2 * i + 1]);
 }
 
 __device__ __forceinline__ floatx16 mfma(const bf16x8& a, const bf16x8& b, const floatx16& c) {

@@ -7,7 +7,7 @@
 // The scores are computed again, twice: one kernel goes over the keys for 128 queries
 // and sums dq (and leaves their delta and lse log2(e) for the other); another goes
 // over the queries for 128 keys and sums dk and dv, over all heads of the group, in
-// registers.  Seven products instead of five,
+// registers.  Eight products instead of five,
 // but no sum is shared between workgroups: no atomics, no order that changes,
 // nothing in memory that is not an output.  p and ds are rounded to bf16 for the
 // products that they enter, half a step each in long sums.
@@ -22,6 +22,12 @@ namespace ufp4 {
 namespace {
 
 using namespace attn;
+
+// x plus both bf16 values of a pair, in fp32.
+__device__ __forceinline__ float add_pair(uint32_t pair, float x) {
+  const bf16x2 one = {(__bf16)1.0f, (__bf16)1.0f};
+  return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pair), one, x, false);
+}
 
 // dk and dv of 128 keys of one key head, 32 to a wave: two waves to a SIMD, whose
 // registers hold the sums and K; V's rows stay in LDS.
@@ -127,7 +133,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first, in
         dp[r] = mul_legacy(s[r], dp[r] - de[e]);   // 0 for a key that is not seen
       }
     }
-    const bf16x8 w[2] = {frag_of(s, 0), frag_of(s, 1)}, ds[2] = {frag_of(dp, 0), frag_of(dp, 1)};
+    uint32_t pw[8], pd[8];
+    round_pairs(s, pw);
+    round_pairs(dp, pd);
+    const bf16x8 w[2] = {frag_of(pw, 0), frag_of(pw, 1)}, ds[2] = {frag_of(pd, 0), frag_of(pd, 1)};
     run.go(read_t, [&](int i, const bf16x8& f) {
       const int x = i / (2 * NB), b = (i >> 1) % NB;
       if (i & 1) dk[b] = mfma(ds[x], f, dk[b]);
@@ -152,11 +161,18 @@ __global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first, in
   }
 }
 
-// dq of 128 queries of one head, 32 to a wave.
+// dq of 128 queries of one head, 32 to a wave.  The forward pass' o is rounded, and
+// with it delta, which enters every ds of a row: it would be the largest error of both
+// gradients (4.3e-3 of the norm, where the outputs' rounding is 1.7e-3).  But the ds
+// of a row add to 0, so that from a near delta0
+//   dq = scale (sum_j ds0_j k_j - (sum_j ds0_j) (sum_j p_j k_j))     ds0 = p (dp - delta0)
+// holds for whatever is summed: with the rounded ds0 in both sums the roundings' common
+// part goes as well (2.2e-3).  It takes one product more, on fragments of K that are
+// there.  The row's sum of the ds0 themselves is what delta lacks, for dk.
 template <int DP, int S, int NB>
 __global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int first, int tiles_in_all) {
-  constexpr int TILE = 64 * DP * 2;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * TILE];
+  constexpr int TILE = 32 * DP * 2;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[8 * TILE];
   int64_t row0;
   int n, t;
   const Share me = share_of(blockIdx.x, p.kv_heads, p.group);
@@ -167,21 +183,25 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int first, int
   const int qi = qw + (lane & 31);
   const uint16_t* kb = p.k + row0 * p.ldk + (int64_t)hk * p.D;
   const uint16_t* vb = p.v + row0 * p.ldv + (int64_t)hk * p.D;
-  const int tiles = (min(n, q0 + kAttnTile) + 63) / 64;
-  TileCopy<DP, 64, 4> copy;
+  const uint16_t* gb = p.dout + row0 * p.lddo + (int64_t)h * p.D;
+  const int tiles = (min(n, q0 + kAttnTile) + 31) / 32;
+  const uint32_t lds0 = lds_address(lds), steps0 = lds0 + 4 * TILE;
+  {
+    TileCopy<DP, 128, 4> copy;   // the rows of do
+    copy.init(lane);
+    copy.issue(lds0, gb, p.lddo, q0, n, p.D, wave, lane);
+  }
+  TileCopy<DP, 32, 4> copy;
   copy.init(lane);
-  const uint32_t lds0 = lds_address(lds);
-  copy.issue(lds0, kb, p.ldk, 0, n, p.D, wave, lane);
-  copy.issue(lds0 + TILE, vb, p.ldv, 0, n, p.D, wave, lane);
-  bf16x8 q[S], g[S];
-  load_rows<S>(q, p.q + row0 * p.ldq + (int64_t)h * p.D, p.ldq, qw, n, p.D, lane);
-  load_rows<S>(g, p.dout + row0 * p.lddo + (int64_t)h * p.D, p.lddo, qw, n, p.D, lane);
-  // delta is the diagonal of o do^T, by the instructions that v do^T comes from: where a
-  // query has one key, o is that v and do . v - delta exactly 0
+  copy.issue(steps0, kb, p.ldk, 0, n, p.D, wave, lane);
+  copy.issue(steps0 + TILE, vb, p.ldv, 0, n, p.D, wave, lane);
+  // delta0 is the diagonal of o do^T, by the instructions that v do^T comes from: where a
+  // query has one key, o is that v and do . v - delta0 exactly 0
   float lw = INFINITY, delta = 0.0f;
   {
-    bf16x8 o[S];
+    bf16x8 o[S], g[S];
     load_rows<S>(o, p.o + row0 * p.ldo + (int64_t)h * p.D, p.ldo, qw, n, p.D, lane);
+    load_rows<S>(g, gb, p.lddo, qw, n, p.D, lane);
     floatx16 x = zero16();
 #pragma unroll
     for (int s = 0; s < S; ++s) x = mfma(o[s], g[s], x);
@@ -190,14 +210,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int first, int
     for (int r = 0; r < 16; ++r)
       if ((lane & 31) == 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) delta = x[r];
     delta = both_sum(delta);
-    if (qi < n) {
-      lw = p.lse[(row0 + qi) * p.heads + h] * kLog2e;
-      if (lane < 32) {
-        p.delta[h * p.T + row0 + qi] = delta;
-        p.lw[h * p.T + row0 + qi] = lw;
-      }
-    }
+    if (qi < n) lw = p.lse[(row0 + qi) * p.heads + h] * kLog2e;
   }
+  bf16x8 q[S];
+  load_rows<S>(q, p.q + row0 * p.ldq + (int64_t)h * p.D, p.ldq, qw, n, p.D, lane);
   const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);   // as the forward pass
   if (p.scale < 0.0f) {
 #pragma unroll
@@ -206,52 +222,71 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int first, int
   }
   const RowFrag<DP> rows(lane);
   const TurnedFrag<DP> turned(lane);
-  floatx16 dq[NB];
+  floatx16 dq[NB], pk[NB];
 #pragma unroll
-  for (int b = 0; b < NB; ++b) dq[b] = zero16();
+  for (int b = 0; b < NB; ++b) dq[b] = pk[b] = zero16();
+  float lacks = 0.0f, rounded = 0.0f;   // this lane's half of the sums of ds0
 
   for (int j = 0; j < tiles; ++j) {
-    const uint8_t* kt = lds + (j & 1) * 2 * TILE;
+    const uint8_t* kt = lds + 4 * TILE + (j & 1) * 2 * TILE;
     const uint8_t* vt = kt + TILE;
     wait_vmcnt<0>();
     __syncthreads();   // tile j is there, and tile j - 1 has been read
     if (j + 1 < tiles) {
-      const uint32_t to = lds0 + ((j + 1) & 1) * 2 * TILE;
-      copy.issue(to, kb, p.ldk, 64 * (j + 1), n, p.D, wave, lane);
-      copy.issue(to + TILE, vb, p.ldv, 64 * (j + 1), n, p.D, wave, lane);
+      const uint32_t to = steps0 + ((j + 1) & 1) * 2 * TILE;
+      copy.issue(to, kb, p.ldk, 32 * (j + 1), n, p.D, wave, lane);
+      copy.issue(to + TILE, vb, p.ldv, 32 * (j + 1), n, p.D, wave, lane);
     }
-    const int j0 = 64 * j;
+    const int j0 = 32 * j;
     if (j0 > qw + 31 || qw >= n) continue;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      if (j0 + 32 * u > qw + 31) continue;
-      floatx16 s = zero16(), dp = zero16();
-      {
-        auto read = [&](int i) { return rows.read((i & 1) ? vt : kt, 32 * u, i >> 1); };
-        Run<2 * S, 4, bf16x8> run;
-        run.begin(read);
-        run.go(read, [&](int i, const bf16x8& f) {
-          if (i & 1) dp = mfma(f, g[i >> 1], dp);
-          else s = mfma(f, q[i >> 1], s);
-        });
-      }
-      auto read_k = [&](int i) { return turned.read(kt, 32 * u + 16 * (i / NB), 32 * (i % NB)); };
-      Run<2 * NB, 3, bf16x8> run;
-      run.begin(read_k);
-      if (j0 + 32 * u + 31 > qw) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r)
-          if (j0 + 32 * u + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3) > qi) s[r] = -INFINITY;
-      }
-#pragma unroll
-      for (int r = 0; r < 16; ++r)   // 0 for a key that is not seen
-        s[r] = mul_legacy(__builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c, -lw)), dp[r] - delta);
-      const bf16x8 ds[2] = {frag_of(s, 0), frag_of(s, 1)};
-      run.go(read_k, [&](int i, const bf16x8& f) { dq[i % NB] = mfma(f, ds[i / NB], dq[i % NB]); });
+    floatx16 s = zero16(), dp = zero16();
+    {
+      struct Three {
+        bf16x8 k, v, g;
+      };
+      auto read = [&](int x) {
+        return Three{rows.read(kt, 0, x), rows.read(vt, 0, x), rows.read(lds, 32 * wave, x)};
+      };
+      Run<S, 1, Three> run;
+      run.begin(read);
+      run.go(read, [&](int x, const Three& f) {
+        s = mfma(f.k, q[x], s);
+        dp = mfma(f.v, f.g, dp);
+      });
     }
+    auto read_k = [&](int i) { return turned.read(kt, 16 * (i / NB), 32 * (i % NB)); };
+    Run<2 * NB, 2, bf16x8> run;
+    run.begin(read_k);
+    if (j0 + 31 > qw) {
+#pragma unroll
+      for (int r = 0; r < 16; ++r)
+        if (j0 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3) > qi) s[r] = -INFINITY;
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      s[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[r], c, -lw));
+      dp[r] = mul_legacy(s[r], dp[r] - delta);   // 0 for a key that is not seen
+      lacks += dp[r];
+    }
+    uint32_t pw[8], pd[8];
+    round_pairs(s, pw);
+    round_pairs(dp, pd);
+    const bf16x8 w[2] = {frag_of(pw, 0), frag_of(pw, 1)}, ds[2] = {frag_of(pd, 0), frag_of(pd, 1)};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rounded = add_pair(pd[i], rounded);
+    run.go(read_k, [&](int i, const bf16x8& f) {
+      dq[i % NB] = mfma(f, ds[i / NB], dq[i % NB]);
+      pk[i % NB] = mfma(f, w[i / NB], pk[i % NB]);
+    });
   }
   wait_vmcnt<0>();
   if (qi >= n) return;
+  rounded = both_sum(rounded);
+  delta += both_sum(lacks);
+  if (lane < 32) {
+    p.delta[h * p.T + row0 + qi] = delta;
+    p.lw[h * p.T + row0 + qi] = lw;
+  }
   uint16_t* out = p.dq + (row0 + qi) * p.lddq + (int64_t)h * p.D;
 #pragma unroll
   for (int b = 0; b < NB; ++b)
@@ -259,9 +294,12 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int first, int
     for (int r = 0; r < 16; r += 4) {
       const int d = 32 * b + 2 * r + 4 * (lane >> 5);
       if (d < p.D) {
-        const u32x2 x = {pack_bf16(dq[b][r] * p.scale, dq[b][r + 1] * p.scale),
-                         pack_bf16(dq[b][r + 2] * p.scale, dq[b][r + 3] * p.scale)};
-        *reinterpret_cast<u32x2*>(out + d) = x;
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[e] = __builtin_fmaf(-rounded, pk[b][r + e], dq[b][r + e]) * p.scale;
+        const u32x2 v = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+        *reinterpret_cast<u32x2*>(out + d) = v;
       }
     }
 }
