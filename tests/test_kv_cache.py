@@ -246,6 +246,44 @@ def test_several_rows_of_a_sequence(mode, block, n, grid):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("new,heads", [(1, 10), (5, 10), (2, 40)])
+@pytest.mark.parametrize("mode,block,n", [(F32, 16, 64), (F32, 32, 1), (POW2, 32, 32)])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("grid", GRIDS)
+def test_pages_of_whole_steps(grid, D, mode, block, n, new, heads):
+    """Pages of 64 tokens and more, whose steps are copied as one run: lengths around the steps' and pages'
+    ends, a page that does not exist, one and two tiles of rows."""
+    s = Setup([new, 64, 129, 500], [new] * 4, 2, D, 128 if new == 5 else 64, make(grid, mode, block, n))
+    filled(s)
+    s.table[3, 1] = s.pages
+    check(s, rand(s.T, heads, D, 41))
+
+
+@pytest.mark.gpu
+def test_more_sequences_than_are_kept_at_hand():
+    lens = [1 + (7 * i) % 40 for i in range(1100)]
+    cfg = make(U.UFP4_E2M1, POW2, 32, 32)
+    s = Setup(lens, [1] * 1100, 1, 32, 16, cfg)
+    k, _ = filled(s)
+    first = [0] + list(np.cumsum(lens))
+    starts = torch.tensor(first, dtype=torch.int32).cuda()
+    all_rows = U.ufp4_kv_read(s.cache, starts, s.lens.cuda(), s.table.cuda(), sum(lens))
+    ref = O.quantize(bits(k.view(-1, 32)), 0, spec_of(cfg))
+    want = torch.from_numpy(ref["codes"]).view(-1, 1, 16)
+    codes = s.cache.k_codes.cpu()
+    for b in (0, 1, 63, 64, 500, 1023, 1024, 1025, 1099):   # each by itself
+        n = lens[b]
+        one = U.ufp4_kv_read(s.cache, torch.tensor([0, n], dtype=torch.int32).cuda(), s.lens[b:b + 1].cuda(),
+                             s.table[b:b + 1].cuda(), n)
+        for x, y in zip(one, all_rows):
+            assert torch.equal(x, y[first[b]:first[b] + n])
+        for t in range(n):
+            page, at = s.slot(b, t)
+            assert torch.equal(codes[page, :, at], want[first[b] + t])
+    check(s, rand(s.T, 2, 32, 42))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("kv,lens", [(1, [5000]), (2, [1, 3000, 7, 64 * 17]), (8, [650, 2])])
 def test_split_and_joined(kv, lens):
     """Long sequences cut among many workgroups, short ones beside them."""
