@@ -57,6 +57,8 @@ void attn_fill(AttnLaunch& p, const void* q, int64_t ldq, const void* k, int64_t
   p.kv_heads = kv_heads;
   p.group = heads / kv_heads;
   p.D = D;
+  p.by_heads = make_fastdiv((uint32_t)heads);
+  p.by_kv_heads = make_fastdiv((uint32_t)kv_heads);
   p.scale = scale;
 }
 

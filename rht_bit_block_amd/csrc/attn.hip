@@ -29,10 +29,10 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p, int first, in
   __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * TILE];
   int64_t row0;
   int n, t;
-  const Share me = share_of(blockIdx.x, p.kv_heads, p.group);
+  const Share me = share_of(blockIdx.x, p.by_heads, p.by_kv_heads, p.group);
   if (!find_tile<false>(p.starts, p.B, p.T, tiles_in_all, first + me.tile, row0, n, t)) return;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int h = me.head, hk = h / p.group;
+  const int h = me.head, hk = me.kv_head;
   const int q0 = t * kAttnTile, qw = q0 + 32 * wave;   // the workgroup's and the wave's first query
   const int qi = qw + (lane & 31);
   const uint16_t* kb = p.k + row0 * p.ldk + (int64_t)hk * p.D;

@@ -65,8 +65,8 @@ __device__ __forceinline__ void rows_of(const int32_t* starts, int b, int64_t T,
 // last one.  A sequence of N tiles has one of each work 1 .. N (its tile t attends to t +
 // 1 tiles of keys, and is attended to from N - t of queries: FROM_END).  Up to 64
 // sequences, a lane each: of the tiles with more work than w there are sum of max(0, N -
-// w), and the work of number x is found by halving.  More sequences: one after
-// another, from the last one.
+// w), and the work of number x is found by trying 64 w at once, a lane each.  More
+// sequences: one after another, from the last one.
 template <bool FROM_END>
 __device__ __forceinline__ bool find_tile(const int32_t* starts, int B, int64_t T, int tiles, int x,
                                           int64_t& row0, int& n, int& t) {
@@ -76,29 +76,31 @@ __device__ __forceinline__ bool find_tile(const int32_t* starts, int B, int64_t 
     int rows = 0;
     if (lane < B) rows_of(starts, lane, T, r0, rows);
     const int own = (rows + kAttnTile - 1) / kAttnTile;
-    int most = own;
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) most = max(most, __shfl_xor(most, d));
-    auto beyond = [&](int w) {   // tiles with more work than w
-      int c = max(own - w, 0);
-#pragma unroll
-      for (int d = 32; d > 0; d >>= 1) c += __shfl_xor(c, d);
-      return __builtin_amdgcn_readfirstlane(c);
-    };
-    if (x >= beyond(0)) return false;
-    int lo = 0, hi = __builtin_amdgcn_readfirstlane(most);   // beyond(lo) > x >= beyond(hi)
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (beyond(mid) > x) lo = mid;
-      else hi = mid;
+    int all = 0, most = 0;
+    for (int b = 0; b < B; ++b) {
+      const int N = __builtin_amdgcn_readlane(own, b);
+      all += N;
+      most = max(most, N);
     }
-    // work hi: the (x - beyond(hi))-th sequence of that many tiles or more
+    if (x >= all) return false;
+    // tiles with more work than lo: more than x; than hi: `beyond`, not more than x
+    int lo = 0, hi = most, beyond = 0;
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 63) >> 6, w = min(lo + (lane + 1) * step, hi);
+      int c = 0;
+      for (int b = 0; b < B; ++b) c += max(__builtin_amdgcn_readlane(own, b) - w, 0);
+      const int l = __builtin_ctzll(__ballot(c <= x));   // lane 63 has w = hi
+      lo += l * step;
+      hi = min(hi, lo + step);
+      beyond = __builtin_amdgcn_readlane(c, l);
+    }
+    // work hi: the (x - beyond)-th sequence of that many tiles or more
     uint64_t in = __ballot(own >= hi);
-    for (int skip = x - beyond(hi); skip > 0; --skip) in &= in - 1;
+    for (int skip = x - beyond; skip > 0; --skip) in &= in - 1;
     const int l = __builtin_ctzll(in);
-    t = FROM_END ? __builtin_amdgcn_readfirstlane(__shfl(own, l)) - hi : hi - 1;
-    n = __builtin_amdgcn_readfirstlane(__shfl(rows, l));
-    row0 = __builtin_amdgcn_readfirstlane(__shfl((int)r0, l));
+    t = FROM_END ? __builtin_amdgcn_readlane(own, l) - hi : hi - 1;
+    n = __builtin_amdgcn_readlane(rows, l);
+    row0 = __builtin_amdgcn_readlane((int)r0, l);
     return true;
   }
   const int tile = FROM_END ? x : tiles - 1 - x;
@@ -134,13 +136,15 @@ __device__ __forceinline__ bool find_tile(const int32_t* starts, int B, int64_t 
 // alternate first, then the heads of a group: workgroups go to the XCDs in turn, so
 // with eight key heads each XCD keeps one of them in its cache.
 struct Share {
-  int tile, head;
+  int tile, head, kv_head;
 };
-__device__ __forceinline__ Share share_of(uint32_t id, int kv_heads, int group) {
-  const uint32_t heads = (uint32_t)(kv_heads * group);
-  const uint32_t tile = id / heads, r = id - tile * heads;
-  const uint32_t in_group = r / (uint32_t)kv_heads;
-  return Share{(int)tile, (int)((r - in_group * kv_heads) * group + in_group)};
+__device__ __forceinline__ uint32_t over(uint32_t x, FastDiv f) {
+  return (uint32_t)(((uint64_t)__umulhi(x, f.m) + x) >> f.l);
+}
+__device__ __forceinline__ Share share_of(uint32_t id, FastDiv by_heads, FastDiv by_kv, int group) {
+  const uint32_t tile = over(id, by_heads), r = id - tile * by_heads.d;
+  const uint32_t in_group = over(r, by_kv);
+  return Share{(int)tile, (int)((r - in_group * by_kv.d) * group + in_group), (int)(r - in_group * by_kv.d)};
 }
 
 // Launches over `tiles` tiles of `heads` heads, fewer than 2^24 workgroups at a time; f(first

@@ -30,6 +30,7 @@ struct AttnLaunch {
   float* delta;            // workspace: do . o, [heads][T]
   int64_t T;
   int32_t B, heads, kv_heads, group, D;
+  FastDiv by_heads, by_kv_heads;
   float scale;
 };
 int64_t attn_workspace(int64_t T, int32_t heads);
