@@ -54,6 +54,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p, int first, in
     for (int x = 0; x < S; ++x)
       q[x] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, q[x]) ^ 0x80008000u);
   }
+  arrived(q);
   const RowFrag<DP> rows(lane);
   const TurnedFrag<DP> turned(lane);
 

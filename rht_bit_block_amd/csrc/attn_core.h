@@ -248,6 +248,14 @@ __device__ __forceinline__ void load_rows(bf16x8 (&f)[S], const uint16_t* base, 
   }
 }
 
+// Waits for fragments that load_rows asked for.  Left to their first use inside a loop, the
+// compiler's wait stands there in every pass, and with it one for all copies in flight.
+template <int S>
+__device__ __forceinline__ void arrived(bf16x8 (&f)[S]) {
+#pragma unroll
+  for (int s = 0; s < S; ++s) asm volatile("" : "+v"(f[s]));
+}
+
 // Registers 8 t .. 8 t + 7 of a product as a fragment, rounded to bf16: pairs w[4 t] .. w[4 t + 3].
 __device__ __forceinline__ bf16x8 frag_of(const uint32_t (&w)[8], int t) {
   return __builtin_bit_cast(bf16x8, (u32x4{w[4 * t], w[4 * t + 1], w[4 * t + 2], w[4 * t + 3]}));

@@ -78,6 +78,7 @@ __global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first, in
                 rsrc4((wave ? p.delta : p.lw) + h * p.T + row0 + i0, 4u * (uint32_t)min(n - i0, 32)),
                 4u * lane, 0u);
   };
+  arrived(k);
   const RowFrag<DP> rows(lane);
   const TurnedFrag<DP> turned(lane);
   const int h_end = (hk + 1) * p.group;
@@ -220,6 +221,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int first, int
     for (int x = 0; x < S; ++x)
       q[x] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, q[x]) ^ 0x80008000u);
   }
+  arrived(q);
+  asm volatile("" : "+v"(lw));
   const RowFrag<DP> rows(lane);
   const TurnedFrag<DP> turned(lane);
   floatx16 dq[NB], pk[NB];
