@@ -224,6 +224,29 @@ def test_a_single_key_has_no_gradient_of_scores(heads, kv, D):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[9000, 130, 17000, 1, 0, 8300], [20011], [64 * 128, 64 * 128 + 1, 128, 127], [40 * 128] * 64, [300] * 70 + [9000, 2]])
+def test_every_tile_is_found(lens):
+    """Keys of zeros and values of ones, so that row i has lse = log(i + 1) and o = 1, and with a
+    gradient of ones dv[j] = sum over i >= j of 1 / (i + 1): p rounded to bf16, 2^-8 relative, with the
+    exponential's 2^-20, a sum of n terms, and the result's own rounding."""
+    T = sum(lens)
+    starts = packed(lens).cuda()
+    K, V = torch.zeros(T, 1, 8, dtype=torch.bfloat16, device="cuda"), torch.ones(T, 1, 8, dtype=torch.bfloat16, device="cuda")
+    o, lse = U.ufp4_attn_fwd(rand(T, 1, 8, 31).cuda(), K, V, starts, out=torch.full_like(V, 7.0), lse=torch.full((T, 1), 7.0, device="cuda"))
+    dq, dk, dv = U.ufp4_attn_bwd(K, K, V, starts, o, lse, V, out=tuple(torch.full_like(V, 7.0) for _ in range(3)))
+    i = torch.cat([torch.arange(n, dtype=torch.float64) for n in lens])
+    top = max(lens)
+    assert bool((o.cpu() == 1).all())
+    near("lse", lse[:, 0], (torch.log(i + 1), (top + 16) * EPS + 2.0 ** -20 + 4 * EPS * torch.log(i + 1)))
+    want = torch.cat([torch.flip(torch.cumsum(torch.flip(1 / torch.arange(1, n + 1, dtype=torch.float64), (0,)), 0), (0,)) for n in lens])
+    for d in (0, 7):
+        near("dv", dv[:, 0, d], (want, want * (2 * BF16 + 2.0 ** -16 + 2 * (top + 16) * EPS)))
+    assert bool((dq == 0).all())   # sums of keys that are 0
+    # q is 0 in the backward call
+    assert bool((dk == 0).all())
+
+
+@pytest.mark.gpu
 def test_many_sequences_and_one_long():
     """More sequences than a wave has lanes, and a sequence of several dozen tiles."""
     lens = [(7 * i) % 23 for i in range(150)]
