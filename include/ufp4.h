@@ -485,8 +485,9 @@ size_t ufp4_moe_tokens_workspace_bytes(int64_t T, int32_t E, int32_t top_k, int6
  *   q, o : [T][heads][D], k, v : [T][kv_heads][D];  lse : fp32 [T][heads], or
  *   NULL (no gradient wanted).
  * Products of the inputs are exact and summed in fp32, as are the weights' sums;
- * the weights e^(z - m) (m: a maximum of the row, up to 2^8 above 1) are rounded to bf16 for the second
- * product, o once at the end.  An infinity or NaN in a token may turn up in
+ * the weights e^(z - m) (m: a running maximum of the row, or up to 8 ln 2 less)
+ * are rounded to bf16 for the second product, o once at the end.  Equal inputs
+ * give equal bits.  An infinity or NaN in a token may turn up in
  * earlier tokens of the same sequence, never in another one.
  * Errors: UFP4_ERR_INVALID_ARG (negative sizes, null pointers, pitches,
  * alignment, a scale that is not finite, heads not a multiple of kv_heads),
@@ -498,13 +499,16 @@ int ufp4_attn_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const 
                   void* stream);
 
 /* Gradients of ufp4_attn_fwd: with p = e^(z - lse), do the gradient of o and
- * delta[i] = do[i] . o[i],
+ * delta[i] = sum over j of p[i][j] do[i] . v[j] (= do[i] . o[i]),
  *   dv[j] = sum over i of p[i][j] do[i]
  *   ds[i][j] = scale p[i][j] (do[i] . v[j] - delta[i])
  *   dq[i] = sum over j of ds[i][j] k[j]      dk[j] = sum over i of ds[i][j] q[i]
  * dk and dv sum over the heads that share a key head.  p and ds / scale are
  * rounded to bf16 for the products, whose sums are fp32; the outputs (bf16,
- * laid out as q, k and v) are rounded once.  o and lse are the forward call's.
+ * laid out as q, k and v) are rounded once.  o and lse are the forward call's;
+ * do . o is where delta starts from, but o's rounding does not stay in it: the
+ * ds of a row are made to add to 0.  Infinities and NaN of a sequence may turn
+ * up in any of its gradients, never in another sequence's.
  * Equal inputs give equal bits.  workspace: ufp4_attn_workspace_bytes(T,
  * heads) bytes, 256-byte aligned, any contents; calls that share one must be
  * ordered on one stream.  Errors as the forward call, and

@@ -132,7 +132,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* starts, int B, int64_t 
 
 // Which tile and head a workgroup takes.  All heads of a tile follow one another, so that
 // workgroups that start late have little work (one head after another, a head's
-// longest tiles started last: 32768 tokens 2.76 ms instead of 2.33).  Key heads
+// longest tiles started last: 32768 tokens 2.76 ms instead of 2.33, as the kernel was then).  Key heads
 // alternate first, then the heads of a group: workgroups go to the XCDs in turn, so
 // with eight key heads each XCD keeps one of them in its cache.
 struct Share {
@@ -249,7 +249,8 @@ __device__ __forceinline__ void load_rows(bf16x8 (&f)[S], const uint16_t* base, 
 }
 
 // Waits for fragments that load_rows asked for.  Left to their first use inside a loop, the
-// compiler's wait stands there in every pass, and with it one for all copies in flight.
+// compiler's wait stands there in every pass, and with it one for all copies in flight
+// (701 + 1300 + 17 + 983 tokens of 80 elements, forward and backward: 142 us instead of 122).
 template <int S>
 __device__ __forceinline__ void arrived(bf16x8 (&f)[S]) {
 #pragma unroll

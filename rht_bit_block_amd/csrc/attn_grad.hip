@@ -12,6 +12,11 @@
 // nothing in memory that is not an output.  p and ds are rounded to bf16 for the
 // products that they enter, half a step each in long sums.
 //
+// Bound as the forward pass is: 4 sequences of 4096 tokens, 40 heads on 8 key heads, D =
+// 128, on cards of 3.16 .. 3.37 ms for forward and backward: forward 0.69 .. 0.72 ms
+// (0.95 .. 1.0 PFLOP/s), dq 1.20 .. 1.30 and dk/dv 1.26 .. 1.36 ms (four products
+// each: 1.06 .. 1.15 and 1.01 .. 1.09 PFLOP/s).
+//
 // As in the forward pass a product's registers are the next one's fragments: with
 // s = q k^T (a key per lane) p and ds enter dv = p^T do and dk = ds^T q, with s^T =
 // k q^T (a query per lane) ds enters dq^T = k^T ds^T.
