@@ -30,16 +30,19 @@ namespace {
 
 using namespace attn;
 
-// DP: elements of a row in LDS; S, NB: 16- and 32-element pieces of a head in use.
-template <int DP, int S, int NB>
-__global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p, int first, int tiles_in_all) {
+// DP: elements of a row in LDS; S, NB: 16- and 32-element pieces of a head in use; PARTS: sets of
+// four waves that share the tile's keys (in_parts).
+template <int DP, int S, int NB, int PARTS>
+__global__ __launch_bounds__(256 * PARTS, 2) void k_attn_fwd(AttnLaunch p, int first, int tiles_in_all) {
   constexpr int TILE = 64 * DP * 2;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * TILE];
+  __shared__ __attribute__((aligned(1024))) uint8_t all_lds[PARTS * 4 * TILE];
   int64_t row0;
   int n, t;
   const Share me = share_of(blockIdx.x, p.by_heads, p.by_kv_heads, p.group);
   if (!find_tile<false>(p.starts, p.B, p.T, tiles_in_all, first + me.tile, row0, n, t)) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, any_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = any_wave & 3, part = any_wave >> 2;
+  uint8_t* const lds = all_lds + part * 4 * TILE;
   const int h = me.head, hk = me.kv_head;
   const int q0 = t * kAttnTile, qw = q0 + 32 * wave;   // the workgroup's and the wave's first query
   const int qi = qw + (lane & 31);
@@ -50,8 +53,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p, int first, in
   TileCopy<DP, 64, 4> copy;
   copy.init(lane);
   const uint32_t lds0 = lds_address(lds);
-  copy.issue(lds0, kb, p.ldk, 0, n, p.D, wave, lane);
-  copy.issue(lds0 + TILE, vb, p.ldv, 0, n, p.D, wave, lane);
+  copy.issue(lds0, kb, p.ldk, 64 * part, n, p.D, wave, lane);
+  copy.issue(lds0 + TILE, vb, p.ldv, 64 * part, n, p.D, wave, lane);
   bf16x8 q[S];
   load_rows<S>(q, p.q + row0 * p.ldq + (int64_t)h * p.D, p.ldq, qw, n, p.D, lane);
   // the factor of the scores is c >= 0, its sign in q; not 0, because -inf marks a key that
@@ -71,15 +74,16 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p, int first, in
   for (int b = 0; b < NB; ++b) o[b] = zero16();
   float m = -INFINITY, l = 0.0f;   // m: of c s
 
-  for (int j = 0; j < tiles; ++j) {
-    const uint8_t* kt = lds + (j & 1) * 2 * TILE;
+  for (int step = 0; PARTS * step < tiles; ++step) {
+    const int j = PARTS * step + part;
+    const uint8_t* kt = lds + (step & 1) * 2 * TILE;
     const uint8_t* vt = kt + TILE;
     wait_vmcnt<0>();
-    __syncthreads();   // tile j is there, and tile j - 1 has been read
-    if (j + 1 < tiles) {
-      const uint32_t to = lds0 + ((j + 1) & 1) * 2 * TILE;
-      copy.issue(to, kb, p.ldk, 64 * (j + 1), n, p.D, wave, lane);
-      copy.issue(to + TILE, vb, p.ldv, 64 * (j + 1), n, p.D, wave, lane);
+    __syncthreads();   // tile j is there, and the one before has been read
+    if (j + PARTS < tiles) {
+      const uint32_t to = lds0 + ((step + 1) & 1) * 2 * TILE;
+      copy.issue(to, kb, p.ldk, 64 * (j + PARTS), n, p.D, wave, lane);
+      copy.issue(to + TILE, vb, p.ldv, 64 * (j + PARTS), n, p.D, wave, lane);
     }
     const int j0 = 64 * j;
     if (j0 > qw + 31 || qw >= n) continue;   // nothing for this wave in the tile
@@ -134,8 +138,26 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p, int first, in
     run.go(read_v, [&](int i, const bf16x8& v) { o[i % NB] = mfma(v, w[i / NB], o[i % NB]); });
   }
   wait_vmcnt<0>();
-  if (qi >= n) return;
   l = both_sum(l);
+  if constexpr (PARTS == 2) {
+    static_assert(PARTS * 4 * TILE >= 4 * (NB * 4096 + 512), "a lane's sums and two more");
+    float* sums = reinterpret_cast<float*>(all_lds) + wave * (NB * 1024 + 128);
+    __syncthreads();   // all tiles have been read
+    if (part) {
+      leave_sums(sums, o, lane);
+      sums[NB * 1024 + lane] = m;
+      sums[NB * 1024 + 64 + lane] = l;
+    }
+    __syncthreads();
+    if (part) return;
+    // the first part has seen key 0; the second may have seen none, m1 = -inf and l1 = 0
+    const float m1 = sums[NB * 1024 + lane], top = fmaxf(m, m1);
+    const float f0 = __builtin_amdgcn_exp2f(m - top), f1 = __builtin_amdgcn_exp2f(m1 - top);
+    m = top;
+    l = l * f0 + sums[NB * 1024 + 64 + lane] * f1;
+    take_sums(sums, o, f0, f1, lane);
+  }
+  if (qi >= n) return;
   const float inv = 1.0f / l;
   const int64_t row = row0 + qi;
   if (p.lse && lane < 32) p.lse[row * p.heads + h] = (m + __builtin_amdgcn_logf(l)) * kLn2;
@@ -153,16 +175,22 @@ __global__ __launch_bounds__(256, 2) void k_attn_fwd(AttnLaunch p, int first, in
     }
 }
 
+template <int DP, int S, int NB>
+void launch(const AttnLaunch& p, hipStream_t s) {
+  const int64_t tiles = p.T / kAttnTile + p.B;
+  over_tiles(tiles, p.heads, [&](int t0, unsigned blocks) {
+    if (in_parts(tiles * p.heads)) k_attn_fwd<DP, S, NB, 2><<<blocks, 512, 0, s>>>(p, t0, (int)tiles);
+    else k_attn_fwd<DP, S, NB, 1><<<blocks, 256, 0, s>>>(p, t0, (int)tiles);
+  });
+}
+
 }  // namespace
 
 hipError_t launch_attn_fwd(const AttnLaunch& p, hipStream_t s) {
-  const int64_t tiles = p.T / kAttnTile + p.B;
-  over_tiles(tiles, p.heads, [&](int t0, unsigned blocks) {
-    if (p.D <= 32) k_attn_fwd<64, 2, 1><<<blocks, 256, 0, s>>>(p, t0, (int)tiles);
-    else if (p.D <= 64) k_attn_fwd<64, 4, 2><<<blocks, 256, 0, s>>>(p, t0, (int)tiles);
-    else if (p.D <= 96) k_attn_fwd<128, 6, 3><<<blocks, 256, 0, s>>>(p, t0, (int)tiles);
-    else k_attn_fwd<128, 8, 4><<<blocks, 256, 0, s>>>(p, t0, (int)tiles);
-  });
+  if (p.D <= 32) launch<64, 2, 1>(p, s);
+  else if (p.D <= 64) launch<64, 4, 2>(p, s);
+  else if (p.D <= 96) launch<128, 6, 3>(p, s);
+  else launch<128, 8, 4>(p, s);
   return hipGetLastError();
 }
 

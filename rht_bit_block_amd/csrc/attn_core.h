@@ -147,6 +147,38 @@ __device__ __forceinline__ Share share_of(uint32_t id, FastDiv by_heads, FastDiv
   return Share{(int)tile, (int)((r - in_group * by_kv.d) * group + in_group), (int)(r - in_group * by_kv.d)};
 }
 
+// Whether a launch of so many workgroups (at most) takes them in two parts, of which each
+// has every other step of its tile: eight waves instead of four, joined at the end.
+// The last tile to finish is then what a launch takes, and half as long; with more
+// workgroups than fit at once the waves' common barriers cost more.  Forward and
+// backward, four waves and eight: 2048 tokens of 4 heads (68 workgroups) 173 and 137 us, 2
+// x 1500 of 16 (400) 156 and 135; 3001 tokens of 20 heads (540) 123 and 130, 4 x
+// 4096 of 40 (5280) 3.16 and 3.41 ms.
+inline bool in_parts(int64_t workgroups) { return workgroups <= kInParts; }
+
+// The second part's sums of a wave's 32 x 32 N accumulators pass through LDS to the first
+// part: `sums` is the wave's, 4096 N bytes.
+template <int N>
+__device__ __forceinline__ void leave_sums(float* sums, const floatx16 (&x)[N], int lane) {
+#pragma unroll
+  for (int b = 0; b < N; ++b)
+#pragma unroll
+    for (int r = 0; r < 16; r += 4)
+      *reinterpret_cast<f32x4*>(sums + 256 * (4 * b + r / 4) + 4 * lane) =
+          f32x4{x[b][r], x[b][r + 1], x[b][r + 2], x[b][r + 3]};
+}
+template <int N>
+__device__ __forceinline__ void take_sums(const float* sums, floatx16 (&x)[N], float mine, float theirs, int lane) {
+#pragma unroll
+  for (int b = 0; b < N; ++b)
+#pragma unroll
+    for (int r = 0; r < 16; r += 4) {
+      const f32x4 y = *reinterpret_cast<const f32x4*>(sums + 256 * (4 * b + r / 4) + 4 * lane);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[b][r + e] = x[b][r + e] * mine + y[e] * theirs;
+    }
+}
+
 // Launches over `tiles` tiles of `heads` heads, fewer than 2^24 workgroups at a time; f(first
 // tile, workgroups).
 template <class F>

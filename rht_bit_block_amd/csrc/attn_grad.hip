@@ -36,17 +36,19 @@ __device__ __forceinline__ float add_pair(uint32_t pair, float x) {
 
 // dk and dv of 128 keys of one key head, 32 to a wave: two waves to a SIMD, whose
 // registers hold the sums and K; V's rows stay in LDS.
-template <int DP, int S, int NB>
-__global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first, int tiles_in_all) {
+template <int DP, int S, int NB, int PARTS>
+__global__ __launch_bounds__(256 * PARTS, 2) void k_attn_dkv(AttnLaunch p, int first, int tiles_in_all) {
   constexpr int TILE = 32 * DP * 2;
   constexpr int STAGE = 2 * TILE;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * TILE + 2 * STAGE];
-  __shared__ __attribute__((aligned(16))) float stat[2][64];   // stage; lse log2(e) and delta of 32 queries
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[4 * TILE + PARTS * 2 * STAGE];
+  __shared__ __attribute__((aligned(16))) float all_stat[PARTS][2][64];   // stage; lse log2(e) and delta of 32 queries
   int64_t row0;
   int n, t;
   const Share me = share_of(blockIdx.x, p.by_kv_heads, p.by_kv_heads, 1);
   if (!find_tile<true>(p.starts, p.B, p.T, tiles_in_all, first + me.tile, row0, n, t)) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, any_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = any_wave & 3, part = any_wave >> 2;
+  float (&stat)[2][64] = all_stat[part];
   const int hk = me.head;
   const int k0 = t * kAttnTile, kw = k0 + 32 * wave;
   const int key = kw + (lane & 31);
@@ -65,11 +67,12 @@ __global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first, in
 
   // the queries from the first key on, 32 a step, head after head of the group
   const int per_head = (n - k0 + 31) / 32;
-  const uint32_t lds0 = lds_address(lds), steps0 = lds0 + 4 * TILE;
+  uint8_t* const stages = lds + 4 * TILE + part * 2 * STAGE;
+  const uint32_t lds0 = lds_address(lds), steps0 = lds_address(stages);
   {
-    TileCopy<DP, 128, 4> copy;
+    TileCopy<DP, 128, 4 * PARTS> copy;
     copy.init(lane);
-    copy.issue(lds0, p.v + row0 * p.ldv + (int64_t)hk * p.D, p.ldv, k0, n, p.D, wave, lane);
+    copy.issue(lds0, p.v + row0 * p.ldv + (int64_t)hk * p.D, p.ldv, k0, n, p.D, any_wave, lane);
   }
   TileCopy<DP, 32, 4> copy;
   copy.init(lane);
@@ -87,20 +90,28 @@ __global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first, in
   const RowFrag<DP> rows(lane);
   const TurnedFrag<DP> turned(lane);
   const int h_end = (hk + 1) * p.group;
-  int h = hk * p.group, step = 0;   // of the step in work
-  issue(h, k0, 0);
-  for (int st = 0; h < h_end; st ^= 1) {
-    const uint8_t* qt = lds + 4 * TILE + st * STAGE;
-    const uint8_t* ot = qt + TILE;
-    const int i0 = k0 + 32 * step;
-    wait_vmcnt<0>();
-    __syncthreads();   // the step is there, and the one before has been read
-    if (++step == per_head) {
-      step = 0;
+  int h = hk * p.group, step = part;   // of the step in work
+  auto settle = [&] {
+    while (step >= per_head) {   // at most PARTS times
+      step -= per_head;
       ++h;
     }
+  };
+  settle();
+  if (h < h_end) issue(h, k0 + 32 * step, 0);
+  const int passes = ((int)p.group * per_head + PARTS - 1) / PARTS;
+  for (int x = 0; x < passes; ++x) {
+    const int st = x & 1;
+    const uint8_t* qt = stages + st * STAGE;
+    const uint8_t* ot = qt + TILE;
+    const int i0 = k0 + 32 * step;
+    const bool live = h < h_end;   // a part may have a step less
+    wait_vmcnt<0>();
+    __syncthreads();   // the step is there, and the one before has been read
+    step += PARTS;
+    settle();
     if (h < h_end) issue(h, k0 + 32 * step, st ^ 1);
-    if (i0 + 31 < kw || kw >= n) continue;   // every query lies before the wave's keys
+    if (!live || i0 + 31 < kw || kw >= n) continue;   // every query lies before the wave's keys
     floatx16 s = zero16(), dp = zero16();
     {
       struct Three {
@@ -150,6 +161,19 @@ __global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first, in
     });
   }
   wait_vmcnt<0>();
+  if constexpr (PARTS == 2) {
+    static_assert(sizeof(lds) >= 4 * NB * 4096, "the sums of four waves");
+    float* sums = reinterpret_cast<float*>(lds) + wave * NB * 1024;
+    __syncthreads();   // all steps have been read
+    if (part) leave_sums(sums, dk, lane);
+    __syncthreads();
+    if (!part) take_sums(sums, dk, 1.0f, 1.0f, lane);
+    __syncthreads();
+    if (part) leave_sums(sums, dv, lane);
+    __syncthreads();
+    if (part) return;
+    take_sums(sums, dv, 1.0f, 1.0f, lane);
+  }
   // a lane holds element 32 b + l % 32 of keys kw + 8 (r / 4) + 4 (l / 32) + r % 4
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
@@ -175,15 +199,16 @@ __global__ __launch_bounds__(256, 2) void k_attn_dkv(AttnLaunch p, int first, in
 // holds for whatever is summed: with the rounded ds0 in both sums the roundings' common
 // part goes as well (2.2e-3).  It takes one product more, on fragments of K that are
 // there.  The row's sum of the ds0 themselves is what delta lacks, for dk.
-template <int DP, int S, int NB>
-__global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int first, int tiles_in_all) {
+template <int DP, int S, int NB, int PARTS>
+__global__ __launch_bounds__(256 * PARTS, 2) void k_attn_dq(AttnLaunch p, int first, int tiles_in_all) {
   constexpr int TILE = 32 * DP * 2;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[8 * TILE];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[(4 + 4 * PARTS) * TILE];
   int64_t row0;
   int n, t;
   const Share me = share_of(blockIdx.x, p.by_heads, p.by_kv_heads, p.group);
   if (!find_tile<false>(p.starts, p.B, p.T, tiles_in_all, first + me.tile, row0, n, t)) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, any_wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave = any_wave & 3, part = any_wave >> 2;
   const int h = me.head, hk = me.kv_head;
   const int q0 = t * kAttnTile, qw = q0 + 32 * wave;
   const int qi = qw + (lane & 31);
@@ -191,16 +216,17 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int first, int
   const uint16_t* vb = p.v + row0 * p.ldv + (int64_t)hk * p.D;
   const uint16_t* gb = p.dout + row0 * p.lddo + (int64_t)h * p.D;
   const int tiles = (min(n, q0 + kAttnTile) + 31) / 32;
-  const uint32_t lds0 = lds_address(lds), steps0 = lds0 + 4 * TILE;
+  uint8_t* const stages = lds + (4 + 4 * part) * TILE;
+  const uint32_t lds0 = lds_address(lds), steps0 = lds_address(stages);
   {
-    TileCopy<DP, 128, 4> copy;   // the rows of do
+    TileCopy<DP, 128, 4 * PARTS> copy;   // the rows of do
     copy.init(lane);
-    copy.issue(lds0, gb, p.lddo, q0, n, p.D, wave, lane);
+    copy.issue(lds0, gb, p.lddo, q0, n, p.D, any_wave, lane);
   }
   TileCopy<DP, 32, 4> copy;
   copy.init(lane);
-  copy.issue(steps0, kb, p.ldk, 0, n, p.D, wave, lane);
-  copy.issue(steps0 + TILE, vb, p.ldv, 0, n, p.D, wave, lane);
+  copy.issue(steps0, kb, p.ldk, 32 * part, n, p.D, wave, lane);
+  copy.issue(steps0 + TILE, vb, p.ldv, 32 * part, n, p.D, wave, lane);
   // delta0 is the diagonal of o do^T, by the instructions that v do^T comes from: where a
   // query has one key, o is that v and do . v - delta0 exactly 0
   float lw = INFINITY, delta = 0.0f;
@@ -235,15 +261,16 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int first, int
   for (int b = 0; b < NB; ++b) dq[b] = pk[b] = zero16();
   float lacks = 0.0f, rounded = 0.0f;   // this lane's half of the sums of ds0
 
-  for (int j = 0; j < tiles; ++j) {
-    const uint8_t* kt = lds + 4 * TILE + (j & 1) * 2 * TILE;
+  for (int step = 0; PARTS * step < tiles; ++step) {
+    const int j = PARTS * step + part;
+    const uint8_t* kt = stages + (step & 1) * 2 * TILE;
     const uint8_t* vt = kt + TILE;
     wait_vmcnt<0>();
-    __syncthreads();   // tile j is there, and tile j - 1 has been read
-    if (j + 1 < tiles) {
-      const uint32_t to = steps0 + ((j + 1) & 1) * 2 * TILE;
-      copy.issue(to, kb, p.ldk, 32 * (j + 1), n, p.D, wave, lane);
-      copy.issue(to + TILE, vb, p.ldv, 32 * (j + 1), n, p.D, wave, lane);
+    __syncthreads();   // tile j is there, and the one before has been read
+    if (j + PARTS < tiles) {
+      const uint32_t to = steps0 + ((step + 1) & 1) * 2 * TILE;
+      copy.issue(to, kb, p.ldk, 32 * (j + PARTS), n, p.D, wave, lane);
+      copy.issue(to + TILE, vb, p.ldv, 32 * (j + PARTS), n, p.D, wave, lane);
     }
     const int j0 = 32 * j;
     if (j0 > qw + 31 || qw >= n) continue;
@@ -288,11 +315,31 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int first, int
     });
   }
   wait_vmcnt<0>();
-  if (qi >= n) return;
   rounded = both_sum(rounded);
-  delta += both_sum(lacks);
+  lacks = both_sum(lacks);
+  float* sums = reinterpret_cast<float*>(lds) + wave * (NB * 1024);
+  if constexpr (PARTS == 2) {
+    __shared__ float both[2][2][4][64];   // part; rounded and lacks, of both parts in the end
+    both[part][0][wave][lane] = rounded;
+    both[part][1][wave][lane] = lacks;
+    __syncthreads();   // and all tiles have been read
+    rounded = both[0][0][wave][lane] + both[1][0][wave][lane];
+    lacks = both[0][1][wave][lane] + both[1][1][wave][lane];
+  }
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int r = 0; r < 16; ++r) dq[b][r] = __builtin_fmaf(-rounded, pk[b][r], dq[b][r]);
+  if constexpr (PARTS == 2) {
+    static_assert(sizeof(lds) >= 4 * NB * 4096, "the sums of four waves");
+    if (part) leave_sums(sums, dq, lane);
+    __syncthreads();
+    if (part) return;
+    take_sums(sums, dq, 1.0f, 1.0f, lane);
+  }
+  if (qi >= n) return;
   if (lane < 32) {
-    p.delta[h * p.T + row0 + qi] = delta;
+    p.delta[h * p.T + row0 + qi] = delta + lacks;
     p.lw[h * p.T + row0 + qi] = lw;
   }
   uint16_t* out = p.dq + (row0 + qi) * p.lddq + (int64_t)h * p.D;
@@ -302,11 +349,8 @@ __global__ __launch_bounds__(256, 2) void k_attn_dq(AttnLaunch p, int first, int
     for (int r = 0; r < 16; r += 4) {
       const int d = 32 * b + 2 * r + 4 * (lane >> 5);
       if (d < p.D) {
-        float x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          x[e] = __builtin_fmaf(-rounded, pk[b][r + e], dq[b][r + e]) * p.scale;
-        const u32x2 v = {pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+        const u32x2 v = {pack_bf16(dq[b][r] * p.scale, dq[b][r + 1] * p.scale),
+                         pack_bf16(dq[b][r + 2] * p.scale, dq[b][r + 3] * p.scale)};
         *reinterpret_cast<u32x2*>(out + d) = v;
       }
     }
@@ -316,10 +360,12 @@ template <int DP, int S, int NB>
 void launch(const AttnLaunch& p, hipStream_t s) {
   const int64_t tiles = p.T / kAttnTile + p.B;
   over_tiles(tiles, p.heads, [&](int t0, unsigned blocks) {
-    k_attn_dq<DP, S, NB><<<blocks, 256, 0, s>>>(p, t0, (int)tiles);
+    if (in_parts(tiles * p.heads)) k_attn_dq<DP, S, NB, 2><<<blocks, 512, 0, s>>>(p, t0, (int)tiles);
+    else k_attn_dq<DP, S, NB, 1><<<blocks, 256, 0, s>>>(p, t0, (int)tiles);
   });
   over_tiles(tiles, p.kv_heads, [&](int t0, unsigned blocks) {   // reads what dq's left
-    k_attn_dkv<DP, S, NB><<<blocks, 256, 0, s>>>(p, t0, (int)tiles);
+    if (in_parts(tiles * p.kv_heads)) k_attn_dkv<DP, S, NB, 2><<<blocks, 512, 0, s>>>(p, t0, (int)tiles);
+    else k_attn_dkv<DP, S, NB, 1><<<blocks, 256, 0, s>>>(p, t0, (int)tiles);
   });
 }
 

@@ -9,6 +9,9 @@
 namespace ufp4 {
 
 constexpr int kAttnTile = 128;                       // queries (or keys) of a workgroup
+// Workgroups of four waves that the chip holds at once: launches of no more take eight waves
+// each (see in_parts).
+constexpr int64_t kInParts = 512;
 constexpr int64_t kAttnMaxRows = (int64_t)1 << 30, kAttnMaxSeqs = (int64_t)1 << 20;
 constexpr int64_t kAttnMaxPitch = (int64_t)1 << 22;  // 32-bit offsets inside a tile of 128 rows
 constexpr int kAttnMaxHeads = 1024, kAttnMaxWidth = 128;

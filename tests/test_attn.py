@@ -121,6 +121,27 @@ def test_forward_and_backward(lens, heads, kv, D):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("empty", [0, 600])
+@pytest.mark.parametrize("lens,heads,kv,D", [([200, 70], 2, 1, 32), ([129, 257], 2, 2, 64), ([300, 1], 3, 1, 96), ([31, 450], 4, 2, 128)])
+def test_few_and_many_workgroups(lens, heads, kv, D, empty):
+    """Launches of few workgroups, whose tiles two sets of waves share, and (empty sequences
+    count) of many; a group's heads of odd and even number of steps."""
+    T = sum(lens)
+    q, k, v, do = rand(T, heads, D, 51), rand(T, kv, D, 52), rand(T, kv, D, 53), rand(T, heads, D, 54)
+    want = formulas(q, k, v, lens, 0.2, do)
+    starts = packed(lens + [0] * empty).cuda()
+    Q, K, V, dO = (x.cuda() for x in (q, k, v, do))
+    o, lse = U.ufp4_attn_fwd(Q, K, V, starts, scale=0.2)
+    near("o", o, want["o"])
+    near("lse", lse, want["lse"])
+    got = U.ufp4_attn_bwd(Q, K, V, starts, o, lse, dO, scale=0.2)
+    for name, x in zip(("dq", "dk", "dv"), got):
+        near(name, x, want[name])
+    again = U.ufp4_attn_bwd(Q, K, V, starts, o, lse, dO, scale=0.2)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("scale,spread", [(-0.3, 1.0), (0.0, 1.0), (1.0, 3.0), (0.02, 30.0)])
 def test_scales(scale, spread):
     """Factors of any sign, rows that one key wins."""
