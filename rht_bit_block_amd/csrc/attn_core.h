@@ -153,8 +153,11 @@ __device__ __forceinline__ Share share_of(uint32_t id, FastDiv by_heads, FastDiv
 // workgroups than fit at once the waves' common barriers cost more.  Forward and
 // backward, four waves and eight: 2048 tokens of 4 heads (68 workgroups) 173 and 137 us, 2
 // x 1500 of 16 (400) 156 and 135; 3001 tokens of 20 heads (540) 123 and 130, 4 x
-// 4096 of 40 (5280) 3.16 and 3.41 ms.
-inline bool in_parts(int64_t workgroups) { return workgroups <= kInParts; }
+// 4096 of 40 (5280) 3.16 and 3.41 ms.  Sequences of one tile of keys have nothing for a
+// second part to do (19 tokens, forward: 5.6 and 6.4 us).
+inline bool in_parts(const AttnLaunch& p, int64_t workgroups) {
+  return workgroups <= kInParts && p.T > 64 * (int64_t)p.B;
+}
 
 // The second part's sums of a wave's 32 x 32 N accumulators pass through LDS to the first
 // part: `sums` is the wave's, 4096 N bytes.

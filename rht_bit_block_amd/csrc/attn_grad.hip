@@ -360,11 +360,11 @@ template <int DP, int S, int NB>
 void launch(const AttnLaunch& p, hipStream_t s) {
   const int64_t tiles = p.T / kAttnTile + p.B;
   over_tiles(tiles, p.heads, [&](int t0, unsigned blocks) {
-    if (in_parts(tiles * p.heads)) k_attn_dq<DP, S, NB, 2><<<blocks, 512, 0, s>>>(p, t0, (int)tiles);
+    if (in_parts(p, tiles * p.heads)) k_attn_dq<DP, S, NB, 2><<<blocks, 512, 0, s>>>(p, t0, (int)tiles);
     else k_attn_dq<DP, S, NB, 1><<<blocks, 256, 0, s>>>(p, t0, (int)tiles);
   });
   over_tiles(tiles, p.kv_heads, [&](int t0, unsigned blocks) {   // reads what dq's left
-    if (in_parts(tiles * p.kv_heads)) k_attn_dkv<DP, S, NB, 2><<<blocks, 512, 0, s>>>(p, t0, (int)tiles);
+    if (in_parts(p, tiles * p.kv_heads)) k_attn_dkv<DP, S, NB, 2><<<blocks, 512, 0, s>>>(p, t0, (int)tiles);
     else k_attn_dkv<DP, S, NB, 1><<<blocks, 256, 0, s>>>(p, t0, (int)tiles);
   });
 }
