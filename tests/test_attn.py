@@ -294,6 +294,51 @@ def test_many_sequences_and_one_long():
 
 
 @pytest.mark.gpu
+def test_rows_past_32_bits():
+    """The last rows of tensors of more than 2^32 elements."""
+    T, W, heads, kv, D, n = 530000, 8192, 4, 2, 64, 200
+    assert (T - n) * W > 1 << 32
+    big, grads = (torch.empty(T, W, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    cut = lambda m: (m[:, :256].unflatten(1, (4, 64)), m[:, 256:384].unflatten(1, (2, 64)),  # noqa: E731
+                     m[:, 8064:].unflatten(1, (2, 64)), m[:, 512:768].unflatten(1, (4, 64)), m[:, 1024:1280].unflatten(1, (4, 64)))
+    q, k, v, do = rand(n, heads, D, 61), rand(n, kv, D, 62), rand(n, kv, D, 63), rand(n, heads, D, 64)
+    Q, K, V, dO, out = cut(big)
+    for x, y in ((Q, q), (K, k), (V, v), (dO, do)):
+        x[T - n:] = y.cuda()
+    starts = packed([n], T - n).cuda()
+    o, lse = U.ufp4_attn_fwd(Q, K, V, starts, out=out)
+    got = U.ufp4_attn_bwd(Q, K, V, starts, o, lse, dO, out=cut(grads)[:3])
+    want = formulas(q, k, v, [n], D ** -0.5, do)
+    for name, x in zip(("o", "lse", "dq", "dk", "dv"), (o, lse, *got)):
+        near(name, x[T - n:], want[name])
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    """Calls on two streams, each with memory of its own, give what they give one after another."""
+    lens, heads, kv, D = [700, 800], 8, 2, 128
+    T = sum(lens)
+    starts = packed(lens).cuda()
+    sets = [[rand(T, h, D, 70 + 4 * i + j).cuda() for j, h in enumerate((heads, kv, kv, heads))] for i in range(2)]
+
+    def run(Q, K, V, dO):
+        o, lse = U.ufp4_attn_fwd(Q, K, V, starts)
+        return (o, lse, *U.ufp4_attn_bwd(Q, K, V, starts, o, lse, dO))
+
+    want = [run(*x) for x in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(3):
+        got = []
+        for s, x in zip(streams, sets):
+            with torch.cuda.stream(s):
+                got.append(run(*x))
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.gpu
 def test_nothing_to_do():
     z = lambda t, h: torch.zeros(t, h, 64, dtype=torch.bfloat16, device="cuda")  # noqa: E731
     o, lse = U.ufp4_attn_fwd(z(0, 2), z(0, 1), z(0, 1), packed([0]).cuda())

@@ -311,6 +311,46 @@ def test_pages_of_any_size(page):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("page,pages", [(64, 140000), (16, 560000)])
+def test_pages_past_32_bits(page, pages):
+    """Pages of a cache whose codes are more than 2^32 bytes hold what those of a small one do."""
+    cfg, kv, heads, D, n = make(U.UFP4_E2M1, F32, 32, 32), 8, 8, 128, 150
+    assert pages * kv * page * (D // 2) > 1 << 32
+    starts, lens = torch.tensor([0, n], dtype=torch.int32).cuda(), torch.tensor([n], dtype=torch.int32).cuda()
+    k, v, q = (rand(n, h, D, 80 + i).cuda() for i, h in enumerate((kv, kv, heads)))
+    slots = -(-n // page)
+    places = torch.arange(slots, dtype=torch.int32)
+    got = []
+    for cache, table in ((U.KVCache.empty(pages, kv, page, D, cfg), pages - 1 - 37 * places),
+                         (U.KVCache.empty(slots, kv, page, D, cfg), places)):
+        table = table[None].cuda()
+        U.ufp4_kv_write(k, v, starts, lens, table, cache)
+        got.append((*U.ufp4_kv_read(cache, starts, lens, table, n), U.ufp4_kv_attn(q, starts, lens, table, cache)))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    """Calls on two streams over one cache, each with a workspace of its own."""
+    cfg, heads = make(U.UFP4_INT4, F32, 16, 64), 10
+    s = Setup([3000, 700, 65], [1, 1, 1], 2, 128, 64, cfg)
+    filled(s)
+    place = s.dev()
+    qs = [rand(s.T, heads, 128, 90 + i).cuda() for i in range(2)]
+    want = [U.ufp4_kv_attn(q, *place, s.cache) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in qs]
+    for _ in range(3):
+        got = []
+        for st, q in zip(streams, qs):
+            with torch.cuda.stream(st):
+                got.append(U.ufp4_kv_attn(q, *place, s.cache))
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.gpu
 def test_rows_that_see_nothing():
     """No tokens, tokens without places, pages that do not exist in the middle of a sequence; rows behind
     the last sequence keep what they hold."""
