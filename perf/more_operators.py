@@ -249,7 +249,7 @@ def _plain_rounding(x, s):
         e = torch.where(m == 0, torch.full_like(e, -127), torch.where(f > f0, e - e0 + 1, e - e0).clamp(-127, 127))
         scales, v = (e + 127).to(torch.uint8), torch.ldexp(b, -e[..., None])
     else:
-        scales = m / torch.full_like(m, top)  # a scalar divisor would be multiplied with its reciprocal
+        scales = m / top
         v = torch.where(scales[..., None] == 0, torch.zeros_like(b), b / scales[..., None])
     v = v.view(x.shape)
     a = v.abs()
@@ -424,7 +424,7 @@ def _exact_quantized(x, case, turn):
     """Rows [N, D] rounded to the grid, out of the rotation's basis again."""
     y = (x.double().view(-1, case["n"]) @ turn).view(-1, case["block"])
     m, top = y.abs().amax(1, keepdim=True), TOP[case["grid"]]
-    size = (m / torch.full_like(m, top)).float().double()  # a scale is kept in 32 bits
+    size = (m / top).float().double()  # a scale is kept in 32 bits
     if case["scale"] == "pow2":
         size = m / top
         e = torch.ceil(torch.log2(size))
