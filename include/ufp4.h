@@ -488,7 +488,9 @@ size_t ufp4_moe_tokens_workspace_bytes(int64_t T, int32_t E, int32_t top_k, int6
  * the weights e^(z - m) (m: a running maximum of the row, or up to 8 ln 2 less)
  * are rounded to bf16 for the second product, o once at the end.  Equal inputs
  * give equal bits.  An infinity or NaN in a token may turn up in
- * earlier tokens of the same sequence, never in another one.
+ * earlier tokens of the same sequence, never in another one.  A key whose score
+ * is -inf has weight 0; a row whose scores are all -inf has o = NaN and lse =
+ * -inf.
  * Errors: UFP4_ERR_INVALID_ARG (negative sizes, null pointers, pitches,
  * alignment, a scale that is not finite, heads not a multiple of kv_heads),
  * UFP4_ERR_SHAPE (D % 8), UFP4_ERR_UNSUPPORTED (D > 128, T > 2^30, B > 2^20,

@@ -120,13 +120,15 @@ __global__ __launch_bounds__(256 * PARTS, 2) void k_attn_fwd(AttnLaunch p, int f
 #pragma unroll
         for (int r = 0; r < 16; ++r) o[b][r] *= f;
     }
+    // a row whose keys so far all score -inf has weights of 0, and m for a later one to move
+    const float base = m == -INFINITY ? 0.0f : m;
     bf16x8 w[4];
     float sum = 0.0f;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        s[u][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][r], c, -m));
+        s[u][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[u][r], c, -base));
         sum += s[u][r];
       }
       uint32_t pairs[8];
@@ -150,9 +152,10 @@ __global__ __launch_bounds__(256 * PARTS, 2) void k_attn_fwd(AttnLaunch p, int f
     }
     __syncthreads();
     if (part) return;
-    // the first part has seen key 0; the second may have seen none, m1 = -inf and l1 = 0
+    // a part that has seen no key, or none above -inf, has m = -inf and l = 0
     const float m1 = sums[NB * 1024 + lane], top = fmaxf(m, m1);
-    const float f0 = __builtin_amdgcn_exp2f(m - top), f1 = __builtin_amdgcn_exp2f(m1 - top);
+    const float base = top == -INFINITY ? 0.0f : top;
+    const float f0 = __builtin_amdgcn_exp2f(m - base), f1 = __builtin_amdgcn_exp2f(m1 - base);
     m = top;
     l = l * f0 + sums[NB * 1024 + 64 + lane] * f1;
     take_sums(sums, o, f0, f1, lane);
