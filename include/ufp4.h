@@ -510,7 +510,9 @@ int ufp4_attn_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const 
  * laid out as q, k and v) are rounded once.  o and lse are the forward call's;
  * do . o is where delta starts from, but o's rounding does not stay in it: the
  * ds of a row are made to add to 0.  Infinities and NaN of a sequence may turn
- * up in any of its gradients, never in another sequence's.
+ * up in any of its gradients, never in another sequence's.  Where a score is
+ * -inf, dk and dv get 0 from it; a row whose scores are all -inf (its o is not
+ * looked at) adds 0 to both, if its do is finite.
  * Equal inputs give equal bits.  workspace: ufp4_attn_workspace_bytes(T,
  * heads) bytes, 256-byte aligned, any contents; calls that share one must be
  * ordered on one stream.  Errors as the forward call, and

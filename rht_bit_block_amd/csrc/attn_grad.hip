@@ -76,7 +76,7 @@ __global__ __launch_bounds__(256 * PARTS, 2) void k_attn_dkv(AttnLaunch p, int f
   }
   TileCopy<DP, 32, 4> copy;
   copy.init(lane);
-  // queries past the sequence: q, do, lse and delta are 0, and so is what they add
+  // queries past the sequence: q, do, lse and delta are 0
   auto issue = [&](int h, int i0, int st) {
     copy.issue(steps0 + st * STAGE, p.q + row0 * p.ldq + (int64_t)h * p.D, p.ldq, i0, n, p.D, wave, lane);
     copy.issue(steps0 + st * STAGE + TILE, p.dout + row0 * p.lddo + (int64_t)h * p.D, p.lddo, i0, n, p.D,
@@ -133,10 +133,14 @@ __global__ __launch_bounds__(256 * PARTS, 2) void k_attn_dkv(AttnLaunch p, int f
     };
     Run<4 * NB, 3, bf16x8> run;
     run.begin(read_t);
-    if (i0 < kw + 31) {
+    // queries before the key, and past the sequence: their score may be 0 times an infinite
+    // element of the key
+    if (i0 < kw + 31 || i0 + 32 > n) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r)
-        if (key > i0 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) s[r] = -INFINITY;
+      for (int r = 0; r < 16; ++r) {
+        const int i = i0 + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+        if (key > i || i >= n) s[r] = -INFINITY;
+      }
     }
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
@@ -340,7 +344,9 @@ __global__ __launch_bounds__(256 * PARTS, 2) void k_attn_dq(AttnLaunch p, int fi
   if (qi >= n) return;
   if (lane < 32) {
     p.delta[h * p.T + row0 + qi] = delta + lacks;
-    p.lw[h * p.T + row0 + qi] = lw;
+    // finite for a row whose every score is -inf, so that its weights are 0 and keys that it does not
+    // see keep theirs
+    p.lw[h * p.T + row0 + qi] = lw == -INFINITY ? -3.0e38f : lw;
   }
   uint16_t* out = p.dq + (row0 + qi) * p.lddq + (int64_t)h * p.D;
 #pragma unroll

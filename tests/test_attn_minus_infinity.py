@@ -38,3 +38,50 @@ def test_first_keys(first, bad, empty):
     near("o", o[first:], want["o"])
     near("lse", lse[first:], want["lse"])
     assert bool(torch.isnan(o[:first]).all()) and bool((lse[:first] == -math.inf).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("empty", [0, 600])
+@pytest.mark.parametrize("bad", [-math.inf, LOWEST])
+@pytest.mark.parametrize("a,b", [(1, 64), (64, 128), (1, 128), (32, 96), (64, 300)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_keys_among_others(D, a, b, bad, empty):
+    """Keys in the middle, forward and backward: whole tiles, halves of tiles, the second set of waves'
+    first tile.  Their gradients are 0; dq's channel that meets -inf is 0 times it, and not looked at."""
+    n, heads, kv, scale = 330, 4, 2, D ** -0.5
+    q, k, v, do, far, open_k = inputs(n, heads, kv, D, slice(a, b), bad, 15)
+    want = formulas(q, far, v, [n], scale, do)
+    # errors of the scores that count; those of the keys that do not are as large as they are
+    slack = formulas(q, open_k, v, [n], scale)["lse"][1]
+    starts = packed([n] + [0] * empty).cuda()
+    Q, K, V, dO = (x.cuda() for x in (q, k, v, do))
+    o, lse = U.ufp4_attn_fwd(Q, K, V, starts)
+    near("o", o, want["o"])
+    near("lse", lse, (want["lse"][0], slack + 4 * EPS * want["lse"][0].abs()))
+    dq, dk, dv = U.ufp4_attn_bwd(Q, K, V, starts, o, lse, dO)
+    keep = [d for d in range(D) if d != 5]
+    near("dq", dq[..., keep], tuple(x[..., keep] for x in want["dq"]))
+    near("dk", dk, want["dk"])
+    near("dv", dv, want["dv"])
+    assert not bool(dk[a:b].any()) and not bool(dv[a:b].any())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("empty", [0, 600])
+@pytest.mark.parametrize("first", [1, 64, 200])
+def test_rows_without_a_score_have_no_gradient_of_others(first, empty):
+    """Rows whose every key is hidden (filling before a sequence), gradients of 0 for them: keys and values
+    behind them have the rest's own gradients, those among them 0."""
+    n, heads, kv, D = 330, 4, 2, 64
+    q, k, v, do, _, _ = inputs(n, heads, kv, D, slice(0, first), -math.inf, 25)
+    do[:first] = 0
+    want = formulas(q[first:], k[first:], v[first:], [n - first], D ** -0.5, do[first:])
+    starts = packed([n] + [0] * empty).cuda()
+    Q, K, V, dO = (x.cuda() for x in (q, k, v, do))
+    o, lse = U.ufp4_attn_fwd(Q, K, V, starts)
+    dq, dk, dv = U.ufp4_attn_bwd(Q, K, V, starts, o, lse, dO)
+    keep = [d for d in range(D) if d != 5]
+    near("dq", dq[first:][..., keep], tuple(x[..., keep] for x in want["dq"]))
+    near("dk", dk[first:], want["dk"])
+    near("dv", dv[first:], want["dv"])
+    assert not bool(dk[:first].any()) and not bool(dv[:first].any())
