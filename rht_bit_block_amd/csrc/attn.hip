@@ -57,14 +57,8 @@ __global__ __launch_bounds__(256 * PARTS, 2) void k_attn_fwd(AttnLaunch p, int f
   copy.issue(lds0 + TILE, vb, p.ldv, 64 * part, n, p.D, wave, lane);
   bf16x8 q[S];
   load_rows<S>(q, p.q + row0 * p.ldq + (int64_t)h * p.D, p.ldq, qw, n, p.D, lane);
-  // the factor of the scores is c >= 0, its sign in q; not 0, because -inf marks a key that
-  // is not seen
-  const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);
-  if (p.scale < 0.0f) {
-#pragma unroll
-    for (int x = 0; x < S; ++x)
-      q[x] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, q[x]) ^ 0x80008000u);
-  }
+  const float c = score_factor(p.scale);
+  apply_sign(q, p.scale);
   arrived(q);
   const RowFrag<DP> rows(lane);
   const TurnedFrag<DP> turned(lane);

@@ -283,6 +283,21 @@ __device__ __forceinline__ void load_rows(bf16x8 (&f)[S], const uint16_t* base, 
   }
 }
 
+// The factor of the scores in base 2.  Its size multiplies the products, so it is kept above 0 (-inf
+// marks a key that is not seen); its sign, or that it is 0, goes into the operand held in
+// registers.
+__device__ __forceinline__ float score_factor(float scale) {
+  return scale == 0.0f ? 1.0f : fabsf(scale) * kLog2e;
+}
+template <int S>
+__device__ __forceinline__ void apply_sign(bf16x8 (&f)[S], float scale) {
+  if (scale > 0.0f) return;
+  const uint32_t flip = scale < 0.0f ? 0x80008000u : 0u, keep = scale < 0.0f ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+    f[s] = __builtin_bit_cast(bf16x8, (__builtin_bit_cast(u32x4, f[s]) & keep) ^ flip);
+}
+
 // Waits for fragments that load_rows asked for.  Left to their first use inside a loop, the
 // compiler's wait stands there in every pass, and with it one for all copies in flight
 // (701 + 1300 + 17 + 983 tokens of 80 elements, forward and backward: 142 us instead of 122).

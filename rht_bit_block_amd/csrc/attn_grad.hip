@@ -52,15 +52,11 @@ __global__ __launch_bounds__(256 * PARTS, 2) void k_attn_dkv(AttnLaunch p, int f
   const int hk = me.head;
   const int k0 = t * kAttnTile, kw = k0 + 32 * wave;
   const int key = kw + (lane & 31);
-  const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);   // as the forward pass
+  const float c = score_factor(p.scale);
 
   bf16x8 k[S];
   load_rows<S>(k, p.k + row0 * p.ldk + (int64_t)hk * p.D, p.ldk, kw, n, p.D, lane);
-  if (p.scale < 0.0f) {
-#pragma unroll
-    for (int x = 0; x < S; ++x)
-      k[x] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, k[x]) ^ 0x80008000u);
-  }
+  apply_sign(k, p.scale);
   floatx16 dk[NB], dv[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) dk[b] = dv[b] = zero16();
@@ -250,12 +246,8 @@ __global__ __launch_bounds__(256 * PARTS, 2) void k_attn_dq(AttnLaunch p, int fi
   }
   bf16x8 q[S];
   load_rows<S>(q, p.q + row0 * p.ldq + (int64_t)h * p.D, p.ldq, qw, n, p.D, lane);
-  const float c = fmaxf(fabsf(p.scale) * kLog2e, 1e-30f);   // as the forward pass
-  if (p.scale < 0.0f) {
-#pragma unroll
-    for (int x = 0; x < S; ++x)
-      q[x] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(u32x4, q[x]) ^ 0x80008000u);
-  }
+  const float c = score_factor(p.scale);
+  apply_sign(q, p.scale);
   arrived(q);
   asm volatile("" : "+v"(lw));
   const RowFrag<DP> rows(lane);
