@@ -114,13 +114,13 @@ __device__ __forceinline__ float query_sum(float x) {
   return __uint_as_float(a[0]) + __uint_as_float(a[1]);
 }
 
-// Eight codes as bf16 values, in the order of `order`: levels times 2^e of `scale`, or with
-// OFF (INT4) 136 + n, where `scale` is not used: n ^ 8 in the low mantissa bits of 128
-// is two instructions for two codes where tables and a conversion take four, and the
-// products' excess, 136 times the sum of the other operand, is taken off in the
-// accumulator.  SPLIT: the codes of two 1 x 16 blocks, nibbles 0 .. 3 of the first in
-// registers 0, 1, nibbles 4 .. 7 of the second in 2, 3.
-template <int GRID, bool OFF, bool SPLIT>
+// Eight codes as bf16 values, in the order of `order`: levels times 2^e of `scale`.  SPLIT: the codes of
+// two 1 x 16 blocks, nibbles 0 .. 3 of the first in registers 0, 1, nibbles 4 .. 7 of the
+// second in 2, 3.  (INT4 as 136 + n, n ^ 8 in the low mantissa bits of 128, is two
+// instructions for two codes where tables and a conversion take four, and 6 to 9 % faster with one
+// tile of queries; but taking 136 times the sum of the other operand off again leaves the
+// rounding of that sum, however small the codes are.)
+template <int GRID, bool SPLIT>
 __device__ __forceinline__ u32x4 decode8(uint32_t x, float scale) {
   u32x4 v;
   if constexpr (GRID == 2) {
@@ -128,19 +128,6 @@ __device__ __forceinline__ u32x4 decode8(uint32_t x, float scale) {
     v[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 1));
     v[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 2));
     v[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, scale, 3));
-  } else if constexpr (OFF) {
-    const uint32_t y = x ^ 0x88888888u;
-    if constexpr (SPLIT) {
-      const uint32_t a = __builtin_amdgcn_perm(0u, y, 0x04010400u);   // bytes 0 and 1 apart
-      const uint32_t b = __builtin_amdgcn_perm(0u, y, 0x04030402u);
-      v[0] = (a & 0x000F000Fu) | 0x43004300u;
-      v[1] = ((a >> 4) & 0x000F000Fu) | 0x43004300u;
-      v[2] = (b & 0x000F000Fu) | 0x43004300u;
-      v[3] = ((b >> 4) & 0x000F000Fu) | 0x43004300u;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = ((y >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-    }
   } else {
     // E4M3 bytes of the even and of the odd nibbles
     const uint32_t y = x >> 4;
@@ -165,11 +152,10 @@ __device__ __forceinline__ u32x4 decode8(uint32_t x, float scale) {
   return v;
 }
 // Which nibble is the i-th value.
-template <int GRID, bool OFF, bool SPLIT>
+template <int GRID, bool SPLIT>
 __device__ constexpr int order(int i) {
   if (GRID == 2) return i;
   if (SPLIT) return (i & 4) | ((i & 1) << 1) | ((i >> 1) & 1);
-  if (OFF) return (i >> 1) + 4 * (i & 1);
   return i < 4 ? 2 * i : 2 * i - 7;
 }
 
@@ -400,9 +386,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
   using L = Lay<KIND, NB>;
   constexpr int DP = 32 * NB, QP = DP + 4;
   constexpr bool SPLIT = KIND == 1;
-  // with two tiles of queries the excess costs more than the tables, and sums of values
-  // would carry the rounding of 136 weights where a value is 0
-  constexpr bool OFF = GRID == 1 && MT == 1 && KIND != 2;
   constexpr int NBLK = SPLIT ? 2 * NB : NB;   // blocks of a row
   constexpr int GB = NBLK < 4 ? NBLK : 4;     // blocks whose scales are read together
   constexpr int kRows = kWaves * L::PAIR;   // where the waves' third buffers lie, and `rows`
@@ -596,7 +579,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
     __syncthreads();
     // its fragments, in two bf16 pieces; value i of a lane is element `order`
     u32x4 qh[MT][NB], ql[MT][NB];
-    f32x4 excess[OFF ? NBLK : 1];   // -136 times the sum over a block of q', every row alike
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -606,7 +588,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
           float x[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int nib = order<GRID, OFF, SPLIT>(i + e);
+            const int nib = order<GRID, SPLIT>(i + e);
             const int d = SPLIT ? 32 * s + 16 * (nib >> 2) + 4 * g + (nib & 3) : 32 * s + 8 * g + nib;
             x[e] = rows[(16 * mt + li) * QP + d];
           }
@@ -615,22 +597,6 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
           // an infinite piece leaves nothing
           const float l0 = x[0] - __uint_as_float(hi << 16), l1 = x[1] - __uint_as_float(hi & 0xFFFF0000u);
           ql[mt][s][i / 2] = pack_bf16(fabsf(x[0]) < INFINITY ? l0 : 0.0f, fabsf(x[1]) < INFINITY ? l1 : 0.0f);
-        }
-        if constexpr (OFF) {
-          const uint32_t m136 = 0xC308C308u;   // -136 in bf16
-          const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-          if constexpr (SPLIT) {
-            const s16x4 k = __builtin_bit_cast(s16x4, (u32x2{m136, m136}));
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              f32x4 y = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(k, __builtin_bit_cast(s16x4, (u32x2{qh[mt][s][2 * e], qh[mt][s][2 * e + 1]})), z, 0, 0, 0);
-              excess[2 * s + e] = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(k, __builtin_bit_cast(s16x4, (u32x2{ql[mt][s][2 * e], ql[mt][s][2 * e + 1]})), y, 0, 0, 0);
-            }
-          } else {
-            const bf16x8 k = __builtin_bit_cast(bf16x8, (u32x4{m136, m136, m136, m136}));
-            f32x4 y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, __builtin_bit_cast(bf16x8, qh[mt][s]), z, 0, 0, 0);
-            excess[s] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, __builtin_bit_cast(bf16x8, ql[mt][s]), y, 0, 0, 0);
-          }
         }
       }
     wait_lds();
@@ -684,13 +650,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
             if constexpr (SPLIT) {
               const uint32_t x = (uint32_t)*reinterpret_cast<const uint16_t*>(at_k + 2 * g) |
                                  (uint32_t)*reinterpret_cast<const uint16_t*>(at_k + 8 + 2 * g) << 16;
-              const u32x4 v = decode8<GRID, OFF, true>(x, 1.0f);
+              const u32x4 v = decode8<GRID, true>(x, 1.0f);
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
                 const s16x4 k = __builtin_bit_cast(s16x4, (u32x2{v[2 * e], v[2 * e + 1]}));
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                  f32x4 y = OFF ? excess[OFF ? 2 * b + e : 0] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                  f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
                   y = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(k, __builtin_bit_cast(s16x4, (u32x2{qh[mt][b][2 * e], qh[mt][b][2 * e + 1]})), y, 0, 0, 0);
                   y = __builtin_amdgcn_mfma_f32_16x16x16bf16_1k(k, __builtin_bit_cast(s16x4, (u32x2{ql[mt][b][2 * e], ql[mt][b][2 * e + 1]})), y, 0, 0, 0);
 #pragma unroll
@@ -701,10 +667,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
               const uint32_t x = *reinterpret_cast<const uint32_t*>(at_k + 4 * g);
               float scale = 1.0f;
               if constexpr (KIND == 2) scale = __uint_as_float(((sw >> (8 * b)) & 0xFFu) << 23);
-              const bf16x8 k8 = __builtin_bit_cast(bf16x8, decode8<GRID, OFF, false>(x, scale));
+              const bf16x8 k8 = __builtin_bit_cast(bf16x8, decode8<GRID, false>(x, scale));
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
-                f32x4 y = KIND == 2 ? s[mt][j] : OFF ? excess[OFF ? b : 0] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                f32x4 y = KIND == 2 ? s[mt][j] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                 y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8, __builtin_bit_cast(bf16x8, qh[mt][b]), y, 0, 0, 0);
                 y = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k8, __builtin_bit_cast(bf16x8, ql[mt][b]), y, 0, 0, 0);
                 if constexpr (KIND == 2) {   // the conversion has applied the scale
@@ -790,8 +756,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
             u32x4 w[MT][GB];                              // weights times scales
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              constexpr bool NO = false;
-              const int e0 = order<GRID, NO, NO>(2 * i), e1 = order<GRID, NO, NO>(2 * i + 1);
+              const int e0 = order<GRID, false>(2 * i), e1 = order<GRID, false>(2 * i + 1);
               float a[GB], b[GB];
               read_scales<GB>(a, reinterpret_cast<const float*>(vs + (32 * x + 16 * (e0 >> 2) + 4 * g + (e0 & 3)) * VSC) + k0);
               read_scales<GB>(b, reinterpret_cast<const float*>(vs + (32 * x + 16 * (e1 >> 2) + 4 * g + (e1 & 3)) * VSC) + k0);
@@ -805,7 +770,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
             }
 #pragma unroll
             for (int e = 0; e < GB * BD; ++e) {
-              const bf16x8 v = __builtin_bit_cast(bf16x8, decode8<GRID, false, false>((uint32_t)vc[e][x], 1.0f));
+              const bf16x8 v = __builtin_bit_cast(bf16x8, decode8<GRID, false>((uint32_t)vc[e][x], 1.0f));
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt)
                 o[mt][BD * k0 + e] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
