@@ -535,6 +535,7 @@ size_t ufp4_attn_workspace_bytes(int64_t T, int32_t heads);
  * pages kv_heads page_tokens, K = D, which ufp4_dequant reads.  cfg: a 4-bit
  * codebook, 1 x 16 or 1 x 32 blocks, UFP4_RTNE, tensor_scale 0; D a multiple of
  * 16, block_cols and rht_n, at most 128; page_tokens a power of two up to 2^16.
+ * An E8M0 byte e is 2^(e - 127) in every call, 0 included.
  * Device pointers, codes 16-byte and scales 16-byte aligned. */
 typedef struct ufp4_kv_cache {
   uint8_t* k_codes;

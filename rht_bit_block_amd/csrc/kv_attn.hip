@@ -695,7 +695,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_kv_attn(KvAttn p) {
           const uint32_t w = scale_word(buffer(vb) + L::CODES, lane);
           float* vs = reinterpret_cast<float*>(wide) + lane * NB;
 #pragma unroll
-          for (int i = 0; i < NB; ++i) vs[i] = __uint_as_float(((w >> (8 * i)) & 0xFFu) << 23);
+          for (int i = 0; i < NB; ++i)   // 2^(byte - 127); of byte 0 that is below the exponents' range
+            vs[i] = __uint_as_float(max(((w >> (8 * i)) & 0xFFu) << 23, 0x00400000u));
         }
         const int t0 = t_first + step * kStep;
         if (valid != ~(uint64_t)0 || t0 + kStep - 1 > sure) {
