@@ -137,3 +137,18 @@ def test_many_steps_of_a_wave(grid, mode, block, n, D, page, new, heads):
     for b in (3, 17, 40, 43):
         s.table[b, s.table.shape[1] * lens[b] // max(lens) // 2] = -1
     check(s, rand(s.T, heads, D, 6, 2.0))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads", [4, 24])
+@pytest.mark.parametrize("B", [64, 65, 200, 256, 257])
+def test_batches_of_every_plan(B, heads):
+    """Up to 64 sequences a lane each, up to 256 a thread each, more of them block by block; empty ones first,
+    last and between, one that many workgroups share."""
+    lens = [(37 * i) % 400 for i in range(B)]
+    new = [int(x > 0) for x in lens]
+    lens[B // 2], new[B // 2] = 20000, 1
+    lens[0], new[0], lens[-1], new[-1], lens[5], new[5] = 0, 0, 300, 0, 0, 0
+    s = Setup(lens, new, 1, 64, 64, make(U.UFP4_E2M1, POW2, 32, 32))
+    fill(s, 7)
+    check(s, rand(s.T, heads, 64, 8, 2.0))
