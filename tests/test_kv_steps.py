@@ -152,3 +152,46 @@ def test_batches_of_every_plan(B, heads):
     s = Setup(lens, new, 1, 64, 64, make(U.UFP4_E2M1, POW2, 32, 32))
     fill(s, 7)
     check(s, rand(s.T, heads, 64, 8, 2.0))
+
+
+@pytest.mark.gpu
+def test_captured_write():
+    """The cache after a replayed step is, in every byte, the cache after the same calls made eagerly."""
+    cfg, kv, heads, D, page, B = make(U.UFP4_INT4, F32, 16, 16), 2, 4, 64, 16, 3
+    s = Setup([200] * B, [1] * B, kv, D, page, cfg)
+    fill(s, 9)
+    buffers = ("k_codes", "k_scales", "v_codes", "v_scales")
+    q, k, v = (rand(B, h, D, 5).cuda() for h in (heads, kv, kv))
+    starts, lens, table = s.dev()
+    out = torch.zeros_like(q)
+    ws = torch.empty(U.ufp4_kv_attn_workspace_bytes(B, B, heads, kv, D), dtype=torch.uint8, device="cuda")
+
+    def step(cache, out, workspace=None):
+        U.ufp4_kv_write(k, v, starts, lens, table, cache)
+        return U.ufp4_kv_attn(q, starts, lens, table, cache, out=out, workspace=workspace)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(s.cache, out, ws)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(s.cache, out, ws)
+    for i, n in enumerate((1, 16, 17, 64, 130, 200)):
+        for x, y in ((q, rand(B, heads, D, 50 + i)), (k, rand(B, kv, D, 60 + i)), (v, rand(B, kv, D, 70 + i))):
+            x.copy_(y)
+        lens.copy_(torch.tensor([n, max(1, n - 5), 201 - n]))
+        twin = U.KVCache(*(getattr(s.cache, x).clone() for x in buffers), cfg)
+        before = twin.k_codes.clone()
+        torch.cuda.synchronize()
+        graph.replay()
+        got = out.clone()
+        torch.cuda.synchronize()
+        want = step(twin, torch.zeros_like(q))
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        for x in buffers:
+            assert torch.equal(getattr(s.cache, x), getattr(twin, x)), x
+        changed = (s.cache.k_codes != before).flatten(2).any(2).any(1).cpu()
+        assert changed.nonzero().flatten().tolist() == sorted(s.slot(b, int(t) - 1)[0] for b, t in enumerate(lens.tolist()))
