@@ -192,9 +192,16 @@ def _check(fn, st):
         raise UFP4Error(fn, st)
 
 
+# A device's current stream as a number, and the current device: by torch's direct calls, which
+# spare a small call some 2 us, where this build of it has them, else by the public ones.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _stream(t: Optional[torch.Tensor] = None):
     if t is not None and t.is_cuda:
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
+        return _raw_stream(t.get_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -202,12 +209,12 @@ def _call(name, t, *args):
     """The library's function `name` with the current stream of t's device behind its
     arguments, on that device."""
     fn, dev = getattr(_lib(), name), t.get_device()
-    if dev < 0 or dev == torch._C._cuda_getDevice():   # an empty tensor may lie anywhere
-        dev = torch._C._cuda_getDevice()
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if dev < 0 or dev == _current_device():   # an empty tensor may lie anywhere
+        dev = _current_device()
+        st = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+            st = fn(*args, _raw_stream(dev))
     if st != UFP4_OK:
         raise UFP4Error(name, st)
 
