@@ -486,7 +486,9 @@ size_t ufp4_moe_tokens_workspace_bytes(int64_t T, int32_t E, int32_t top_k, int6
  *   NULL (no gradient wanted).
  * Products of the inputs are exact and summed in fp32, as are the weights' sums;
  * the weights e^(z - m) (m: a running maximum of the row, or up to 8 ln 2 less)
- * are rounded to bf16 for the second product, o once at the end.  Equal inputs
+ * are rounded to bf16 for the second product, o once at the end.  The sums of
+ * weights times v are up to 2^8 times those of |v| before they are divided: |v|
+ * above some 1e36 / n can overflow in a row of n keys.  Equal inputs
  * give equal bits.  An infinity or NaN in a token may turn up in
  * earlier tokens of the same sequence, never in another one.  A key whose score
  * is -inf has weight 0; a row whose scores are all -inf has o = NaN and lse =
@@ -585,7 +587,8 @@ int ufp4_kv_read(const ufp4_kv_cache* cache, const int32_t* starts, int32_t B, i
  * call is made for few.
  *   q, o : bf16 [T][heads][D].
  * q keeps 16 bits of mantissa, levels are exact, scales and sums fp32; weights
- * times value scales are rounded to bf16, o once at the end.  Equal inputs give
+ * times value scales are rounded to bf16, o once at the end.  Weights are up to
+ * 2^8 before the division, as in ufp4_attn_fwd.  Equal inputs give
  * equal bits.  workspace: ufp4_kv_attn_workspace_bytes bytes, 256-byte aligned,
  * any contents; calls that share one must be ordered on one stream. */
 int ufp4_kv_attn(const void* q, int64_t ldq, const int32_t* starts, int32_t B, int64_t T,

@@ -15,11 +15,11 @@
 // ... lds while the tile before is computed.  s^T = k q^T comes out with a query per
 // lane, so the softmax is in-lane but for one exchange of halves.
 //
-// Bound by the matrix cores and the clock that they leave: 32768 tokens, 8 heads on one
-// key head, D = 128: 1.97 .. 2.04 ms (1.08 .. 1.11 PFLOP/s), the MFMAs busy 60 % of the
-// cycles at 1.73 GHz, where they alone, busy all the time, run at 1.65.  Two
-// workgroups to a compute unit, so that one's softmax is covered by the other's
-// products.  Tried and slower: eight waves that share a tile (two sets of keys: 2.17
+// Bound by the matrix cores and the vector units after each other: 32768 tokens, 8 heads on
+// one key head, D = 128: 1.97 .. 2.07 ms (1.06 .. 1.11 PFLOP/s), the MFMAs busy 60 % of the
+// cycles (at 1.73 GHz, where they alone, busy all the time, run at 1.65), the six vector
+// instructions to an MFMA most of the rest, although two workgroups to a compute unit should cover
+// one's softmax with the other's products.  Tried and slower: eight waves that share a tile (two sets of keys: 2.17
 // ms; 256 queries: 2.03), the next tile's scores multiplied between the exponentials of
 // this one (2.05, registers spilled), waves' priorities (no change).
 #include "attn_core.h"

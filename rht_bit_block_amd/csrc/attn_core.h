@@ -66,7 +66,7 @@ __device__ __forceinline__ void rows_of(const int32_t* starts, int b, int64_t T,
 // 1 tiles of keys, and is attended to from N - t of queries: FROM_END).  Up to 64
 // sequences, a lane each: of the tiles with more work than w there are sum of max(0, N -
 // w), and the work of number x is found by trying 64 w at once, a lane each.  More
-// sequences: one after another, from the last one.
+// sequences: one after another, from the last one, whatever their lengths.
 template <bool FROM_END>
 __device__ __forceinline__ bool find_tile(const int32_t* starts, int B, int64_t T, int tiles, int x,
                                           int64_t& row0, int& n, int& t) {

@@ -27,11 +27,13 @@
 // two bf16 pieces, 16 bits of mantissa.
 //
 // Bound: HBM first, 4 sequences of 131072 tokens on 8 key heads of 128 (E1M2, fp32 scales of 32)
-// 130 us for 670 MB, 5.2 TB/s, with the vector instructions next (719 a step: the
-// same in E2M1 with E8M0 scales 111 us); 64 sequences of 1 to 16384 tokens (E2M1, E8M0)
+// 130 us for 670 MB, 5.2 TB/s, with the vector instructions next (719 a step, two thirds of the
+// cycles; the same in E2M1 with E8M0 scales 111 us); 64 sequences of 1 to 16384 tokens (E2M1, E8M0)
 // 80 us for 385 MB.  Two tiles of queries (16 sequences of about 5900 tokens, 5 rows of 5
-// heads) take 75 us for 146 MB: twice the arithmetic on the same bytes, and all
-// registers.  Tried and slower at 131072 tokens: three workgroups to a compute unit with
+// heads) take 76 us for 146 MB: twice the arithmetic on the same bytes, all registers, and 11 to 22
+// spilled, whose reloads in the steps wait for the copies issued before them.  Pages below 64 tokens
+// and heads other than 64 and 128 (the 64 sequences in pages of 16: 139 us with the join)
+// take their addresses lane by lane, with two tiles and 45 to 87 spilled.  Tried and slower at 131072 tokens: three workgroups to a compute unit with
 // two buffers a wave (162 us instead of 141 with the join), two or four times as many
 // workgroups (141 and 158 instead of 131); with two tiles, one wave to a SIMD (107 instead
 // of 81) and scales read two at a time (95 instead of 79).

@@ -10,8 +10,8 @@
 // head's row and then the next token's, because a page holds one head's tokens
 // one after another: codes and scales of a page are touched in whole lines.
 // Bound by HBM: 2 bytes an element on one side, 0.53 to 0.75 on the other: 16381 tokens of
-// eight key heads of 128 (E2M1, E8M0 scales, 85 MB in and out) are written in 23.7 us and
-// read in 24.6, where the quantizer takes 22 for as many rows without pages.  A lane with one item
+// eight key heads of 128 (E2M1, E8M0 scales, 85 MB in and out) are written in 24 to 25 us and
+// read in 25, where the quantizer takes 22 for as many rows without pages.  A lane with one item
 // of many rows waits for four loads in a row; a row's items one after another hide
 // them.  (Lanes that take a token's heads in turn instead of its elements: 31 us.)
 #pragma once
