@@ -494,7 +494,7 @@ size_t ufp4_moe_tokens_workspace_bytes(int64_t T, int32_t E, int32_t top_k, int6
  * is -inf has weight 0; a row whose scores are all -inf has o = NaN and lse =
  * -inf.
  * Errors: UFP4_ERR_INVALID_ARG (negative sizes, null pointers, pitches,
- * alignment, a scale that is not finite, heads not a multiple of kv_heads),
+ * alignment, a scale that is not finite times log2(e), heads not a multiple of kv_heads),
  * UFP4_ERR_SHAPE (D % 8), UFP4_ERR_UNSUPPORTED (D > 128, T > 2^30, B > 2^20,
  * heads > 1024, a pitch > 2^22).  T = 0 or B = 0 is a no-op. */
 int ufp4_attn_fwd(const void* q, int64_t ldq, const void* k, int64_t ldk, const void* v,
@@ -560,7 +560,7 @@ typedef struct ufp4_kv_cache {
  * .. pages - 1 -- is not written, reads as zeros, and is not attended to.
  * Sequences may share pages that no call writes.
  * Errors of all three: UFP4_ERR_INVALID_ARG (negative sizes, null pointers,
- * pitches, alignment, page_tokens, heads), UFP4_ERR_SHAPE (D),
+ * pitches, alignment, page_tokens, heads, a scale as in ufp4_attn_fwd), UFP4_ERR_SHAPE (D),
  * UFP4_ERR_UNSUPPORTED (what cfg does not allow here, T > 2^30, B > 2^20,
  * width or a pitch > 2^22, kv_heads or heads > 1024), UFP4_ERR_INVALID_ARG or
  * as ufp4_rht_quant for cfg.  T = 0 or B = 0 is a no-op. */

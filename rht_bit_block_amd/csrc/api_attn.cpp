@@ -14,6 +14,9 @@ namespace {
 bool aligned(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 int hip_status(hipError_t e) { return e == hipSuccess ? UFP4_OK : UFP4_ERR_HIP; }
 
+// The kernels compute powers of 2: a factor of the scores has to be finite times log2(e) as well.
+bool factor_ok(float scale) { return std::isfinite(scale * 1.4426950408889634f); }
+
 // Sizes of packed rows with heads.
 int packed_sizes(int64_t T, int64_t B, int64_t heads, int64_t kv_heads, int64_t D) {
   if (T < 0 || B < 0 || heads < 1 || kv_heads < 1 || heads % kv_heads || D < 1)
@@ -36,7 +39,7 @@ int attn_inputs(const void* q, int64_t ldq, const void* k, int64_t ldk, const vo
   if ((st = rows_of(q, ldq, heads, D)) || (st = rows_of(k, ldk, kv_heads, D)) ||
       (st = rows_of(v, ldv, kv_heads, D)))
     return st;
-  if (!starts || !aligned(starts, 4) || !std::isfinite(scale)) return UFP4_ERR_INVALID_ARG;
+  if (!starts || !aligned(starts, 4) || !factor_ok(scale)) return UFP4_ERR_INVALID_ARG;
   return UFP4_OK;
 }
 
@@ -242,7 +245,7 @@ int ufp4_kv_attn(const void* q, int64_t ldq, const int32_t* starts, int32_t B, i
   if ((st = packed_sizes(T, B, heads, cache->kv_heads, cache->D))) return st;
   if (T == 0 || B == 0) return UFP4_OK;
   if ((st = rows_of(q, ldq, heads, cache->D)) || (st = rows_of(o, ldo, heads, cache->D))) return st;
-  if (!std::isfinite(scale) || !workspace || !aligned(workspace, 256) ||
+  if (!factor_ok(scale) || !workspace || !aligned(workspace, 256) ||
       workspace_bytes < ufp4_kv_attn_workspace_bytes(T, B, heads, cache->kv_heads, cache->D))
     return UFP4_ERR_INVALID_ARG;
   KvAttn p;
