@@ -119,7 +119,7 @@ __device__ __forceinline__ float query_sum(float x) {
 // Eight codes as bf16 values, in the order of `order`: levels times 2^e of `scale`.  SPLIT: the codes of
 // two 1 x 16 blocks, nibbles 0 .. 3 of the first in registers 0, 1, nibbles 4 .. 7 of the
 // second in 2, 3.  (INT4 as 136 + n, n ^ 8 in the low mantissa bits of 128, is two
-// instructions for two codes where tables and a conversion take four, and 6 to 9 % faster with one
+// instructions for two codes where tables and a conversion take four, and 5 to 10 % faster with one
 // tile of queries; but taking 136 times the sum of the other operand off again leaves the
 // rounding of that sum, however small the codes are.)
 template <int GRID, bool SPLIT>
